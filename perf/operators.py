@@ -135,6 +135,11 @@ def work(case):
 
 
 # ---------------------------------------------------------------------------- the inputs
+def _power_of_two(k):
+    """2^k, exactly (the device's exp2 and pow may be off by an ulp)."""
+    return ((k.long() + 1023) << 52).view(torch.float64)
+
+
 def _quantise(x, fmt):
     """Codes and scales of rows x[..., D]: float64, so that quotients next to a border fall on
     the right side of it."""
@@ -144,11 +149,11 @@ def _quantise(x, fmt):
         # the scale is a float32: the quotient by it is what is rounded
         s = (top / 127.0).float().double().clamp_min(SCALE_MIN)
         return torch.round(x / s).to(torch.int8), s.squeeze(-1).float()
-    # the least power of two that brings the row's largest magnitude to 448 or less
+    # the least power of two that brings the row's largest magnitude to 448 or less, 2^-100 at
+    # least
     m, e = torch.frexp(top)            # top = m 2^e, m in [0.5, 1)
     k = e - 9 + (m > 0.875).to(e.dtype)
-    s = torch.ldexp(torch.ones_like(top), k).clamp_min(SCALE_MIN)
-    s = torch.where(top > 0, s, torch.full_like(s, SCALE_MIN))
+    s = torch.where(top > 0, _power_of_two(k), 0.0).clamp_min(SCALE_MIN)
     return (x / s).float().to(torch.float8_e4m3fn), s.squeeze(-1).float()
 
 
@@ -312,13 +317,14 @@ def _exact_codes(x, fmt):
         s = torch.maximum((top / 127).to(torch.float32).to(torch.float64),
                           torch.tensor(SCALE_MIN, dtype=torch.float64, device=x.device))
         return torch.round(x / s[..., None]), s
-    k = torch.ceil(torch.log2(torch.where(top > 0, top, torch.ones_like(top)) / 448.0))
-    s = torch.maximum(torch.where(top > 0, torch.exp2(k), torch.zeros_like(top)),
-                      torch.tensor(SCALE_MIN, dtype=torch.float64, device=x.device))
+    # the powers of two that are candidates, as a table: the first with amax / s <= 448
+    table = torch.tensor([2.0 ** e for e in range(-100, 122)], dtype=torch.float64,
+                         device=x.device)
+    s = table[torch.searchsorted(table, top / 448.0)]
     y = x / s[..., None]
     # e4m3: three fraction bits, least exponent -6; round half to even on that grid
-    e = torch.floor(torch.log2(torch.clamp(y.abs(), min=2.0 ** -6)))
-    step = torch.exp2(e - 3)
+    steps = torch.tensor([2.0 ** e for e in range(-6, 10)], dtype=torch.float64, device=x.device)
+    step = steps[torch.searchsorted(steps, y.abs(), right=True).clamp_(min=1) - 1] / 8.0
     return torch.round(y / step) * step, s
 
 
