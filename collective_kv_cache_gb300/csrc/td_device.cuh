@@ -141,10 +141,10 @@ __device__ __forceinline__ void pdl_trigger() {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 template <typename... P, typename... A>
-inline cudaError_t launch_after(void (*kernel)(P...), unsigned grid, int threads, size_t smem,
+inline cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, size_t smem,
                                 cudaStream_t st, A... args) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(grid);
+  cfg.gridDim = grid;
   cfg.blockDim = dim3(static_cast<unsigned>(threads));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;

@@ -8,80 +8,11 @@
 #include <new>
 #include <vector>
 
-#include "td.h"
-#include "td_internal.h"
+#include "td_ctx.h"
 
 using namespace td;
 
-struct td_ctx {
-  td_shape shape;
-  Geom g;
-  int max_agents, max_blocks, max_shared, max_nb, nbw_max;
-  int device;
-
-  // round tables (device) and their pinned staging
-  int32_t* d_off = nullptr;
-  float* d_cos = nullptr;
-  float* d_sin = nullptr;
-  int32_t* d_tok_block = nullptr;
-  int32_t* d_blk_start = nullptr;
-  unsigned char* h_stage = nullptr;
-  size_t stage_bytes = 0;
-  cudaEvent_t stage_done = nullptr;
-  bool stage_pending = false;
-
-  // Streams that have read the round tables since their last upload, each with an event
-  // recorded after its latest launch. A round change makes the uploading stream wait on
-  // all of them; a stream's first call after an upload waits on tables_ready.
-  struct StreamUse {
-    cudaStream_t stream;
-    cudaEvent_t last_use;
-    bool ordered;      // ordered after the current tables' upload
-  };
-  std::vector<StreamUse> users;
-  cudaEvent_t tables_ready = nullptr;
-  cudaStream_t tables_stream = nullptr;
-  bool tables_recorded = false;
-
-  // cached round (host copy) and its device view
-  bool have_round = false;
-  int N = 0, M = 0, S = 0;
-  std::vector<int32_t> c_len, c_hist, c_perm;
-
-  // scratch
-  float* d_dev = nullptr;           // [max_agents * max_shared]
-  int32_t* d_pos = nullptr;         // [max_agents * max_shared] prompt position of each token
-  uint32_t* d_sel_hist = nullptr;   // [max_agents * kSelHistBins] selection histograms (zero)
-  float* d_gdev = nullptr;          // [max_shared] group deviation (variant)
-  double* d_score = nullptr;        // [max_agents] deviation totals (variant)
-  uint32_t* d_selbits = nullptr;    // [max_agents * max_nb]
-  int32_t* d_firstrank = nullptr;   // [max_agents * max_nb]
-  uint32_t* d_mask = nullptr;       // [max_agents * nbw_max]
-  uint32_t* d_cand = nullptr;       // [max_agents * nbw_max]
-  uint32_t* d_pm_mask = nullptr;    // [max_agents * nbw_max] masks of td_pick_master
-  int32_t* d_wprefix = nullptr;     // [max_agents * nbw_max + max_agents]
-  int64_t* d_aprefix = nullptr;     // [max_agents + 1]
-  uint32_t* d_flag = nullptr;       // [max_agents * L * max_nb] flags + [max_agents * L] counts
-  int sm_count = 0;                 // of the context's device
-  int32_t* d_ints = nullptr;        // encode's words (unused, m_ok, over, prep_done), spare,
-                                    // pick_master's counter, spare
-  int64_t* d_bound = nullptr;
-  uint32_t* d_err = nullptr;
-  float* d_attn = nullptr;          // attention partials, grown on demand
-  size_t attn_cap = 0;              // its size in floats
-  uint32_t attn_tx_pad = 0;         // fault injection: bytes the attention never receives
-  // pinned host words for results
-  int64_t* h_words = nullptr;       // [4]
-};
-
 namespace {
-
-bool is_pow2(int x) { return x > 0 && (x & (x - 1)) == 0; }
-int log2i(int x) {
-  int s = 0;
-  while ((1 << s) < x) ++s;
-  return s;
-}
 
 void free_ctx(td_ctx* c) {
   if (!c) return;
@@ -107,26 +38,14 @@ void free_ctx(td_ctx* c) {
   cudaFree(c->d_bound);
   cudaFree(c->d_err);
   cudaFree(c->d_attn);
+  cudaFree(c->d_chunk);
+  for (float* p : c->old_chunk) cudaFree(p);
   if (c->h_stage) cudaFreeHost(c->h_stage);
   if (c->h_words) cudaFreeHost(c->h_words);
   if (c->stage_done) cudaEventDestroy(c->stage_done);
   if (c->tables_ready) cudaEventDestroy(c->tables_ready);
   for (auto& u : c->users) cudaEventDestroy(u.last_use);
   delete c;
-}
-
-bool same_device(const td_ctx* c) {
-  int d = -1;
-  return cudaGetDevice(&d) == cudaSuccess && d == c->device;
-}
-
-bool capturing(cudaStream_t st) {
-  cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(st, &cs) != cudaSuccess) {
-    cudaGetLastError();
-    return false;
-  }
-  return cs != cudaStreamCaptureStatusNone;
 }
 
 td_ctx::StreamUse* find_use(td_ctx* c, cudaStream_t st) {
@@ -322,27 +241,6 @@ td_status pool_dev(const td_ctx* c, const td_round* r, const td_paged* p, PoolDe
   out->P = P;
   out->p_shift = is_pow2(P) ? log2i(P) : -1;
   return TD_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-// cuTensorMapEncodeTiled from the driver, looked up once (no link-time dependency).
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_tiled() {
-  static EncodeTiledFn fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                         &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiledFn>(nullptr);
-    return reinterpret_cast<EncodeTiledFn>(p);
-  }();
-  return fn;
 }
 
 // A [rows][E] bf16 array as a 2-D tensor map with 16 x 64 boxes and 128-byte swizzle.

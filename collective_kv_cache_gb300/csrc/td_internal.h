@@ -189,4 +189,79 @@ cudaError_t launch_materialise(const Geom& g, const RoundDev& rd, const StoreDev
                                int agent, int sl0, int nl, uint16_t* dk, uint16_t* dv,
                                uint32_t* err, cudaStream_t st);
 
+// ---- chunks of new tokens over paged caches (k_quant.cu, k_chunk.cu) -----------------
+constexpr int kMaxChunkSeqs = 256;  // sequences per launch (passed by value)
+
+// The sequences of one launch. Token t of the launch belongs to the sequence x with
+// row[x] <= t < row[x + 1], at position start[x] + t - row[x] of agent[x].
+struct ChunkList {
+  int n;
+  int32_t agent[kMaxChunkSeqs];
+  int32_t start[kMaxChunkSeqs];
+  int32_t row[kMaxChunkSeqs + 1];     // exclusive prefix of the sequences' tokens
+};
+
+// How the attention's work is cut: sequence x has units base[x] .. base[x + 1] - 1 for each
+// (layer, kv head), nsplit[x] of them (parts of its visible positions) per tile of query rows.
+struct ChunkUnits {
+  int32_t base[kMaxChunkSeqs + 1];
+  int32_t nsplit[kMaxChunkSeqs];
+};
+
+// What the cache's pages hold: bf16 rows, or 8-bit codes with a float scale per head row.
+enum CacheKind { kCacheBf16 = 0, kCacheInt8 = 1, kCacheE4m3 = 2 };
+
+// 8-bit pages: codes [L][2][num_pages][P][H][D], scale [L][2][num_pages][P][H]. The page
+// geometry is PoolDev's (its base points at the codes).
+struct Cache8Dev {
+  PoolDev pool;
+  float* scale;
+};
+
+struct QuantArgs {
+  Geom g;
+  Cache8Dev cache;
+  uint16_t* k;               // bf16 rows [nl][tokens][E]: read by the write, written by the read
+  uint16_t* v;
+  int64_t tokens;            // tokens of the whole call
+  int64_t tok0;              // this launch's first
+  int nl, layer_begin;
+  int lane_shift;            // lanes per head row = 1 << lane_shift (>= D / 8, at most 32)
+  int head_mul;              // ceil(2^20 / H): row / H without a division
+  int per_cta;               // tokens per CTA, at most kQuantTokens
+  uint32_t* err;
+};
+constexpr int kQuantTokens = 32;
+
+cudaError_t launch_quantise(const QuantArgs& a, const ChunkList& list, CacheKind kind,
+                            cudaStream_t st);
+cudaError_t launch_dequantise(const QuantArgs& a, const ChunkList& list, CacheKind kind,
+                              cudaStream_t st);
+
+struct ChunkArgs {
+  Geom g;
+  PoolDev pool;              // the pages (bf16 rows, or 8-bit codes)
+  const float* scale;        // 8-bit pages: their scales
+  const uint16_t* q;         // [nl][tokens][nq][D] bf16
+  uint16_t* out;             // [nl][tokens][nq][D] bf16
+  float* lse;                // [nl][tokens][nq] or nullptr
+  float* part_o;             // [units][rows per tile][D] unnormalised outputs
+  float* part_ml;            // [units][rows per tile][2]: max, sum (base 2)
+  int64_t tokens, tok0;      // tokens of the whole call; this launch's first
+  int nq, G;                 // query heads, query heads per kv head
+  int nl, layer_begin;
+  int window, n_sink;        // 0: every earlier position is seen
+  int span;                  // visible positions per unit (a multiple of 16)
+  int direct;                // 1: one unit per tile everywhere, outputs written at once
+  float scale_log2;          // softmax scale * log2(e)
+  uint32_t* err;
+};
+
+// Query rows (token, head of the group) per tile of the streaming kernel: 8 or 16.
+cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                              CacheKind kind, int rows_per_tile, cudaStream_t st);
+// Joins the units of every query row.
+cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                              int rows_per_tile, cudaStream_t st);
+
 }  // namespace td

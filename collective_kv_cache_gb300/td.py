@@ -51,6 +51,20 @@ class td_diff_store(C.Structure):
                 ("layer_begin", C.c_int32), ("layer_end", C.c_int32)]
 
 
+class td_chunks(C.Structure):
+    _fields_ = [("n", C.c_int32), ("agent", C.POINTER(C.c_int32)),
+                ("start", C.POINTER(C.c_int32)), ("len", C.POINTER(C.c_int32))]
+
+
+TD_KV_INT8, TD_KV_E4M3 = 0, 1
+
+
+class td_paged8(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scale", C.c_void_p), ("num_pages", C.c_int64),
+                ("block_table", C.c_void_p), ("max_pages_per_agent", C.c_int32),
+                ("format", C.c_int32)]
+
+
 class td_prompt(C.Structure):
     _fields_ = [("tokens", C.c_void_p), ("n_tokens", C.c_int64), ("pages", C.c_void_p)]
 
@@ -93,6 +107,12 @@ def _load() -> C.CDLL:
                                VP, I32, C.c_float, VP, VP, VP],
         "td_paged_attention": [VP, P(td_round), P(td_paged), VP, I32, I32, I32, VP, I32,
                                C.c_float, VP, VP, VP],
+        "td_quantise_append": [VP, P(td_chunks), P(td_paged8), VP, VP, I32, I32, VP],
+        "td_dequantise_read": [VP, P(td_chunks), P(td_paged8), I32, I32, VP, VP, VP],
+        "td_chunk_attention": [VP, P(td_chunks), P(td_paged), I32, I32, VP, I32, C.c_float, I32,
+                               I32, VP, VP, VP],
+        "td_chunk_attention_q8": [VP, P(td_chunks), P(td_paged8), I32, I32, VP, I32, C.c_float,
+                                  I32, I32, VP, VP, VP],
         "td_inject_attention_wait_fault": [VP, C.c_uint32],
         "td_form_rounds": [P(td_prompt), I32, I32, I32, VP, I32, VP, VP, P(I32)],
         "td_group_round": [P(td_prompt), I32, I32, VP, I32, I32, I32, VP, P(I32), VP, P(I32),
@@ -115,7 +135,9 @@ EXPORTS = ("td_ctx_create", "td_ctx_destroy", "td_status_string", "td_round_offs
            "td_fused_restore", "td_get_error", "td_check_select_noalloc",
            "td_check_select_group", "td_pick_master_min_deviation", "td_segment_hash",
            "td_form_rounds", "td_group_round", "td_materialise_mirror",
-           "td_fused_attention", "td_paged_attention", "td_inject_attention_wait_fault")
+           "td_fused_attention", "td_paged_attention", "td_quantise_append",
+           "td_dequantise_read", "td_chunk_attention", "td_chunk_attention_q8",
+           "td_inject_attention_wait_fault")
 
 
 def lib_path() -> str:
@@ -241,6 +263,36 @@ def td_paged_attention(ctx, rnd, pool, agents, layer_begin, layer_end, q, n_q_he
     return _check(s, "td_paged_attention") if check else s
 
 
+def td_quantise_append(ctx, chunks: td_chunks, cache: td_paged8, k_new, v_new, layer_begin,
+                       layer_end, stream=0, check=True) -> int:
+    s = _lib.td_quantise_append(ctx, C.byref(chunks), C.byref(cache), k_new, v_new, layer_begin,
+                                layer_end, stream)
+    return _check(s, "td_quantise_append") if check else s
+
+
+def td_dequantise_read(ctx, chunks: td_chunks, cache: td_paged8, layer_begin, layer_end, k_out,
+                       v_out, stream=0, check=True) -> int:
+    s = _lib.td_dequantise_read(ctx, C.byref(chunks), C.byref(cache), layer_begin, layer_end,
+                                k_out, v_out, stream)
+    return _check(s, "td_dequantise_read") if check else s
+
+
+def td_chunk_attention(ctx, chunks: td_chunks, pool: td_paged, layer_begin, layer_end, q,
+                       n_q_heads, scale, window, n_sink, out, lse=None, stream=0,
+                       check=True) -> int:
+    s = _lib.td_chunk_attention(ctx, C.byref(chunks), C.byref(pool), layer_begin, layer_end, q,
+                                n_q_heads, scale, window, n_sink, out, lse, stream)
+    return _check(s, "td_chunk_attention") if check else s
+
+
+def td_chunk_attention_q8(ctx, chunks: td_chunks, cache: td_paged8, layer_begin, layer_end, q,
+                          n_q_heads, scale, window, n_sink, out, lse=None, stream=0,
+                          check=True) -> int:
+    s = _lib.td_chunk_attention_q8(ctx, C.byref(chunks), C.byref(cache), layer_begin, layer_end,
+                                   q, n_q_heads, scale, window, n_sink, out, lse, stream)
+    return _check(s, "td_chunk_attention_q8") if check else s
+
+
 def td_inject_attention_wait_fault(ctx, nbytes: int) -> int:
     return _check(_lib.td_inject_attention_wait_fault(ctx, nbytes),
                   "td_inject_attention_wait_fault")
@@ -346,6 +398,28 @@ def make_paged(pool_tensor, block_table_tensor) -> td_paged:
     p = td_paged(pool_tensor.data_ptr(), pool_tensor.shape[2], block_table_tensor.data_ptr(),
                  block_table_tensor.shape[1])
     p._keep = (pool_tensor, block_table_tensor)
+    return p
+
+
+def make_chunks(agents, starts, lens) -> td_chunks:
+    """A batch of chunks: agents[x] gets lens[x] tokens from position starts[x] on."""
+    cols = [np.ascontiguousarray(np.asarray(a, dtype=np.int32)).reshape(-1)
+            for a in (agents, starts, lens)]
+    if not len(cols[0]) == len(cols[1]) == len(cols[2]):
+        raise ValueError("agents, starts and lens differ in length")
+    c = td_chunks(len(cols[0]), *(a.ctypes.data_as(C.POINTER(C.c_int32)) for a in cols))
+    c._keep = cols
+    return c
+
+
+def make_paged8(codes_tensor, scale_tensor, block_table_tensor, fmt) -> td_paged8:
+    """codes_tensor: torch, one byte an element, [L][2][num_pages][P][H][D] on the GPU;
+    scale_tensor: torch float32 [L][2][num_pages][P][H]; fmt: "int8" or "e4m3" (or a
+    TD_KV_ value)."""
+    p = td_paged8(codes_tensor.data_ptr(), scale_tensor.data_ptr(), codes_tensor.shape[2],
+                  block_table_tensor.data_ptr(), block_table_tensor.shape[1],
+                  {"int8": TD_KV_INT8, "e4m3": TD_KV_E4M3}.get(fmt, fmt))
+    p._keep = (codes_tensor, scale_tensor, block_table_tensor)
     return p
 
 

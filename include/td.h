@@ -38,7 +38,10 @@
  *           master     td_pick_master, td_pick_master_min_deviation
  *           encode     td_diff_encode
  *           attention  td_fused_attention, td_paged_attention
- *         td_rerotate_batched, td_fused_restore and td_materialise_mirror use no scratch.
+ *           chunks     td_chunk_attention, td_chunk_attention_q8 (replays of graphs that
+ *                      captured them included)
+ *         td_rerotate_batched, td_fused_restore, td_materialise_mirror, td_quantise_append
+ *         and td_dequantise_read use no scratch.
  *       Calls of different groups may overlap: for example td_check_select and
  *       td_pick_master on one stream while td_rerotate_batched of other layers runs on
  *       another. Data the caller passes (pool, store, selection) is the caller's to order.
@@ -66,7 +69,7 @@ typedef enum td_status {
   TD_ERR_CUDA = 2,           /* a CUDA runtime call failed */
   TD_ERR_CAPACITY = 3,       /* diff store too small (see td_diff_encode) */
   TD_ERR_UNMAPPED_PAGE = 4,  /* a block-table entry was -1 or >= num_pages */
-  TD_ERR_NONFINITE = 5,      /* a key deviation was NaN or infinite */
+  TD_ERR_NONFINITE = 5,      /* a key deviation, or a row to quantise, was NaN or infinite */
   TD_ERR_DEVICE_TIMEOUT = 6, /* a kernel's bounded wait on its own copies ran out */
   TD_ERR_SCRATCH_LIMIT = 7   /* sizes exceed the fixed scratch of td_check_select_noalloc */
 } td_status;
@@ -342,6 +345,105 @@ td_status td_paged_attention(td_ctx* ctx, const td_round* round, const td_paged*
 td_status td_materialise_mirror(td_ctx* ctx, const td_round* round, const td_diff_store* store,
                                 int32_t agent, int32_t layer_begin, int32_t layer_end,
                                 void* dense_k, void* dense_v, void* stream);
+
+/* ---- Chunks of new tokens over paged caches -----------------------------------------
+ * The model side of a round: the recompute of the important positions ([R] §2a
+ * "Per-request selective recompute") and the agents' own outputs are chunks of new tokens
+ * per agent, whose K/V goes into the agent's pages and whose queries attend to them. No
+ * round is needed: a batch of chunks says which agents, positions and lengths.
+ *   n       chunks in the batch, >= 0
+ *   agent   HOST [n] row of the block table, in [0, max_agents) of the context; the table
+ *           must have the rows that are named
+ *   start   HOST [n] position of the chunk's first token, >= 0
+ *   len     HOST [n] tokens, >= 0; start + len <= max_pages_per_agent * page_size
+ * Dense arrays of a batch hold the chunks' tokens one after the other in batch order: T =
+ * the sum of len rows per layer. A batch without tokens is valid: nothing is launched and
+ * nothing written. An agent may be listed several times (td_quantise_append refuses chunks
+ * of one agent that overlap). The arrays are read during the call only: a captured call
+ * keeps its batch. */
+typedef struct td_chunks {
+  int32_t n;
+  const int32_t* agent;
+  const int32_t* start;
+  const int32_t* len;
+} td_chunks;
+
+typedef enum td_kv_format {
+  TD_KV_INT8 = 0,   /* signed 8-bit codes in [-127, 127] */
+  TD_KV_E4M3 = 1    /* 8-bit floats: 4 exponent and 3 fraction bits, no infinities */
+} td_kv_format;
+
+/* Paged KV cache in 8 bits, laid out as td_paged with one scale per position and kv head:
+ * the value of an element is code * scale.
+ *   codes   DEVICE [L][2][num_pages][page_size][H][D] bytes (index 0 = K, 1 = V), 16-byte
+ *           aligned
+ *   scale   DEVICE float [L][2][num_pages][page_size][H]
+ * num_pages * page_size <= 2^31 - 1 (td_paged as well in the calls below). */
+typedef struct td_paged8 {
+  void* codes;
+  float* scale;
+  int64_t num_pages;
+  const int32_t* block_table;
+  int32_t max_pages_per_agent;
+  int32_t format;            /* td_kv_format */
+} td_paged8;
+
+/* Quantise the K and V of new tokens as they are written into 8-bit pages. For every layer
+ * of [layer_begin, layer_end), token and kv head, with x the D elements of the row and
+ * amax their largest magnitude:
+ *   TD_KV_INT8   scale = max(fl32(amax / 127), 2^-100)
+ *   TD_KV_E4M3   scale = max(2^ceil(log2(amax / 448)), 2^-100)   (a power of two)
+ * and each code is the value of the format nearest to the exact quotient x / scale, ties to
+ * even. A row that holds a NaN or an infinity gets the scale NaN and codes 0 (it reads back
+ * as NaN) and sets TD_ERR_NONFINITE in the error word. Nothing but the listed positions is
+ * written. Chunks of one agent must not overlap, and a position's page must not be mapped
+ * by two of the listed agents at positions of this call (that is not checked: the later
+ * write would depend on timing). An unmapped page sets TD_ERR_UNMAPPED_PAGE; its tokens are
+ * not written.
+ *   k_new, v_new   DEVICE bf16 [layer_end-layer_begin][T][E], 16-byte aligned
+ * Head dims up to 256. */
+td_status td_quantise_append(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
+                             const void* k_new, const void* v_new, int32_t layer_begin,
+                             int32_t layer_end, void* stream);
+
+/* Read positions of 8-bit pages back as dense bf16 rows: bf16(fl32(code * scale)), rounded
+ * to nearest even. Rows of an unmapped page are zeros and set TD_ERR_UNMAPPED_PAGE.
+ *   k_out, v_out   DEVICE bf16 [layer_end-layer_begin][T][E], 16-byte aligned
+ * Head dims up to 256. */
+td_status td_dequantise_read(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
+                             int32_t layer_begin, int32_t layer_end, void* k_out, void* v_out,
+                             void* stream);
+
+/* Attention of chunks of new tokens over the agents' pages, the new tokens' own K/V
+ * included (write them first). The token at position t of its agent sees the positions
+ * p <= t; with window > 0 only those with p > t - window or p < n_sink (the first tokens
+ * stay visible). window = 0: no window, n_sink is not read. For every layer, token and
+ * query head g, over the visible positions:
+ *   out = sum_p softmax_p(scale * q . K_p) V_p,   lse = ln sum_p exp(scale * q . K_p)
+ * Query head g reads kv head g / (n_q_heads / H), K and V as the pages hold them.
+ * Positions that no token of the chunk sees are not read: their pages may be unmapped.
+ * Positions that a token does not see have no part in its row, whatever they hold. An
+ * unmapped page within sight sets TD_ERR_UNMAPPED_PAGE and its positions are left out; a row
+ * left with none is zeros with lse = -infinity. A NaN that a token sees makes its row NaN.
+ * Scores, softmax and sums are float32.
+ *   q     DEVICE bf16 [layer_end-layer_begin][T][n_q_heads][D], rotated, 16-byte aligned
+ *   out   DEVICE bf16, as q
+ *   lse   DEVICE float [layer_end-layer_begin][T][n_q_heads], or NULL
+ * n_q_heads a multiple of H, T * n_q_heads < 2^31; head dims 64 and 128 (else
+ * TD_ERR_INVALID_ARG).
+ * The context owns the partial results' scratch, which grows with the calls: a call made in a
+ * stream capture must find it large enough (make the call once before capturing it; else
+ * TD_ERR_INVALID_ARG). */
+td_status td_chunk_attention(td_ctx* ctx, const td_chunks* chunks, const td_paged* pool,
+                             int32_t layer_begin, int32_t layer_end, const void* q,
+                             int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
+                             void* out, float* lse, void* stream);
+
+/* The same over 8-bit pages: K and V are code * scale. */
+td_status td_chunk_attention_q8(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
+                                int32_t layer_begin, int32_t layer_end, const void* q,
+                                int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
+                                void* out, float* lse, void* stream);
 
 /* ---- Round-aware prompts and the KV Collector (host only) --------------------------
  * [R] Summary Method (1): the application puts a reserved separator token ([B] §4.1:

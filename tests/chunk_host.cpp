@@ -1,0 +1,126 @@
+// chunk_host.cpp - the chunk entry points (td_chunks.cpp) on a host without a GPU: the CUDA
+// runtime calls and the kernel launches are stand-ins that record what they were given, so
+// that refusals and launch plans can be tested by tests/test_chunks_host.py.
+#include <cstdlib>
+#include <vector>
+
+#include "td_ctx.h"
+
+using namespace td;
+
+namespace {
+struct Launch {
+  int what;           // 0 quantise, 1 dequantise, 2 streaming attention, 3 join
+  int kind, rows;
+  ChunkArgs a;
+  QuantArgs qa;
+  ChunkList list;
+  ChunkUnits units;
+};
+std::vector<Launch> g_launches;
+int g_device = 0, g_capturing = 0, g_fail_malloc = 0;
+size_t g_floats = 0;
+
+Launch& push(int what, const ChunkList& list) {
+  g_launches.emplace_back();
+  Launch& l = g_launches.back();
+  l.what = what;
+  l.list = list;
+  return l;
+}
+}  // namespace
+
+namespace td {
+cudaError_t launch_quantise(const QuantArgs& a, const ChunkList& list, CacheKind kind, cudaStream_t) {
+  Launch& l = push(0, list);
+  l.qa = a;
+  l.kind = kind;
+  return cudaSuccess;
+}
+cudaError_t launch_dequantise(const QuantArgs& a, const ChunkList& list, CacheKind kind, cudaStream_t) {
+  Launch& l = push(1, list);
+  l.qa = a;
+  l.kind = kind;
+  return cudaSuccess;
+}
+cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                              CacheKind kind, int rows, cudaStream_t) {
+  Launch& l = push(2, list);
+  l.a = a;
+  l.units = units;
+  l.kind = kind;
+  l.rows = rows;
+  return cudaSuccess;
+}
+cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                              int rows, cudaStream_t) {
+  Launch& l = push(3, list);
+  l.a = a;
+  l.units = units;
+  l.rows = rows;
+  return cudaSuccess;
+}
+}  // namespace td
+
+extern "C" {
+
+cudaError_t cudaGetDevice(int* d) {
+  *d = g_device;
+  return cudaSuccess;
+}
+cudaError_t cudaMalloc(void** p, size_t bytes) {
+  if (g_fail_malloc) return cudaErrorMemoryAllocation;
+  g_floats = bytes / sizeof(float);
+  static char place[64];
+  *p = place;
+  return cudaSuccess;
+}
+cudaError_t cudaGetLastError(void) { return cudaSuccess; }
+cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) {
+  *s = g_capturing ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone;
+  return cudaSuccess;
+}
+
+td_ctx* fake_ctx(const td_shape* s, int max_agents, int sms) {
+  td_ctx* c = new td_ctx;
+  c->shape = *s;
+  c->g.H = s->n_kv_heads;
+  c->g.D = s->head_dim;
+  c->g.E = s->n_kv_heads * s->head_dim;
+  c->g.half = s->head_dim / 2;
+  c->max_agents = max_agents;
+  c->device = 0;
+  c->sm_count = sms;
+  return c;
+}
+void fake_state(int device, int capturing, int fail_malloc) {
+  g_device = device;
+  g_capturing = capturing;
+  g_fail_malloc = fail_malloc;
+}
+void fake_reset(void) { g_launches.clear(); }
+int64_t fake_floats(void) { return static_cast<int64_t>(g_floats); }
+int fake_launches(void) { return static_cast<int>(g_launches.size()); }
+// what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul
+void fake_launch(int i, int64_t* out) {
+  const Launch& l = g_launches[i];
+  const bool quant = l.what < 2;
+  const int64_t v[] = {l.what, l.kind, l.rows, l.list.n, l.a.direct, l.a.span,
+                       quant ? l.qa.tok0 : l.a.tok0, quant ? l.qa.tokens : l.a.tokens,
+                       l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul};
+  for (int k = 0; k < 11; ++k) out[k] = v[k];
+}
+void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* base, int32_t* ns) {
+  const Launch& l = g_launches[i];
+  for (int x = 0; x <= l.list.n; ++x) {
+    row[x] = l.list.row[x];
+    base[x] = l.units.base[x];
+    if (x < l.list.n) {
+      agent[x] = l.list.agent[x];
+      start[x] = l.list.start[x];
+      ns[x] = l.units.nsplit[x];
+    }
+  }
+}
+
+}  // extern "C"
