@@ -25,7 +25,7 @@
 // anything. A V row that some rows of the tile see and others do not may hold infinities or
 // NaNs of its own; they must not reach the others through 0 * NaN, so in steps that mask
 // anything such values leave the product and are added to the rows that see them alone.
-#include "td_device.cuh"
+#include "td_cache8.cuh"
 
 namespace td {
 
@@ -49,37 +49,6 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
-}
-
-__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
-  uint32_t y;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
-  return y;
-}
-
-// Two codes, in the high bytes of the halves (kCacheE4m3) or in the low bytes (kCacheInt8),
-// as two bf16 of exactly their values.
-template <int kKind>
-__device__ __forceinline__ uint32_t codes_bf16(uint32_t u) {
-  if constexpr (kKind == kCacheE4m3) {
-    // exponent and fraction moved to bf16's places: 2^120 too small (bias 7 against 127)
-    return hmul2_bf16((u & 0x80008000u) | ((u >> 4) & 0x07F007F0u), 0x7B807B80u);
-  } else {
-    // 128 + (low 7 bits) minus 128, or 256 for a negative code: all exact in 8 bits
-    uint32_t y;
-    asm("sub.rn.bf16x2 %0, %1, %2;"
-        : "=r"(y)
-        : "r"((u & 0x007F007Fu) | 0x43004300u), "r"((u & 0x00800080u) | 0x43004300u));
-    return y;
-  }
-}
-
-// Pair (byte i of a, byte i of b) for codes_bf16.
-template <int kKind>
-__device__ __forceinline__ uint32_t pair_bytes(uint32_t a, uint32_t b, int i) {
-  // e4m3 wants the bytes in the high halves (the low ones are masked out), int8 in the low
-  return kKind == kCacheE4m3 ? __byte_perm(a, b, ((4 + i) << 12) | (i << 4))
-                             : __byte_perm(a, b, ((4 + i) << 8) | i);
 }
 
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
@@ -151,7 +120,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     const int r = r0 + nb * 8 + gid;
     const bool live = r < rows;
     const int tok = live ? r / A.G : 0;
-    const int64_t row = static_cast<int64_t>(li) * A.tokens + A.tok0 + list.row[x] + tok;
+    const int64_t row = static_cast<int64_t>(li) * A.tokens + list.tok[x] + tok;
     const uint16_t* q = A.q + (row * A.nq + h * A.G + (live ? r - tok * A.G : 0)) * D;
 #pragma unroll
     for (int kc = 0; kc < KCH; ++kc)
@@ -264,12 +233,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
         const int j = kc >> 2;
         const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kr[0][j])[kc & 3];
         const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kr[1][j])[kc & 3];
-        constexpr uint32_t lo_sel = kKind == kCacheE4m3 ? 0x1404u : 0x4140u;
-        constexpr uint32_t hi_sel = kKind == kCacheE4m3 ? 0x3424u : 0x4342u;
-        a[0] = codes_bf16<kKind>(__byte_perm(w0, 0u, lo_sel));
-        a[1] = codes_bf16<kKind>(__byte_perm(w1, 0u, lo_sel));
-        a[2] = codes_bf16<kKind>(__byte_perm(w0, 0u, hi_sel));
-        a[3] = codes_bf16<kKind>(__byte_perm(w1, 0u, hi_sel));
+        a[0] = word_bf16<kKind, false>(w0);
+        a[1] = word_bf16<kKind, false>(w1);
+        a[2] = word_bf16<kKind, true>(w0);
+        a[3] = word_bf16<kKind, true>(w1);
       } else {
         const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kr[0][kc >> 1]) + (kc & 1) * 2;
         const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kr[1][kc >> 1]) + (kc & 1) * 2;
@@ -404,10 +371,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       uint32_t a[4];
       if constexpr (Y::k8) {
         const int w = mt >> 1, i0 = (mt & 1) * 2;   // word and first byte of dims 2 mt, 2 mt + 1
-        a[0] = codes_bf16<kKind>(pair_bytes<kKind>(vr[0][0][w], vr[1][0][w], i0));
-        a[1] = codes_bf16<kKind>(pair_bytes<kKind>(vr[0][0][w], vr[1][0][w], i0 + 1));
-        a[2] = codes_bf16<kKind>(pair_bytes<kKind>(vr[2][0][w], vr[3][0][w], i0));
-        a[3] = codes_bf16<kKind>(pair_bytes<kKind>(vr[2][0][w], vr[3][0][w], i0 + 1));
+        a[0] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0);
+        a[1] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0 + 1);
+        a[2] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0);
+        a[3] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0 + 1);
       } else {
         const int j = mt / Y::vWords, w = mt % Y::vWords;
         a[0] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x5410);
@@ -441,7 +408,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       if (A.direct) {
         const int tok = r / A.G;
         const int64_t row =
-            (static_cast<int64_t>(li) * A.tokens + A.tok0 + list.row[x] + tok) * A.nq + h * A.G +
+            (static_cast<int64_t>(li) * A.tokens + list.tok[x] + tok) * A.nq + h * A.G +
             (r - tok * A.G);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;    // a row that sees nothing: zeros
 #pragma unroll
@@ -547,7 +514,8 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
   if (__any_sync(0xFFFFFFFFu, nan)) l = __uint_as_float(0x7FC00000u);
-  const int64_t row = (static_cast<int64_t>(li) * A.tokens + A.tok0 + t) * A.nq + gq;
+  const int64_t row =
+      (static_cast<int64_t>(li) * A.tokens + list.tok[x] + t - list.row[x]) * A.nq + gq;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D + lane * DPL);
 #pragma unroll

@@ -1,0 +1,902 @@
+// k_chunk_tc.cu - attention of a chunk of new tokens over a paged cache, for many query rows:
+// tcgen05 tensor cores, accumulators in TMEM, K and V tiles brought by TMA.
+//
+// The mathematics is k_chunk.cu's: token u of a chunk at pos = start + u sees p <= pos (and,
+// under a window, p > pos - W or p < n_sink); out = softmax(scale q K^T) V over what it sees.
+// The query rows of a kv head are the pairs (token, head of the group): a CTA takes up to 256
+// of them as two tiles of 128 and walks the KV tiles of 128 positions that any of them sees:
+//   S_w = Q_w K^T        (128 x 128, float32 in TMEM; operands in shared memory)
+//   P_w = 2^(S_w - m)    (bf16, written over S_w in TMEM)
+//   O_w += P_w V         (float32 in TMEM; A operand from TMEM, V as stored: dims-major)
+// Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that no statistic
+// crosses threads; one thread issues all products; the two tiles alternate, so that the tensor
+// core works on one while the other is in its softmax. Per KV tile and both query tiles the
+// products take 4 D 2^14 / 8192 = 1024 cycles (D = 128) and the 2 x 2^14 exponentials as many
+// (32 a cycle): the kernel is bound by both, and by the issue of the softmax.
+//
+// The running maximum is lazy: m is raised, and O rescaled (in TMEM, by the softmax warps),
+// only when a row's maximum grew by more than 2^8; until then weights may reach 2^8, which
+// float32 sums and bf16's relative precision do not mind. The weights are rounded to bf16 (2^-9
+// relative, random) for the tensor cores, like the output; their sum is taken before, in
+// float32.
+//
+// bf16 pages: a tile arrives as boxes of 8 to 128 rows x 64 dims, each inside one page
+// (tensor map, 128-byte swizzle), K on a ring of its own, V on another. Every V tile passes
+// two patch warps before the products read it: where a tile holds positions that some row
+// does not see, they clear the rows that none sees (their bytes may be anything) and watch for
+// infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
+// value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
+// 8-bit pages: four warps load codes, turn them into bf16 (exact) and store them as the same
+// tiles; the scale of K's row goes on the score's column, that of V's on the weight's.
+//
+// Every wait is bounded by the global timer; when one runs out TD_ERR_DEVICE_TIMEOUT is set
+// and all roles leave their loops, wait (bounded) for what they started and free the TMEM.
+#include "td_cache8.cuh"
+
+namespace td {
+
+namespace {
+
+constexpr int kKv = 128;              // positions per KV tile
+constexpr int kRows = 128;            // query rows per tile
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMmaWarp = 8;
+constexpr int kLoadWarp = 9;          // bf16: TMA; 8-bit: the first of four converting warps
+constexpr int kPatchWarp = 10;        // bf16: the first of two
+constexpr int kInfo = 8;              // KV tiles whose facts are kept
+
+template <int D, bool k8>
+struct Plan {
+  static constexpr int kTile = kKv * D * 2;              // bytes of a K or V tile
+  static constexpr int kQ = 2 * kRows * D * 2;
+  // K and V tiles in flight. One CTA an SM either way (TMEM is taken whole): D = 64 leaves
+  // room for more, and must take more than half of the shared memory
+  static constexpr int kK = D == 64 ? 4 : (k8 ? 2 : 3);
+  static constexpr int kV = D == 64 ? 4 : 2;
+  static constexpr int kThreads = k8 ? 416 : 384;
+  // 8-bit pages: the last KV tiles' scales, two tiles' page rows
+  static constexpr int kScales = k8 ? kInfo * 2 * kKv * 4 : 0;
+  static constexpr int kPageRows = k8 ? 2 * kKv * 4 : 0;
+  static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + 1024;
+};
+
+// Bit p of a KV tile's words: position p's page is mapped, or nobody needs it.
+struct __align__(16) Info {
+  uint32_t valid[4];
+  __device__ __forceinline__ uint4 load() const {
+    const volatile uint32_t* v = valid;
+    return make_uint4(v[0], v[1], v[2], v[3]);
+  }
+};
+__device__ __forceinline__ bool no_holes(const uint4& v) { return (v.x & v.y & v.z & v.w) == ~0u; }
+
+struct Shared {
+  uint64_t q_full, k_full[4], k_empty[4], v_raw[4], v_full[4], v_empty[4];
+  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint32_t tmem;
+  int abort, bad;
+  Info info[kInfo];
+};
+static_assert(sizeof(Shared) <= 1024, "the block's bookkeeping has 1 KB");
+
+// ---- PTX
+__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ void fence_async_smem() {
+  asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];"
+      ::"r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(bar))
+      : "memory");
+}
+
+__device__ __forceinline__ void tc_fence_before() {
+  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_fence_after() {
+  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               ::"r"(smem_u32(bar)) : "memory");
+}
+
+// D (TMEM) = A B (+ D): both operands in shared memory.
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+      ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+// The same with A in TMEM.
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                          bool add) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+      ::"r"(d), "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add))
+      : "memory");
+}
+
+// 32 columns of the warp's 32 lanes.
+__device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
+      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
+        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};"
+      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
+        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
+        "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+
+// Shared-memory operand of 64-element (128-byte) swizzled rows: `next` = bytes between
+// neighbouring 64-element column blocks (read for dims-major operands only), 1024 bytes
+// between groups of 8 rows.
+__device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t next) {
+  return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) |
+         (static_cast<uint64_t>(next >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+// Instruction descriptor: bf16 operands, float32 accumulators, 128 x n; b_dims: B is stored
+// with its n index contiguous.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_dims) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(b_dims) << 16) |
+         (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mov.b64 c, {%6, %7};\n\tfma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Waits for a phase, for at most kWaitLimitNs or until another role gave up.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, unsigned parity, Shared* sh,
+                                              uint32_t* err) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sh->abort)) return false;
+    if (global_ns() - t0 >= kWaitLimitNs) {
+      *reinterpret_cast<volatile int*>(&sh->abort) = 1;
+      atomicOr(err, err_bit(TD_ERR_DEVICE_TIMEOUT));
+      return false;
+    }
+  }
+}
+
+// Byte offset of 16-byte chunk c of row r in a tile (64-dim column blocks of 128 rows,
+// 128-byte swizzle).
+__device__ __forceinline__ uint32_t tile_at(int r, int c) {
+  return (c >> 3) * (128 * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+}
+
+// What a CTA works on.
+struct Work {
+  int x, h, li;                 // sequence, kv head, layer of the launch
+  int64_t unit;                 // number of its partial results
+  int r0, nrows;                // query rows r0 .. r0 + nrows - 1 of the sequence
+  int start, len;
+  int p_first, p_last;          // positions of the first and the last row's tokens
+  int s_tiles, t_lo;            // KV tiles: 0 .. s_tiles - 1, then t_lo ..
+  int i0, n;                    // the part: KV tiles i0 .. i0 + n - 1 of that list
+  int window, n_sink;
+
+  __device__ __forceinline__ int tile(int j) const {
+    const int i = i0 + j;
+    return i < s_tiles ? i : t_lo + i - s_tiles;
+  }
+  // every row of tokens at positions pf .. pl sees all positions of the tile
+  __device__ __forceinline__ bool whole(int kt, int pf, int pl) const {
+    const int t0 = kt * kKv, t1 = t0 + kKv - 1;
+    return t1 <= pf && (window == 0 || t0 > pl - window || t1 < n_sink);
+  }
+  // some row sees a position of [a, b]
+  __device__ __forceinline__ bool needed(int a, int b) const {
+    return a <= p_last && (window == 0 || b > p_first - window || a < n_sink);
+  }
+};
+
+__device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& list,
+                                        const ChunkUnits& units) {
+  Work w;
+  const int total = units.base[list.n];
+  const int lh = blockIdx.x % (A.g.H * A.nl);
+  const int c = blockIdx.x / (A.g.H * A.nl);
+  w.h = lh % A.g.H;
+  w.li = lh / A.g.H;
+  int x = 0;
+  for (int hi = list.n - 1; x < hi;) {
+    const int mid = (x + hi + 1) >> 1;
+    if (units.base[mid] <= c) x = mid;
+    else hi = mid - 1;
+  }
+  w.x = x;
+  const int ns = units.nsplit[x];
+  w.start = list.start[x];
+  w.len = list.row[x + 1] - list.row[x];
+  const int rows = w.len * A.G;
+  // a sequence's last tiles see most: they start first
+  const int turned = (c - units.base[x]) / ns;
+  const int split = c - units.base[x] - turned * ns;
+  const int tile = (rows + A.rows_cta - 1) / A.rows_cta - 1 - turned;
+  w.unit = (static_cast<int64_t>(w.li) * A.g.H + w.h) * total + units.base[x] +
+           static_cast<int64_t>(tile) * ns + split;
+  w.r0 = tile * A.rows_cta;
+  w.nrows = min(A.rows_cta, rows - w.r0);
+  w.p_first = w.start + w.r0 / A.G;
+  w.p_last = w.start + (w.r0 + w.nrows - 1) / A.G;
+  w.window = A.window;
+  w.n_sink = A.n_sink;
+  const int lo = A.window ? max(0, w.p_first - A.window + 1) : 0;
+  const int sinks = A.window ? min(A.n_sink, lo) : 0;
+  w.s_tiles = (sinks + kKv - 1) / kKv;
+  w.t_lo = max(lo / kKv, w.s_tiles);
+  const int all = w.s_tiles + max(0, w.p_last / kKv - w.t_lo + 1);
+  w.i0 = split * A.span;
+  w.n = min(A.span, all - w.i0);
+  return w;
+}
+
+__device__ __forceinline__ int page_of(const PoolDev& P, int agent, int pos) {
+  const int lp = P.p_shift >= 0 ? (pos >> P.p_shift) : pos / P.P;
+  int32_t page = -1;
+  if (lp < P.max_lp) page = __ldg(P.bt + static_cast<int64_t>(agent) * P.max_lp + lp);
+  return page >= 0 && page < P.num_pages ? page : -1;
+}
+
+// Output row (or partial) addresses of query row r (within the sequence).
+__device__ __forceinline__ int64_t out_row(const ChunkArgs& A, const ChunkList& list,
+                                           const Work& w, int r) {
+  const int tok = r / A.G;
+  return (static_cast<int64_t>(w.li) * A.tokens + list.tok[w.x] + tok) * A.nq +
+         w.h * A.G + (r - tok * A.G);
+}
+
+// Columns of a chunk of 32 that a row sees: c <= hi and (c > lo or c < sk), chunk-relative.
+__device__ __forceinline__ uint32_t first_bits(int n) {   // the lowest n bits
+  return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
+}
+
+// One tile's softmax for the thread's row: raises the maximum (and rescales O), writes the
+// weights over the scores and adds them to the sum. `seen`: the columns in sight, 4 words.
+template <int D, int kKind, bool kMask>
+__device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const uint32_t* seen,
+                                             float scale, const float* ks, const float* vs,
+                                             bool first, uint64_t* o_done, unsigned o_parity,
+                                             float& m_ref, float2& sum, Shared* sh,
+                                             uint32_t* err) {
+  constexpr bool k8 = kKind != kCacheBf16;
+  uint32_t x[32];
+  float mx = -INFINITY;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tc_ld32(x, t_s + c * 32);
+    tc_wait_ld();
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      float s = __uint_as_float(x[i]);
+      if constexpr (k8) s = __fmul_rn(s, ks[c * 32 + i]);
+      if constexpr (kMask) s = (seen[c] >> i) & 1u ? s : -INFINITY;
+      mx = fmaxf(mx, s);
+    }
+  }
+  const float m_tile = mx == -INFINITY ? mx : (k8 ? mx : __fmul_rn(mx, scale));
+  const float m_new = fmaxf(m_ref, m_tile);
+  if (first) {
+    m_ref = m_new;
+  } else if (__any_sync(0xFFFFFFFFu, m_new > m_ref + 8.0f)) {
+    // rows that did not grow keep theirs: a row's result does not depend on the others
+    const bool grow = m_new > m_ref + 8.0f;
+    const float f = grow ? ex2(m_ref - m_new) : 1.0f;
+    if (grow) m_ref = m_new;
+    sum.x *= f;
+    sum.y *= f;
+    if (!__all_sync(0xFFFFFFFFu, wait_or_abort(o_done, o_parity, sh, err))) return false;
+    tc_fence_after();
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      tc_ld32(x, t_o + c * 32);
+      tc_wait_ld();
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+      tc_st32(t_o + c * 32, x);
+    }
+  }
+  const float nm = m_ref == -INFINITY ? 0.0f : -m_ref;
+  const float2 nm2 = make_float2(nm, nm), sc2 = make_float2(scale, scale);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    tc_ld32(x, t_s + c * 32);
+    tc_wait_ld();
+    uint32_t p[16];
+#pragma unroll
+    for (int i = 0; i < 32; i += 2) {
+      float2 s = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      if constexpr (k8) s = fma2(s, *reinterpret_cast<const float2*>(ks + c * 32 + i), nm2);
+      else s = fma2(s, sc2, nm2);
+      float2 w = make_float2(ex2(s.x), ex2(s.y));
+      if constexpr (kMask) {
+        w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
+        w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
+      }
+      sum = add2(sum, w);
+      if constexpr (k8) {
+        const float2 v = *reinterpret_cast<const float2*>(vs + c * 32 + i);
+        w.x = __fmul_rn(w.x, v.x);
+        w.y = __fmul_rn(w.y, v.y);
+        if constexpr (kMask) {      // a scale out of sight may be a NaN
+          w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
+          w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
+        }
+      }
+      p[i / 2] = pack_bf2(w.x, w.y);
+    }
+    tc_st16(t_s + c * 16, p);
+  }
+  tc_wait_st();
+  return true;
+}
+
+// The CTA's rows one by one, a warp a row, in float32 throughout: for tiles that hold
+// infinities or NaNs which some rows see and others do not.
+template <int D>
+__device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list,
+                                       const ChunkUnits& units, int warp) {
+  constexpr int N = D / 32;
+  const Work w = work_of(A, list, units);
+  const int lane = threadIdx.x & 31;
+  const PoolDev& P = A.pool;
+  const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * P.num_pages * P.P;
+  const int64_t vplane = plane + P.num_pages * P.P;
+  for (int rr = warp; rr < w.nrows; rr += kSoftmaxWarps) {
+    const int r = w.r0 + rr;
+    const int pos = w.start + r / A.G;
+    const int64_t orow = out_row(A, list, w, r);
+    float q[N], acc[N], m = -INFINITY, l = 0.0f;
+    for (int i = 0; i < N; ++i) {
+      q[i] = __uint_as_float(static_cast<uint32_t>(A.q[orow * D + lane * N + i]) << 16);
+      acc[i] = 0.0f;
+    }
+    for (int j = 0; j < w.n; ++j) {
+      const int t0 = w.tile(j) * kKv;
+      for (int p = t0; p < t0 + kKv && p <= pos; ++p) {
+        if (w.window && p <= pos - w.window && p >= w.n_sink) continue;
+        const int page = page_of(P, list.agent[w.x], p);
+        if (page < 0) continue;
+        const int64_t row = static_cast<int64_t>(page) * P.P + p % P.P;
+        const uint16_t* k = P.base + (plane + row) * A.g.E + w.h * D + lane * N;
+        const uint16_t* v = P.base + (vplane + row) * A.g.E + w.h * D + lane * N;
+        float s = 0.0f;
+        for (int i = 0; i < N; ++i)
+          s = __fmaf_rn(q[i], __uint_as_float(static_cast<uint32_t>(k[i]) << 16), s);
+        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
+        s *= A.scale_log2;
+        const float m_new = fmaxf(m, s);
+        const float f = m == -INFINITY ? 0.0f : exp2f(m - m_new);
+        const float e = s == -INFINITY ? 0.0f : exp2f(s - m_new);
+        l = __fmaf_rn(l, f, e);
+        m = m_new;
+        for (int i = 0; i < N; ++i) {
+          const float val = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
+          acc[i] = __fmaf_rn(e, val, acc[i] * f);
+        }
+      }
+    }
+    if (A.direct) {
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+      for (int i = 0; i < N; i += 2)
+        *reinterpret_cast<uint32_t*>(A.out + orow * D + lane * N + i) =
+            pack_bf2(acc[i] * inv, acc[i + 1] * inv);
+      if (lane == 0 && A.lse)
+        A.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
+    } else {
+      const int64_t pr = w.unit * A.rows_cta + rr;
+      for (int i = 0; i < N; ++i) A.part_o[pr * D + lane * N + i] = acc[i];
+      if (lane == 0) {
+        A.part_ml[pr * 2] = m;
+        A.part_ml[pr * 2 + 1] = l;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <int D, int kKind>
+__global__ void __launch_bounds__(Plan<D, kKind != kCacheBf16>::kThreads, 1)
+chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
+                const __grid_constant__ ChunkUnits units, const __grid_constant__ CUtensorMap map) {
+  constexpr bool k8 = kKind != kCacheBf16;
+  using PL = Plan<D, k8>;
+  extern __shared__ unsigned char s_dyn[];
+  pdl_wait();
+  const Work w = work_of(A, list, units);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  if (w.n <= 0) {           // a part past the visible positions of its rows: empty
+    for (int rr = tid; rr < w.nrows; rr += PL::kThreads) {
+      A.part_ml[(w.unit * A.rows_cta + rr) * 2] = -INFINITY;
+      A.part_ml[(w.unit * A.rows_cta + rr) * 2 + 1] = 0.0f;
+    }
+    return;
+  }
+  unsigned char* base = s_dyn + ((1024 - (smem_u32(s_dyn) & 1023)) & 1023);
+  unsigned char* s_q = base;
+  unsigned char* s_k = base + PL::kQ;
+  unsigned char* s_v = s_k + PL::kK * PL::kTile;
+  float* s_scale = reinterpret_cast<float*>(s_v + PL::kV * PL::kTile);
+  int* s_rows = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(s_scale) + PL::kScales);
+  Shared* sh = reinterpret_cast<Shared*>(reinterpret_cast<unsigned char*>(s_rows) + PL::kPageRows);
+  const bool two = w.nrows > kRows;      // both query tiles in use
+
+  if (tid == 0) {
+    mbar_init(&sh->q_full, two ? 256 : 128);
+    for (int i = 0; i < PL::kK; ++i) {
+      mbar_init(&sh->k_full[i], k8 ? 128 : 1);
+      mbar_init(&sh->k_empty[i], 1);
+    }
+    for (int i = 0; i < PL::kV; ++i) {
+      mbar_init(&sh->v_raw[i], 1);
+      mbar_init(&sh->v_full[i], k8 ? 128 : 2);
+      mbar_init(&sh->v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->p_ready[i], 4);
+      mbar_init(&sh->o_done[i], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    sh->abort = 0;
+    sh->bad = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
+                 ::"r"(smem_u32(&sh->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh->tmem);
+
+  if (warp < kSoftmaxWarps) {
+    // ------------------------------------------------------------------ softmax
+    const int wg = warp >> 2;
+    const int t = tid & 127;               // the row within the query tile, and the TMEM lane
+    if (wg == 0 || two) {
+      {  // the query tile, rows past the last one zero; a negative scale turns the query's sign
+        const uint32_t flip = A.scale_log2 < 0.0f ? 0x80008000u : 0u;
+        unsigned char* dst = s_q + wg * (PL::kQ / 2);
+#pragma unroll 4
+        for (int i = 0; i < D / 8; ++i) {
+          const int v = t + i * 128;
+          const int r = v / (D / 8), c = v % (D / 8);
+          uint4 val = make_uint4(0u, 0u, 0u, 0u);
+          if (wg * kRows + r < w.nrows) {
+            val = ldg16(A.q + out_row(A, list, w, w.r0 + wg * kRows + r) * D + c * 8);
+            val.x ^= flip;
+            val.y ^= flip;
+            val.z ^= flip;
+            val.w ^= flip;
+          }
+          *reinterpret_cast<uint4*>(dst + tile_at(r, c)) = val;
+        }
+        fence_async_smem();
+        mbar_arrive(&sh->q_full);
+      }
+      const int rr = wg * kRows + t;
+      const bool live = rr < w.nrows;
+      const int pos = live ? w.start + (w.r0 + rr) / A.G : -1;
+      // positions of the query tile's first and last row
+      const int pf = w.start + (w.r0 + wg * kRows) / A.G;
+      const int pl = w.start + (w.r0 + min(wg * kRows + kRows, w.nrows) - 1) / A.G;
+      const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+      const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + 2 * kKv + wg * D;
+      const float scale = fabsf(A.scale_log2);
+      float m_ref = -INFINITY;
+      float2 sum = make_float2(0.0f, 0.0f);
+      bool ok = true;
+      for (int j = 0; j < w.n; ++j) {
+        // (the tensor memory's loads and stores are the whole warp's: it goes on or not as one)
+        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->s_full[wg], j & 1, sh, A.err));
+        if (!ok) break;
+        tc_fence_after();
+        const int kt = w.tile(j);
+        const uint4 valid = sh->info[j % kInfo].load();
+        const float* ks = s_scale + (j % kInfo) * 2 * kKv;
+        if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
+          const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
+          uint32_t seen[4];
+          const int hi = pos - kt * kKv, sk = w.n_sink - kt * kKv;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t b = first_bits(hi + 1 - c * 32);
+            if (w.window) b &= ~first_bits(hi - w.window + 1 - c * 32) | first_bits(sk - c * 32);
+            seen[c] = b & in[c];
+          }
+          ok = softmax_tile<D, kKind, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
+                                            &sh->o_done[wg], (j - 1) & 1, m_ref, sum, sh, A.err);
+        } else {
+          ok = softmax_tile<D, kKind, false>(t_s, t_o, nullptr, scale, ks, ks + kKv, j == 0,
+                                             &sh->o_done[wg], (j - 1) & 1, m_ref, sum, sh, A.err);
+        }
+        if (!ok) break;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_ready[wg]);
+      }
+      if (ok)
+        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->o_done[wg], (w.n - 1) & 1, sh, A.err));
+      if (ok && *reinterpret_cast<volatile int*>(&sh->bad) == 0) {
+        tc_fence_after();
+        const float l = sum.x + sum.y;
+        if (A.direct) {
+          const int64_t row = live ? out_row(A, list, w, w.r0 + rr) : 0;
+          const float inv = l == 0.0f ? 0.0f : 1.0f / l;      // a row that sees nothing: zeros
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tc_ld32(x, t_o + c * 32);
+            tc_wait_ld();
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[i * 8 + e]) * inv;
+                st16(A.out + row * D + c * 32 + i * 8, pack8(y));
+              }
+            }
+          }
+          if (live && A.lse)
+            A.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994530942f;
+        } else {
+          const int64_t pr = w.unit * A.rows_cta + rr;
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tc_ld32(x, t_o + c * 32);
+            tc_wait_ld();
+            if (live) {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                *reinterpret_cast<uint4*>(A.part_o + pr * D + c * 32 + i * 4) =
+                    make_uint4(x[i * 4], x[i * 4 + 1], x[i * 4 + 2], x[i * 4 + 3]);
+            }
+          }
+          if (live) {
+            A.part_ml[pr * 2] = m_ref;
+            A.part_ml[pr * 2 + 1] = l;
+          }
+        }
+        tc_fence_before();
+      }
+    }
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- the products
+    if (lane == 0) {
+      const uint32_t q_addr = smem_u32(s_q), k_addr = smem_u32(s_k), v_addr = smem_u32(s_v);
+      constexpr uint32_t id_s = tc_idesc(kKv, false), id_o = tc_idesc(D, true);
+      auto scores = [&](int wg, int slot) {
+#pragma unroll
+        for (int kc = 0; kc < D / 16; ++kc) {
+          const uint32_t off = (kc >> 2) * (128 * 128) + (kc & 3) * 32;
+          tc_mma_ss(tmem + wg * kKv, tc_desc(q_addr + wg * (PL::kQ / 2) + off, 16),
+                    tc_desc(k_addr + slot * PL::kTile + off, 16), id_s, kc > 0);
+        }
+        tc_commit(&sh->s_full[wg]);
+      };
+      bool ok = wait_or_abort(&sh->q_full, 0, sh, A.err) &&
+                wait_or_abort(&sh->k_full[0], 0, sh, A.err);
+      if (ok) {
+        tc_fence_after();
+        scores(0, 0);
+        if (two) scores(1, 0);
+        tc_commit(&sh->k_empty[0]);
+      }
+      for (int j = 0; ok && j < w.n; ++j) {
+        const int vs = j % PL::kV, ks = (j + 1) % PL::kK;
+        for (int wg = 0; wg < (two ? 2 : 1); ++wg) {
+          ok = wait_or_abort(&sh->p_ready[wg], j & 1, sh, A.err);
+          if (ok && wg == 0) ok = wait_or_abort(&sh->v_full[vs], (j / PL::kV) & 1, sh, A.err);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int kc = 0; kc < kKv / 16; ++kc)
+            tc_mma_ts(tmem + 2 * kKv + wg * D, tmem + wg * kKv + kc * 8,
+                      tc_desc(v_addr + vs * PL::kTile + kc * 2048, 128 * 128), id_o,
+                      j > 0 || kc > 0);
+          tc_commit(&sh->o_done[wg]);
+          if (wg == (two ? 1 : 0)) tc_commit(&sh->v_empty[vs]);
+          if (j + 1 < w.n) {
+            if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], ((j + 1) / PL::kK) & 1, sh, A.err);
+            if (!ok) break;
+            tc_fence_after();
+            scores(wg, ks);
+            if (wg == (two ? 1 : 0)) tc_commit(&sh->k_empty[ks]);
+          }
+        }
+      }
+      // whatever was started has ended before the TMEM goes
+      tc_commit(&sh->drain);
+      mbar_wait_bounded(&sh->drain, 0);
+    }
+    __syncwarp();
+  } else if constexpr (!k8) {
+    if (warp == kLoadWarp) {
+      // ------------------------------------------------------------- K and V by TMA
+      const PoolDev& P = A.pool;
+      const int box = A.box_rows, per = kKv / box;       // boxes per 64 dims
+      const int nbox = per * (D / 64);
+      const int plane = 2 * w.li * static_cast<int>(P.num_pages * P.P);
+      const int vplane = static_cast<int>(P.num_pages * P.P);
+      bool ok = true;
+      int n_k = 0, n_v = 0;                               // tiles started
+      for (int j = 0; j < w.n; ++j) {
+        const int kt = w.tile(j);
+        const int b = lane;                               // at most 32 boxes a tile
+        const int rb = b % per, half = b / per;
+        const int pos = kt * kKv + rb * box;
+        const bool need = b < nbox && w.needed(pos, pos + box - 1);
+        int row = -1;
+        if (need) {
+          const int page = page_of(P, list.agent[w.x], pos);
+          if (page >= 0) row = plane + page * P.P + pos % P.P;
+          else atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+        }
+        const uint32_t holes = __ballot_sync(0xFFFFFFFFu, need && row < 0 && half == 0);
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0)) * box * 128u;
+        const int ks = j % PL::kK, vs = j % PL::kV;
+        if (j >= PL::kK) ok = wait_or_abort(&sh->k_empty[ks], ((j / PL::kK) - 1) & 1, sh, A.err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (lane < 4) {
+          uint32_t v = 0xFFFFFFFFu;
+          if (holes)
+            for (int i = 0; i < 32; ++i)
+              if ((holes >> ((lane * 32 + i) / box)) & 1u) v &= ~(1u << i);
+          sh->info[j % kInfo].valid[lane] = v;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive_expect_tx(&sh->k_full[ks], bytes + A.tx_pad);
+        __syncwarp();
+        const uint32_t off = half * (128 * 128) + rb * box * 128;
+        if (row >= 0)
+          tma_box(smem_u32(s_k) + ks * PL::kTile + off, &map, w.h * D + half * 64, row,
+                  &sh->k_full[ks]);
+        ++n_k;
+        if (j >= PL::kV) ok = wait_or_abort(&sh->v_empty[vs], ((j / PL::kV) - 1) & 1, sh, A.err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) break;
+        if (lane == 0) mbar_arrive_expect_tx(&sh->v_raw[vs], bytes + A.tx_pad);
+        __syncwarp();
+        if (row >= 0)
+          tma_box(smem_u32(s_v) + vs * PL::kTile + off, &map, w.h * D + half * 64, row + vplane,
+                  &sh->v_raw[vs]);
+        ++n_v;
+      }
+      // the copies that were started land before the block goes, time-out or not
+      for (int i = max(0, n_k - PL::kK); i < n_k; ++i)
+        mbar_wait_bounded(&sh->k_full[i % PL::kK], (i / PL::kK) & 1);
+      for (int i = max(0, n_v - PL::kV); i < n_v; ++i)
+        mbar_wait_bounded(&sh->v_raw[i % PL::kV], (i / PL::kV) & 1);
+    } else {
+      // ----------------------------------------------- V tiles patched where they must be
+      const int t = tid - kPatchWarp * 32;
+      for (int j = 0; j < w.n; ++j) {
+        const int vs = j % PL::kV, kt = w.tile(j);
+        const bool ok = wait_or_abort(&sh->v_raw[vs], (j / PL::kV) & 1, sh, A.err);
+        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        const uint4 in = sh->info[j % kInfo].load();
+        if (!w.whole(kt, w.p_first, w.p_last) || !no_holes(in)) {
+          unsigned char* tile = s_v + vs * PL::kTile;
+          bool bad = false;
+#pragma unroll 4
+          for (int i = t; i < kKv * (D / 8); i += 64) {
+            const int r = i / (D / 8), c = i % (D / 8);
+            const int pos = kt * kKv + r;
+            uint4* at = reinterpret_cast<uint4*>(tile + tile_at(r, c));
+            const uint32_t word = r < 64 ? (r < 32 ? in.x : in.y) : (r < 96 ? in.z : in.w);
+            if (!w.needed(pos, pos) || !((word >> (r & 31)) & 1u)) {
+              *at = make_uint4(0u, 0u, 0u, 0u);
+              continue;
+            }
+            uint4 v = *at;
+            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              if ((u[e] & 0x7F80u) == 0x7F80u) {
+                u[e] &= 0xFFFF0000u;
+                hit = true;
+              }
+              if ((u[e] & 0x7F800000u) == 0x7F800000u) {
+                u[e] &= 0x0000FFFFu;
+                hit = true;
+              }
+            }
+            if (hit) *at = v;
+            bad |= hit;
+          }
+          if (bad) *reinterpret_cast<volatile int*>(&sh->bad) = 1;
+          fence_async_smem();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->v_full[vs]);
+      }
+    }
+  } else {
+    // --------------------------------------------------------- K and V from 8-bit codes
+    const int t = tid - kLoadWarp * 32;                   // 0 .. 127: a position of each tile
+    constexpr int kVec = D / 16;                          // 16-byte vectors per row
+    const PoolDev& P = A.pool;
+    const int64_t half = P.num_pages * P.P;
+    const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * half;
+    const float kmul = fabsf(A.scale_log2);
+    // position t's page row of tile j: -1 not needed, -2 unmapped
+    auto lookup = [&](int j) {
+      if (j >= w.n) return -1;
+      const int pos = w.tile(j) * kKv + t;
+      if (!w.needed(pos, pos)) return -1;
+      const int page = page_of(P, list.agent[w.x], pos);
+      return page < 0 ? -2 : page * P.P + pos % P.P;
+    };
+    uint4 code[2][kVec];
+    auto load = [&](int kv, int j) {      // kVec threads a row, 128 / kVec rows a step
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(P.base) + (plane + kv * half) * A.g.E +
+                           w.h * D + (t % kVec) * 16;
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) {
+        const int row = s_rows[(j & 1) * kKv + i * (kKv / kVec) + t / kVec];
+        code[kv][i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                              : __ldg(reinterpret_cast<const uint4*>(
+                                    src + static_cast<int64_t>(row) * A.g.E));
+      }
+    };
+    float ks = 0.0f, vs = 0.0f;
+    auto load_scales = [&](int row) {
+      ks = row < 0 ? 0.0f : __ldg(A.scale + (plane + row) * A.g.H + w.h);
+      vs = row < 0 ? 0.0f : __ldg(A.scale + (plane + half + row) * A.g.H + w.h);
+    };
+    auto group_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    int row = lookup(0), next = lookup(1);
+    s_rows[t] = row;
+    group_sync();
+    load(0, 0);
+    load(1, 0);
+    load_scales(row);
+    bool ok = true;                       // after a time-out the group still meets its barriers
+    for (int j = 0; j < w.n; ++j) {
+      const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
+      if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+      if (lane == 0) sh->info[j % kInfo].valid[t >> 5] = ~hole;
+      s_scale[(j % kInfo) * 2 * kKv + t] = __fmul_rn(ks, kmul);
+      s_scale[(j % kInfo) * 2 * kKv + kKv + t] = vs;
+      row = next;
+      s_rows[((j + 1) & 1) * kKv + t] = row;
+      group_sync();
+      next = lookup(j + 2);
+      load_scales(row);
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        const int slots = kv ? PL::kV : PL::kK, slot = j % slots;
+        if (ok && j >= slots)
+          ok = wait_or_abort(kv ? &sh->v_empty[slot] : &sh->k_empty[slot], ((j / slots) - 1) & 1,
+                             sh, A.err);
+        if (ok) {
+          unsigned char* tile = (kv ? s_v : s_k) + slot * PL::kTile;
+#pragma unroll
+          for (int i = 0; i < kVec; ++i) {
+            const int r = i * (kKv / kVec) + t / kVec, c = (t % kVec) * 2;
+            const uint4 v = code[kv][i];
+            *reinterpret_cast<uint4*>(tile + tile_at(r, c)) =
+                make_uint4(word_bf16<kKind, false>(v.x), word_bf16<kKind, true>(v.x),
+                           word_bf16<kKind, false>(v.y), word_bf16<kKind, true>(v.y));
+            *reinterpret_cast<uint4*>(tile + tile_at(r, c + 1)) =
+                make_uint4(word_bf16<kKind, false>(v.z), word_bf16<kKind, true>(v.z),
+                           word_bf16<kKind, false>(v.w), word_bf16<kKind, true>(v.w));
+          }
+          fence_async_smem();
+          mbar_arrive(kv ? &sh->v_full[slot] : &sh->k_full[slot]);
+        }
+        load(kv, j + 1);
+      }
+    }
+  }
+
+  __syncthreads();
+  if constexpr (!k8) {
+    if (sh->bad && !sh->abort && warp < kSoftmaxWarps) slow_rows<D>(A, list, units, warp);
+  }
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+template <int D, int kKind>
+static cudaError_t run_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                          const CUtensorMap& map, cudaStream_t st) {
+  using PL = Plan<D, kKind != kCacheBf16>;
+  const unsigned grid = static_cast<unsigned>(units.base[list.n]) * a.g.H * a.nl;
+  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<D, kKind>,
+                                       cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(chunk_tc_kernel<D, kKind>, grid, PL::kThreads, PL::kSmem, st, a, list, units,
+                      map);
+}
+
+cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                            const CUtensorMap& map, CacheKind kind, cudaStream_t st) {
+  if (a.g.D != 64 && a.g.D != 128) return cudaErrorInvalidValue;
+  const bool wide = a.g.D == 128;
+  switch (kind) {
+    case kCacheBf16:
+      return wide ? run_tc<128, kCacheBf16>(a, list, units, map, st)
+                  : run_tc<64, kCacheBf16>(a, list, units, map, st);
+    case kCacheInt8:
+      return wide ? run_tc<128, kCacheInt8>(a, list, units, map, st)
+                  : run_tc<64, kCacheInt8>(a, list, units, map, st);
+    case kCacheE4m3:
+      return wide ? run_tc<128, kCacheE4m3>(a, list, units, map, st)
+                  : run_tc<64, kCacheE4m3>(a, list, units, map, st);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace td

@@ -68,14 +68,22 @@ bool layers_ok(const td_ctx* c, int32_t begin, int32_t end) {
   return begin >= 0 && end <= c->shape.n_layers && begin < end;
 }
 
-// The sequences [x0, x0 + list->n) of the call.
-void fill_list(const td_chunks* ch, int x0, ChunkList* list) {
-  list->n = std::min(ch->n - x0, kMaxChunkSeqs);
+// Fills the list with up to kMaxChunkSeqs of the call's sequences from *x on that `take`
+// accepts, and advances *x and *tok (the dense row of sequence *x's first token).
+template <typename Take>
+void fill_list(const td_chunks* ch, int* x, int64_t* tok, Take take, ChunkList* list) {
+  list->n = 0;
   list->row[0] = 0;
-  for (int x = 0; x < list->n; ++x) {
-    list->agent[x] = ch->agent[x0 + x];
-    list->start[x] = ch->start[x0 + x];
-    list->row[x + 1] = list->row[x] + ch->len[x0 + x];
+  for (; *x < ch->n && list->n < kMaxChunkSeqs; ++*x) {
+    const int len = ch->len[*x];
+    if (take(len)) {
+      const int i = list->n++;
+      list->tok[i] = static_cast<int32_t>(*tok);
+      list->agent[i] = ch->agent[*x];
+      list->start[i] = ch->start[*x];
+      list->row[i + 1] = list->row[i] + len;
+    }
+    *tok += len;
   }
 }
 
@@ -126,15 +134,14 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   while (a.per_cta > 4 &&
          (tokens + a.per_cta - 1) / a.per_cta * a.nl * 2 < 4 * static_cast<int64_t>(c->sm_count))
     a.per_cta >>= 1;
-  int64_t tok0 = 0;
-  for (int x0 = 0; x0 < ch->n; x0 += kMaxChunkSeqs) {
+  int64_t tok = 0;
+  for (int x = 0; x < ch->n;) {
     ChunkList list;
-    fill_list(ch, x0, &list);
-    a.tok0 = tok0;
+    a.tok0 = tok;
+    fill_list(ch, &x, &tok, [](int) { return true; }, &list);
     const cudaError_t e = write ? launch_quantise(a, list, kind, st)
                                 : launch_dequantise(a, list, kind, st);
     if (e != cudaSuccess) return TD_ERR_CUDA;
-    tok0 += list.row[list.n];
   }
   return TD_OK;
 }
@@ -157,6 +164,109 @@ td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
   return TD_OK;
 }
 
+constexpr int kFewRows = 16;
+
+// The bf16 pages of the call's layers as a tensor map of boxes that lie inside a page; false
+// where the tensor-core kernel cannot read them: pages that are no multiple of 8 tokens (a
+// box is at least 8 rows, the period of the swizzle), or more rows than a coordinate counts.
+bool bf16_map(const td_ctx* c, const ChunkArgs& a, const PoolDev& pool, int* box, CUtensorMap* m) {
+  if (pool.P % 8 != 0) return false;
+  const int64_t plane = pool.num_pages * pool.P;
+  const int64_t rows = 2 * plane * a.nl;
+  if (rows > INT32_MAX) return false;
+  int b = 8;
+  while (b < 128 && pool.P % (2 * b) == 0) b *= 2;
+  *box = b;
+  EncodeTiledFn fn = encode_tiled();
+  if (!fn) return false;
+  const int E = c->g.E;
+  uint16_t* base = pool.base + static_cast<int64_t>(a.layer_begin) * 2 * plane * E;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(E), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(E) * 2};
+  const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(b)};
+  const cuuint32_t elem[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, base, dims, strides, bx, elem,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+         CUDA_SUCCESS;
+}
+
+// Cuts every tile's visible positions (in steps of `step` positions) into parts of one length
+// and fills base, nsplit, span and direct; the number of units, or -1. tiles(x), seen(x): a
+// sequence's tiles of query rows and the steps that one of them sees at most. `slots` units
+// run at once; a unit costs its steps and `fixed` more. The length is the one with the least
+// waves x cost among the divisions of the longest tile.
+template <typename Tiles, typename Seen>
+int64_t cut(const ChunkList& list, int64_t slots, int64_t heads, int fixed, int least, Tiles tiles,
+            Seen seen, int step, ChunkArgs* a, ChunkUnits* units) {
+  int64_t longest = 1;
+  for (int x = 0; x < list.n; ++x) longest = std::max<int64_t>(longest, seen(x));
+  int64_t best = 0, best_cost = INT64_MAX, last = 0;
+  for (int64_t k = 1; k <= 256; k = k < 16 ? k + 1 : k + k / 8) {
+    const int64_t span = std::max<int64_t>((longest + k - 1) / k, std::min<int64_t>(least, longest));
+    if (span == last) continue;
+    last = span;
+    int64_t n = 0;
+    for (int x = 0; x < list.n; ++x) n += tiles(x) * ((seen(x) + span - 1) / span);
+    n *= heads;
+    const int64_t cost = (n + slots - 1) / slots * (span + fixed) + (k > 1 ? fixed : 0);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = span;
+    }
+    if (span <= least) break;
+  }
+  a->span = static_cast<int>(best * step);
+  a->direct = 1;
+  units->base[0] = 0;
+  int64_t sum = 0;
+  for (int x = 0; x < list.n; ++x) {
+    const int64_t ns = (seen(x) + best - 1) / best;
+    if (ns > 1) a->direct = 0;
+    sum += tiles(x) * ns;
+    if (sum > INT32_MAX) return -1;
+    units->nsplit[x] = static_cast<int32_t>(ns);
+    units->base[x + 1] = static_cast<int32_t>(sum);
+  }
+  return sum * heads > INT32_MAX ? -1 : sum * heads;
+}
+
+// Positions that a tile of `rows` query rows of sequence x sees, at most.
+int64_t seen_positions(const ChunkList& list, const ChunkArgs& a, int x, int rows) {
+  const int64_t all = static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x];
+  if (a.window == 0) return all;
+  return std::min<int64_t>(all, static_cast<int64_t>(a.window) + a.n_sink + (rows - 1) / a.G + 1);
+}
+
+int64_t plan_rows(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
+                  int* rows) {
+  int64_t most = 0;
+  for (int x = 0; x < list.n; ++x)
+    most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
+  const int R = *rows = most <= 8 ? 8 : 16;
+  return cut(
+      list, static_cast<int64_t>(c->sm_count) * 8, static_cast<int64_t>(a->g.H) * a->nl, 4, 8,
+      [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
+      [&](int x) { return (seen_positions(list, *a, x, R) + 15) / 16; }, 16, a, units);
+}
+
+int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
+                int* rows) {
+  int64_t most = 0;
+  for (int x = 0; x < list.n; ++x)
+    most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
+  const int R = *rows = a->rows_cta = most <= 128 ? 128 : 256;
+  return cut(
+      list, c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, 2, 2,
+      [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
+      // a window's positions may straddle one tile more, the first ones' another
+      [&](int x) {
+        const int64_t all = (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
+        return a->window ? std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2) : all;
+      },
+      1, a, units);
+}
+
 td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& pool,
                               const float* scale8, CacheKind kind, int32_t layer_begin,
                               int32_t layer_end, const void* q, int32_t n_q_heads, float scale,
@@ -174,6 +284,7 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
       (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || tokens > INT32_MAX / n_q_heads)
     return TD_ERR_INVALID_ARG;
   ChunkArgs a{};
+  CUtensorMap map{};
   a.g = c->g;
   a.pool = pool;
   a.scale = scale8;
@@ -189,59 +300,39 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   a.n_sink = n_sink;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = c->d_err;
-  int64_t tok0 = 0;
-  for (int x0 = 0; x0 < ch->n; x0 += kMaxChunkSeqs) {
-    ChunkList list;
-    fill_list(ch, x0, &list);
-    a.tok0 = tok0;
-    tok0 += list.row[list.n];
-    if (list.row[list.n] == 0) continue;
-    int most_rows = 0;
-    for (int x = 0; x < list.n; ++x)
-      most_rows = std::max(most_rows, (list.row[x + 1] - list.row[x]) * a.G);
-    const int R = most_rows <= 8 ? 8 : 16;
-    // visible positions of a tile of sequence x, at most
-    auto seen = [&](int x) -> int64_t {
-      const int64_t all = static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x];
-      return window == 0 ? all
-                         : std::min<int64_t>(all, static_cast<int64_t>(window) + n_sink +
-                                                      (R - 1) / a.G + 1);
-    };
-    auto tiles = [&](int x) -> int64_t {
-      return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a.G + R - 1) / R;
-    };
-    int64_t positions = 0, longest = 0;
-    for (int x = 0; x < list.n; ++x) {
-      if (tiles(x) == 0) continue;
-      positions += tiles(x) * seen(x);
-      longest = std::max(longest, seen(x));
+  // Sequences of at most kFewRows query rows per kv head go to the streaming kernel, the
+  // others to the tensor-core kernel, each in lists of kMaxChunkSeqs. Plans first, so that
+  // the scratch is there (or the call refused) before anything is launched.
+  const bool tc_pages = kind != kCacheBf16 || bf16_map(c, a, pool, &a.box_rows, &map);
+  a.tx_pad = c->attn_tx_pad;
+  size_t need = 0;
+  for (int pass = 0; pass < 2; ++pass) {
+    if (pass == 1 && (s = chunk_scratch(c, need, st)) != TD_OK) return s;
+    for (int tc = 0; tc < 2; ++tc) {
+      int64_t tok = 0;
+      for (int x = 0; x < ch->n;) {
+        ChunkList list;
+        ChunkUnits units;
+        fill_list(ch, &x, &tok, [&](int len) {
+          const bool few = !tc_pages || static_cast<int64_t>(len) * a.G <= kFewRows;
+          return len > 0 && few == (tc == 0);
+        }, &list);
+        if (list.n == 0) continue;
+        int rows = 0;
+        const int64_t n = tc ? plan_tc(c, list, &a, &units, &rows)
+                             : plan_rows(c, list, &a, &units, &rows);
+        if (n < 0) return TD_ERR_INVALID_ARG;
+        const size_t floats = a.direct ? 0 : static_cast<size_t>(n) * rows * (D + 2);
+        need = std::max(need, floats);
+        if (pass == 0) continue;
+        a.part_o = c->d_chunk;
+        a.part_ml = a.direct ? nullptr : c->d_chunk + static_cast<size_t>(n) * rows * D;
+        if ((tc ? launch_chunk_tc(a, list, units, map, kind, st)
+                : launch_chunk_rows(a, list, units, kind, rows, st)) != cudaSuccess ||
+            (!a.direct && launch_chunk_join(a, list, units, rows, st) != cudaSuccess))
+          return TD_ERR_CUDA;
+      }
     }
-    const int64_t warps = static_cast<int64_t>(c->sm_count) * 12;
-    int64_t span = positions * H * a.nl / warps;
-    span = std::max<int64_t>((span + 15) / 16 * 16, 128);
-    a.span = static_cast<int>(std::min<int64_t>(span, (longest + 15) / 16 * 16));
-    ChunkUnits units;
-    units.base[0] = 0;
-    a.direct = 1;
-    int64_t sum = 0;
-    for (int x = 0; x < list.n; ++x) {
-      const int64_t ns = std::max<int64_t>((seen(x) + a.span - 1) / a.span, 1);
-      if (tiles(x) > 0 && ns > 1) a.direct = 0;
-      sum += tiles(x) * ns;
-      if (sum > INT32_MAX) return TD_ERR_INVALID_ARG;
-      units.nsplit[x] = static_cast<int32_t>(ns);
-      units.base[x + 1] = static_cast<int32_t>(sum);
-    }
-    const int64_t n = sum * H * a.nl;
-    if (n > INT32_MAX) return TD_ERR_INVALID_ARG;
-    if (!a.direct) {
-      if ((s = chunk_scratch(c, static_cast<size_t>(n) * R * (D + 2), st)) != TD_OK) return s;
-      a.part_o = c->d_chunk;
-      a.part_ml = c->d_chunk + static_cast<size_t>(n) * R * D;
-    }
-    if (launch_chunk_rows(a, list, units, kind, R, st) != cudaSuccess ||
-        (!a.direct && launch_chunk_join(a, list, units, R, st) != cudaSuccess))
-      return TD_ERR_CUDA;
   }
   return TD_OK;
 }

@@ -193,9 +193,11 @@ cudaError_t launch_materialise(const Geom& g, const RoundDev& rd, const StoreDev
 constexpr int kMaxChunkSeqs = 256;  // sequences per launch (passed by value)
 
 // The sequences of one launch. Token t of the launch belongs to the sequence x with
-// row[x] <= t < row[x + 1], at position start[x] + t - row[x] of agent[x].
+// row[x] <= t < row[x + 1], at position start[x] + t - row[x] of agent[x]; its dense row is
+// tok[x] + t - row[x].
 struct ChunkList {
   int n;
+  int32_t tok[kMaxChunkSeqs];
   int32_t agent[kMaxChunkSeqs];
   int32_t start[kMaxChunkSeqs];
   int32_t row[kMaxChunkSeqs + 1];     // exclusive prefix of the sequences' tokens
@@ -224,7 +226,7 @@ struct QuantArgs {
   uint16_t* k;               // bf16 rows [nl][tokens][E]: read by the write, written by the read
   uint16_t* v;
   int64_t tokens;            // tokens of the whole call
-  int64_t tok0;              // this launch's first
+  int64_t tok0;              // this launch's first (its sequences follow one another)
   int nl, layer_begin;
   int lane_shift;            // lanes per head row = 1 << lane_shift (>= D / 8, at most 32)
   int head_mul;              // ceil(2^20 / H): row / H without a division
@@ -247,11 +249,15 @@ struct ChunkArgs {
   float* lse;                // [nl][tokens][nq] or nullptr
   float* part_o;             // [units][rows per tile][D] unnormalised outputs
   float* part_ml;            // [units][rows per tile][2]: max, sum (base 2)
-  int64_t tokens, tok0;      // tokens of the whole call; this launch's first
+  int64_t tokens;            // tokens of the whole call
   int nq, G;                 // query heads, query heads per kv head
   int nl, layer_begin;
   int window, n_sink;        // 0: every earlier position is seen
-  int span;                  // visible positions per unit (a multiple of 16)
+  int span;                  // per unit: visible positions (streaming kernel; a multiple of
+                             // 16) or KV tiles of 128 positions (tensor-core kernel)
+  int rows_cta;              // tensor-core kernel: query rows per unit, 128 or 256
+  int box_rows;              // ... and rows per box of its tensor map
+  uint32_t tx_pad;           // ... extra bytes every tile expects (fault injection; 0 normally)
   int direct;                // 1: one unit per tile everywhere, outputs written at once
   float scale_log2;          // softmax scale * log2(e)
   uint32_t* err;
@@ -260,6 +266,10 @@ struct ChunkArgs {
 // Query rows (token, head of the group) per tile of the streaming kernel: 8 or 16.
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               CacheKind kind, int rows_per_tile, cudaStream_t st);
+// The tensor-core kernel for many rows. map: the bf16 pool's rows of the call's layers, boxes
+// of box_rows x 64 (8-bit pages: not read).
+cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                            const CUtensorMap& map, CacheKind kind, cudaStream_t st);
 // Joins the units of every query row.
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st);

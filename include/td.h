@@ -497,9 +497,10 @@ td_status td_group_round(const td_prompt* prompts, int32_t n_prompts, int32_t se
                          int32_t* perm);
 
 /* Fault injection for tests; no counterpart in the paper. With bytes > 0 every later
- * td_fused_attention / td_paged_attention call on this context makes each stage's barrier
- * expect `bytes` more than its copies deliver, so every bounded wait runs out (0.2 s of
- * device time each): the units record TD_ERR_DEVICE_TIMEOUT in the error word, wait
+ * td_fused_attention / td_paged_attention call on this context, and every
+ * td_chunk_attention call of chunks that its tensor-core kernel takes, makes each stage's
+ * barrier expect `bytes` more than its copies deliver, so every bounded wait runs out (0.2 s
+ * of device time each): the units record TD_ERR_DEVICE_TIMEOUT in the error word, wait
  * (bounded) for their own copies and return, and the outputs are not valid. No copy is
  * lost and nothing faults: the context stays usable. bytes = 0 restores normal calls. */
 td_status td_inject_attention_wait_fault(td_ctx* ctx, uint32_t bytes);

@@ -10,7 +10,7 @@ using namespace td;
 
 namespace {
 struct Launch {
-  int what;           // 0 quantise, 1 dequantise, 2 streaming attention, 3 join
+  int what;           // 0 quantise, 1 dequantise, 2 streaming attention, 3 join, 4 tensor cores
   int kind, rows;
   ChunkArgs a;
   QuantArgs qa;
@@ -52,6 +52,15 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
   l.rows = rows;
   return cudaSuccess;
 }
+cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
+                            const CUtensorMap&, CacheKind kind, cudaStream_t) {
+  Launch& l = push(4, list);
+  l.a = a;
+  l.units = units;
+  l.kind = kind;
+  l.rows = a.rows_cta;
+  return cudaSuccess;
+}
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows, cudaStream_t) {
   Launch& l = push(3, list);
@@ -62,8 +71,26 @@ cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const C
 }
 }  // namespace td
 
+// What cuTensorMapEncodeTiled checks, and that a box is 8 to 128 rows of 64.
+static CUresult fake_encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t rank, void* base,
+                            const cuuint64_t* dims, const cuuint64_t* strides,
+                            const cuuint32_t* box, const cuuint32_t*, CUtensorMapInterleave,
+                            CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill) {
+  const bool ok = rank == 2 && (reinterpret_cast<uintptr_t>(base) & 15) == 0 &&
+                  strides[0] % 16 == 0 && strides[0] == dims[0] * 2 && dims[1] > 0 &&
+                  dims[1] <= INT32_MAX && box[0] == 64 && box[1] >= 8 && box[1] <= 128 &&
+                  box[1] % 8 == 0;
+  return ok ? CUDA_SUCCESS : CUDA_ERROR_INVALID_VALUE;
+}
+
 extern "C" {
 
+cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, unsigned long long,
+                                             cudaDriverEntryPointQueryResult* q) {
+  *f = reinterpret_cast<void*>(fake_encode);
+  *q = cudaDriverEntryPointSuccess;
+  return cudaSuccess;
+}
 cudaError_t cudaGetDevice(int* d) {
   *d = g_device;
   return cudaSuccess;
@@ -101,16 +128,17 @@ void fake_state(int device, int capturing, int fail_malloc) {
 void fake_reset(void) { g_launches.clear(); }
 int64_t fake_floats(void) { return static_cast<int64_t>(g_floats); }
 int fake_launches(void) { return static_cast<int>(g_launches.size()); }
-// what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul
+// what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul, box_rows
 void fake_launch(int i, int64_t* out) {
   const Launch& l = g_launches[i];
   const bool quant = l.what < 2;
   const int64_t v[] = {l.what, l.kind, l.rows, l.list.n, l.a.direct, l.a.span,
-                       quant ? l.qa.tok0 : l.a.tok0, quant ? l.qa.tokens : l.a.tokens,
-                       l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul};
-  for (int k = 0; k < 11; ++k) out[k] = v[k];
+                       quant ? l.qa.tok0 : 0, quant ? l.qa.tokens : l.a.tokens,
+                       l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul, l.a.box_rows};
+  for (int k = 0; k < 12; ++k) out[k] = v[k];
 }
-void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* base, int32_t* ns) {
+void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* base, int32_t* ns,
+               int32_t* tok) {
   const Launch& l = g_launches[i];
   for (int x = 0; x <= l.list.n; ++x) {
     row[x] = l.list.row[x];
@@ -119,6 +147,7 @@ void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* bas
       agent[x] = l.list.agent[x];
       start[x] = l.list.start[x];
       ns[x] = l.units.nsplit[x];
+      tok[x] = l.list.tok[x];
     }
   }
 }

@@ -83,13 +83,14 @@ class Call:
     def launches(self):
         res = []
         for i in range(self.lib.fake_launches()):
-            v = (C.c_int64 * 11)()
+            v = (C.c_int64 * 12)()
             self.lib.fake_launch(i, v)
-            keys = ("what kind rows n direct span tok0 tokens per_cta lane_shift head_mul").split()
+            keys = ("what kind rows n direct span tok0 tokens per_cta lane_shift head_mul "
+                    "box").split()
             d = dict(zip(keys, v))
-            arr = [np.zeros(300, np.int32) for _ in range(5)]
+            arr = [np.zeros(300, np.int32) for _ in range(6)]
             self.lib.fake_list(i, *(a.ctypes.data_as(C.c_void_p) for a in arr))
-            d.update(zip(("agent", "start", "row", "base", "nsplit"), arr))
+            d.update(zip(("agent", "start", "row", "base", "nsplit", "tok"), arr))
             res.append(d)
         return res
 
@@ -210,52 +211,63 @@ def test_plans_of_the_quantising_kernels(td, lib):
                 assert np.array_equal(prod >> 20, rows // H)      # the division it stands for
 
 
-def _check_attention(td, lib, call, H, D, nq, chunks, window, sinks, nl):
+def _steps(what, s, t, G, R, tile, window, sinks):
+    """Steps that the kernel takes for a tile: visible positions, or KV tiles of 128."""
+    first = s + tile * R // G
+    last = s + min(tile * R + R - 1, t * G - 1) // G
+    lo = max(0, first - window + 1) if window else 0
+    kept = min(sinks, lo) if window else 0
+    if what == 2:
+        return last + 1 - lo + kept
+    tiles = set(range(lo // 128, last // 128 + 1)) | set(range(-(-kept // 128)))
+    return len(tiles)
+
+
+def _check_attention(lib, call, H, D, P, nq, chunks, window, sinks, nl, q8):
     G = nq // H
+    at, rows_of = {}, {}
     tok = 0
-    seqs = list(chunks)
-    ls = call.launches()
-    assert ls
-    for l in ls:
-        if l["what"] != 2:
+    for i, (a, s, t) in enumerate(chunks):
+        if t:
+            at[tok] = (a, s, t)
+        tok += t
+    for l in call.launches():
+        if l["what"] == 3:
             continue
-        n, R = int(l["n"]), int(l["rows"])
-        assert R in (8, 16) and n <= 256 and l["tok0"] == tok and l["span"] % 16 == 0
+        n, R, tc = int(l["n"]), int(l["rows"]), l["what"] == 4
+        assert R in ((128, 256) if tc else (8, 16)) and 0 < n <= 256
+        assert tc or l["span"] % 16 == 0
+        assert not tc or q8 or (P % 8 == 0 and P % l["box"] == 0 and 8 <= l["box"] <= 128)
         for x in range(n):
-            a, s, t = seqs.pop(0)
+            a, s, t = at.pop(int(l["tok"][x]))
             assert (l["agent"][x], l["start"][x], l["row"][x + 1] - l["row"][x]) == (a, s, t)
+            assert not tc or t * G > 16
+            assert tc or t * G <= 16 or (not q8 and P % 8)
             tiles = -(-t * G // R)
             ns = int(l["nsplit"][x])
             assert l["base"][x + 1] - l["base"][x] == tiles * ns
-            assert ns == 1 or t == 0 or not l["direct"]
+            assert ns == 1 or not l["direct"]
             for tile in range(tiles):
-                first = s + tile * R // G
-                last = s + min(tile * R + R - 1, t * G - 1) // G
-                lo = max(0, first - window + 1) if window else 0
-                seen = last + 1 - lo + (min(sinks, lo) if window else 0)
-                assert ns * int(l["span"]) >= seen
-        tok += int(l["row"][n])
+                assert ns * int(l["span"]) >= _steps(l["what"], s, t, G, R, tile, window, sinks)
         units = int(l["base"][n]) * H * nl
         if not l["direct"]:
             assert units * R * (D + 2) <= lib.fake_floats()
         assert units < 2**31
-    while seqs and seqs[0][2] == 0:
-        seqs.pop(0)
-    assert not seqs
+    assert not at                                   # every sequence in one launch
 
 
 def test_plans_cover_every_visible_position(td, lib):
     rng = random.Random(7)
-    for _ in range(300):
+    for i in range(400):
         H, D, G = rng.choice((1, 2, 3, 8)), rng.choice((64, 128)), rng.choice((1, 2, 5, 7, 8, 16, 40))
         P, nl = rng.choice((1, 5, 8, 16, 24, 32, 256)), rng.choice((1, 2))
-        n = rng.choice((1, 2, 9, 300))
+        n = rng.choice((1, 2, 9, 300, 600))
         hi = rng.choice((1, 2, 40, 700))
         chunks = [(i % 8, rng.randint(0, rng.choice((1, 50, 20000))), rng.randint(0, hi)) for i in range(n)]
         window = rng.choice((0, 0, 1, 64, 1000))
         sinks = rng.choice((0, 4, 300))
         call = Call(td, lib, H=H, D=D, P=P, sms=rng.choice((152, 8)))
-        assert call.run("attend", chunks=chunks, nq=H * G, window=window, sinks=sinks,
-                        layers=(0, nl)) == td.TD_OK
-        if sum(c[2] for c in chunks):
-            _check_attention(td, lib, call, H, D, H * G, chunks, window, sinks, nl)
+        op = rng.choice(("attend", "attend8"))
+        assert call.run(op, chunks=chunks, nq=H * G, window=window, sinks=sinks,
+                        layers=(1, 1 + nl)) == td.TD_OK
+        _check_attention(lib, call, H, D, P, H * G, chunks, window, sinks, nl, op == "attend8")
