@@ -26,8 +26,10 @@
 // does not see, they clear the rows that none sees (their bytes may be anything) and watch for
 // infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
 // value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
-// 8-bit pages: four warps load codes, turn them into bf16 (exact) and store them as the same
-// tiles; the scale of K's row goes on the score's column, that of V's on the weight's.
+// 8-bit pages: four warps load K's codes and three V's, turn them into bf16 (exact) and store
+// them as the same tiles. The scale of K's row goes on the score's column, that of V's on the
+// weight's; powers of two (e4m3 as td_quantise_append writes it) go into the conversion
+// itself, exactly, and cost the softmax nothing.
 //
 // Every wait is bounded by the global timer; when one runs out TD_ERR_DEVICE_TIMEOUT is set
 // and all roles leave their loops, wait (bounded) for what they started and free the TMEM.
@@ -41,8 +43,9 @@ constexpr int kKv = 128;              // positions per KV tile
 constexpr int kRows = 128;            // query rows per tile
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8;
-constexpr int kLoadWarp = 9;          // bf16: TMA; 8-bit: the first of four converting warps
-constexpr int kPatchWarp = 10;        // bf16: the first of two
+constexpr int kLoadWarp = 9;          // bf16: K by TMA; V: the next warp
+constexpr int kPatchWarp = 11;
+constexpr int kConvertWarp = 12;      // 8-bit: the first of four that convert K (9-11: V)
 constexpr int kInfo = 8;              // KV tiles whose facts are kept
 
 template <int D, bool k8>
@@ -53,16 +56,22 @@ struct Plan {
   // room for more, and must take more than half of the shared memory
   static constexpr int kK = D == 64 ? 4 : (k8 ? 2 : 3);
   static constexpr int kV = D == 64 ? 4 : 2;
-  static constexpr int kThreads = k8 ? 416 : 384;
+  static constexpr int kThreads = k8 ? 512 : 384;
   // 8-bit pages: the last KV tiles' scales, two tiles' page rows
   static constexpr int kScales = k8 ? kInfo * 2 * kKv * 4 : 0;
   static constexpr int kPageRows = k8 ? 2 * kKv * 4 : 0;
   static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + 1024;
 };
 
-// Bit p of a KV tile's words: position p's page is mapped, or nobody needs it.
+// A KV tile's facts. Bit p of `valid`: position p's page is mapped, or nobody needs it.
+// `folded` (8-bit pages): the scales of word i's positions are in the converted K and V.
 struct __align__(16) Info {
   uint32_t valid[4];
+  uint32_t folded[4];
+  __device__ __forceinline__ bool all_folded() const {
+    const volatile uint32_t* v = folded;
+    return (v[0] & v[1] & v[2] & v[3]) != 0;
+  }
   __device__ __forceinline__ uint4 load() const {
     const volatile uint32_t* v = valid;
     return make_uint4(v[0], v[1], v[2], v[3]);
@@ -72,9 +81,10 @@ __device__ __forceinline__ bool no_holes(const uint4& v) { return (v.x & v.y & v
 
 struct Shared {
   uint64_t q_full, k_full[4], k_empty[4], v_raw[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_ready[2], o_done[2], drain;
+  uint64_t s_full[2], p_ready[2][2], o_done[2], drain;   // p_ready: halves of the weights
   uint32_t tmem;
   int abort, bad;
+  int box_row[2][16];    // K's and V's loader: rows of the tile's boxes
   Info info[kInfo];
 };
 static_assert(sizeof(Shared) <= 1024, "the block's bookkeeping has 1 KB");
@@ -103,7 +113,21 @@ __device__ __forceinline__ void tc_fence_before() {
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the warp's loads; the loaded registers go through it (or through tc_loaded after
+// it), so that nothing reads them earlier.
+#define TD_R8(r, i) "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), \
+                    "+r"(r[i + 4]), "+r"(r[i + 5]), "+r"(r[i + 6]), "+r"(r[i + 7])
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : TD_R8(r, 0), TD_R8(r, 8), TD_R8(r, 16), TD_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tc_loaded(uint32_t* r) {
+  asm volatile("" : TD_R8(r, 0), TD_R8(r, 8), TD_R8(r, 16), TD_R8(r, 24)::"memory");
+}
+__device__ __forceinline__ void tc_wait_ld16(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : TD_R8(r, 0), TD_R8(r, 8)::"memory");
+}
+#undef TD_R8
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
@@ -143,17 +167,14 @@ __device__ __forceinline__ void tc_ld32(uint32_t* r, uint32_t addr) {
         "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
+__device__ __forceinline__ void tc_ld16(uint32_t* r, uint32_t addr) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};"
-      ::"r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]),
-        "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]),
-        "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -163,6 +184,17 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
         "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
         "r"(r[14]), "r"(r[15])
       : "memory");
+}
+
+// One lane of the warp, always the same. The products' warp runs as one and only issues under
+// this: its addresses and descriptors stay warp-uniform, in uniform registers (issued from a
+// branch of lane 0 alone, each product cost about 100 cycles of moves, against 64 of tensor
+// work).
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+               : "=r"(p));
+  return p != 0;
 }
 
 // Shared-memory operand of 64-element (128-byte) swizzled rows: `next` = bytes between
@@ -198,6 +230,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 d;
   asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
       "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
@@ -312,30 +353,51 @@ __device__ __forceinline__ uint32_t first_bits(int n) {   // the lowest n bits
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
-// One tile's softmax for the thread's row: raises the maximum (and rescales O), writes the
-// weights over the scores and adds them to the sum. `seen`: the columns in sight, 4 words.
-template <int D, int kKind, bool kMask>
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// One tile's softmax for the thread's row: all 128 scores into registers, the maximum (and,
+// where it grew, O rescaled), the weights written over the scores and added to the sum. The
+// products may start on the first half of the weights while the second is computed: each half
+// has its barrier. `seen`: the columns in sight, 4 words.
+template <int D, bool kScaled, bool kMask>
 __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const uint32_t* seen,
                                              float scale, const float* ks, const float* vs,
                                              bool first, uint64_t* o_done, unsigned o_parity,
-                                             float& m_ref, float2& sum, Shared* sh,
-                                             uint32_t* err) {
-  constexpr bool k8 = kKind != kCacheBf16;
-  uint32_t x[32];
-  float mx = -INFINITY;
+                                             uint64_t* p_ready, float& m_ref, float2& sum,
+                                             Shared* sh, uint32_t* err) {
+  uint32_t x[4][32];
+#pragma unroll
+  for (int c = 0; c < 4; ++c) tc_ld32(x[c], t_s + c * 32);
+  tc_wait_ld(x[0]);
+#pragma unroll
+  for (int c = 1; c < 4; ++c) tc_loaded(x[c]);
+  float mx[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    tc_ld32(x, t_s + c * 32);
-    tc_wait_ld();
+    mx[c] = -INFINITY;
+    [[maybe_unused]] float4 k4;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float s = __uint_as_float(x[i]);
-      if constexpr (k8) s = __fmul_rn(s, ks[c * 32 + i]);
-      if constexpr (kMask) s = (seen[c] >> i) & 1u ? s : -INFINITY;
-      mx = fmaxf(mx, s);
+    for (int i = 0; i < 32; i += 2) {
+      if constexpr (kScaled) {
+        if (i % 4 == 0) k4 = *reinterpret_cast<const float4*>(ks + c * 32 + i);
+        const float2 v = mul2(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])),
+                              i % 4 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w));
+        x[c][i] = __float_as_uint(v.x);
+        x[c][i + 1] = __float_as_uint(v.y);
+      }
+      if constexpr (kMask) {
+        x[c][i] = (seen[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
+        x[c][i + 1] = (seen[c] >> (i + 1)) & 1u ? x[c][i + 1] : 0xFF800000u;
+      }
+      mx[c] = max3(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
     }
   }
-  const float m_tile = mx == -INFINITY ? mx : (k8 ? mx : __fmul_rn(mx, scale));
+  const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  const float m_tile = top == -INFINITY ? top : __fmul_rn(top, scale);
   const float m_new = fmaxf(m_ref, m_tile);
   if (first) {
     m_ref = m_new;
@@ -348,37 +410,33 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
     sum.y *= f;
     if (!__all_sync(0xFFFFFFFFu, wait_or_abort(o_done, o_parity, sh, err))) return false;
     tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < D / 16; ++c) {
+      uint32_t o[16];
+      tc_ld16(o, t_o + c * 16);
+      tc_wait_ld16(o);
 #pragma unroll
-    for (int c = 0; c < D / 32; ++c) {
-      tc_ld32(x, t_o + c * 32);
-      tc_wait_ld();
-#pragma unroll
-      for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-      tc_st32(t_o + c * 32, x);
+      for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+      tc_st16(t_o + c * 16, o);
     }
   }
   const float nm = m_ref == -INFINITY ? 0.0f : -m_ref;
   const float2 nm2 = make_float2(nm, nm), sc2 = make_float2(scale, scale);
+  float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
-    tc_ld32(x, t_s + c * 32);
-    tc_wait_ld();
     uint32_t p[16];
+    [[maybe_unused]] float4 v4;
 #pragma unroll
     for (int i = 0; i < 32; i += 2) {
-      float2 s = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-      if constexpr (k8) s = fma2(s, *reinterpret_cast<const float2*>(ks + c * 32 + i), nm2);
-      else s = fma2(s, sc2, nm2);
+      float2 s = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+      s = fma2(s, sc2, nm2);
       float2 w = make_float2(ex2(s.x), ex2(s.y));
-      if constexpr (kMask) {
-        w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
-        w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
-      }
-      sum = add2(sum, w);
-      if constexpr (k8) {
-        const float2 v = *reinterpret_cast<const float2*>(vs + c * 32 + i);
-        w.x = __fmul_rn(w.x, v.x);
-        w.y = __fmul_rn(w.y, v.y);
+      if (c & 1) sum = add2(sum, w);
+      else part = add2(part, w);
+      if constexpr (kScaled) {
+        if (i % 4 == 0) v4 = *reinterpret_cast<const float4*>(vs + c * 32 + i);
+        w = mul2(w, i % 4 == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
         if constexpr (kMask) {      // a scale out of sight may be a NaN
           w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
           w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
@@ -387,8 +445,14 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
       p[i / 2] = pack_bf2(w.x, w.y);
     }
     tc_st16(t_s + c * 16, p);
+    if (c & 1) {
+      tc_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if ((threadIdx.x & 31) == 0) mbar_arrive(p_ready + (c >> 1));
+    }
   }
-  tc_wait_st();
+  sum = add2(sum, part);
   return true;
 }
 
@@ -466,7 +530,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   extern __shared__ unsigned char s_dyn[];
   pdl_wait();
   const Work w = work_of(A, list, units);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);    // known to be the warp's
   if (w.n <= 0) {           // a part past the visible positions of its rows: empty
     for (int rr = tid; rr < w.nrows; rr += PL::kThreads) {
       A.part_ml[(w.unit * A.rows_cta + rr) * 2] = -INFINITY;
@@ -491,12 +556,13 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     }
     for (int i = 0; i < PL::kV; ++i) {
       mbar_init(&sh->v_raw[i], 1);
-      mbar_init(&sh->v_full[i], k8 ? 128 : 2);
+      mbar_init(&sh->v_full[i], k8 ? 96 : 1);
       mbar_init(&sh->v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->p_ready[i], 4);
+      mbar_init(&sh->p_ready[i][0], 4);
+      mbar_init(&sh->p_ready[i][1], 4);
       mbar_init(&sh->o_done[i], 1);
     }
     mbar_init(&sh->drain, 1);
@@ -514,6 +580,16 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh->tmem);
 
+  // registers: from the warps that only start copies and products to the softmax (the shares
+  // add up to the launch's: 256 x 200 + 128 x 104 = 384 x 168, and for 8-bit pages
+  // 256 x 168 + 256 x 88 = 512 x 128)
+  if constexpr (!k8) {
+    if (warp < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+  } else {
+    if (warp < kSoftmaxWarps) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+  }
   if (warp < kSoftmaxWarps) {
     // ------------------------------------------------------------------ softmax
     const int wg = warp >> 2;
@@ -522,20 +598,32 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       {  // the query tile, rows past the last one zero; a negative scale turns the query's sign
         const uint32_t flip = A.scale_log2 < 0.0f ? 0x80008000u : 0u;
         unsigned char* dst = s_q + wg * (PL::kQ / 2);
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const int v = t + i * 128;
-          const int r = v / (D / 8), c = v % (D / 8);
-          uint4 val = make_uint4(0u, 0u, 0u, 0u);
-          if (wg * kRows + r < w.nrows) {
-            val = ldg16(A.q + out_row(A, list, w, w.r0 + wg * kRows + r) * D + c * 8);
-            val.x ^= flip;
-            val.y ^= flip;
-            val.z ^= flip;
-            val.w ^= flip;
+        constexpr int kVec = D / 8, kStep = kRows / kVec;     // a thread's rows are kStep apart
+        const int c = t % kVec;
+        int r = w.r0 + wg * kRows + t / kVec;
+        int tok = r / A.G, g = r - tok * A.G;
+        const int dt = kStep / A.G, dg = kStep - dt * A.G;
+        const uint16_t* src =
+            A.q + ((static_cast<int64_t>(w.li) * A.tokens + list.tok[w.x]) * A.nq + w.h * A.G) * D +
+            c * 8;
+        uint4 val[kVec];
+#pragma unroll
+        for (int i = 0; i < kVec; ++i) {
+          val[i] = r < w.r0 + w.nrows
+                       ? ldg16(src + (static_cast<int64_t>(tok) * A.nq + g) * D)
+                       : make_uint4(0u, 0u, 0u, 0u);
+          r += kStep;
+          tok += dt;
+          g += dg;
+          if (g >= A.G) {
+            g -= A.G;
+            ++tok;
           }
-          *reinterpret_cast<uint4*>(dst + tile_at(r, c)) = val;
         }
+#pragma unroll
+        for (int i = 0; i < kVec; ++i)
+          *reinterpret_cast<uint4*>(dst + tile_at(t / kVec + i * kStep, c)) =
+              make_uint4(val[i].x ^ flip, val[i].y ^ flip, val[i].z ^ flip, val[i].w ^ flip);
         fence_async_smem();
         mbar_arrive(&sh->q_full);
       }
@@ -547,7 +635,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const int pl = w.start + (w.r0 + min(wg * kRows + kRows, w.nrows) - 1) / A.G;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
       const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + 2 * kKv + wg * D;
-      const float scale = fabsf(A.scale_log2);
+      // (never 0, which would turn the -infinity of a masked score into a NaN)
+      const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f);
       float m_ref = -INFINITY;
       float2 sum = make_float2(0.0f, 0.0f);
       bool ok = true;
@@ -559,6 +648,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         const int kt = w.tile(j);
         const uint4 valid = sh->info[j % kInfo].load();
         const float* ks = s_scale + (j % kInfo) * 2 * kKv;
+        const bool scaled = k8 && !sh->info[j % kInfo].all_folded();
         if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
           const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
           uint32_t seen[4];
@@ -569,16 +659,21 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             if (w.window) b &= ~first_bits(hi - w.window + 1 - c * 32) | first_bits(sk - c * 32);
             seen[c] = b & in[c];
           }
-          ok = softmax_tile<D, kKind, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
-                                            &sh->o_done[wg], (j - 1) & 1, m_ref, sum, sh, A.err);
+          ok = scaled ? softmax_tile<D, k8, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
+                                                  &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
+                                                  m_ref, sum, sh, A.err)
+                      : softmax_tile<D, false, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
+                                                     &sh->o_done[wg], (j - 1) & 1,
+                                                     sh->p_ready[wg], m_ref, sum, sh, A.err);
         } else {
-          ok = softmax_tile<D, kKind, false>(t_s, t_o, nullptr, scale, ks, ks + kKv, j == 0,
-                                             &sh->o_done[wg], (j - 1) & 1, m_ref, sum, sh, A.err);
+          ok = scaled ? softmax_tile<D, k8, false>(t_s, t_o, nullptr, scale, ks, ks + kKv, j == 0,
+                                                   &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
+                                                   m_ref, sum, sh, A.err)
+                      : softmax_tile<D, false, false>(t_s, t_o, nullptr, scale, ks, ks + kKv,
+                                                      j == 0, &sh->o_done[wg], (j - 1) & 1,
+                                                      sh->p_ready[wg], m_ref, sum, sh, A.err);
         }
         if (!ok) break;
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_ready[wg]);
       }
       if (ok)
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->o_done[wg], (w.n - 1) & 1, sh, A.err));
@@ -592,7 +687,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
             tc_ld32(x, t_o + c * 32);
-            tc_wait_ld();
+            tc_wait_ld(x);
             if (live) {
 #pragma unroll
               for (int i = 0; i < 4; ++i) {
@@ -611,7 +706,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
             tc_ld32(x, t_o + c * 32);
-            tc_wait_ld();
+            tc_wait_ld(x);
             if (live) {
 #pragma unroll
               for (int i = 0; i < 8; ++i)
@@ -629,183 +724,217 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- the products
-    if (lane == 0) {
-      const uint32_t q_addr = smem_u32(s_q), k_addr = smem_u32(s_k), v_addr = smem_u32(s_v);
-      constexpr uint32_t id_s = tc_idesc(kKv, false), id_o = tc_idesc(D, true);
-      auto scores = [&](int wg, int slot) {
+    constexpr uint32_t id_s = tc_idesc(kKv, false), id_o = tc_idesc(D, true);
+    const uint64_t q_desc = tc_desc(smem_u32(s_q), 16), k_desc = tc_desc(smem_u32(s_k), 16);
+    const uint64_t v_desc = tc_desc(smem_u32(s_v), 128 * 128);
+    // (a descriptor counts addresses in 16 bytes)
+    auto scores = [&](int wg, int slot, bool last) {
+      if (elected()) {
+        const uint64_t a = q_desc + wg * (PL::kQ / 2 / 16), b = k_desc + slot * (PL::kTile / 16);
 #pragma unroll
         for (int kc = 0; kc < D / 16; ++kc) {
-          const uint32_t off = (kc >> 2) * (128 * 128) + (kc & 3) * 32;
-          tc_mma_ss(tmem + wg * kKv, tc_desc(q_addr + wg * (PL::kQ / 2) + off, 16),
-                    tc_desc(k_addr + slot * PL::kTile + off, 16), id_s, kc > 0);
+          const uint32_t off = ((kc >> 2) * (128 * 128) + (kc & 3) * 32) / 16;
+          tc_mma_ss(tmem + wg * kKv, a + off, b + off, id_s, kc > 0);
         }
         tc_commit(&sh->s_full[wg]);
-      };
-      bool ok = wait_or_abort(&sh->q_full, 0, sh, A.err) &&
-                wait_or_abort(&sh->k_full[0], 0, sh, A.err);
-      if (ok) {
-        tc_fence_after();
-        scores(0, 0);
-        if (two) scores(1, 0);
-        tc_commit(&sh->k_empty[0]);
+        if (last) tc_commit(&sh->k_empty[slot]);
       }
-      for (int j = 0; ok && j < w.n; ++j) {
-        const int vs = j % PL::kV, ks = (j + 1) % PL::kK;
-        for (int wg = 0; wg < (two ? 2 : 1); ++wg) {
-          ok = wait_or_abort(&sh->p_ready[wg], j & 1, sh, A.err);
-          if (ok && wg == 0) ok = wait_or_abort(&sh->v_full[vs], (j / PL::kV) & 1, sh, A.err);
+      __syncwarp();
+    };
+    const int last = two ? 1 : 0;
+    bool ok = wait_or_abort(&sh->q_full, 0, sh, A.err) &&
+              wait_or_abort(&sh->k_full[0], 0, sh, A.err);
+    ok = __all_sync(0xFFFFFFFFu, ok);
+    if (ok) {
+      tc_fence_after();
+      scores(0, 0, !two);
+      if (two) scores(1, 0, true);
+    }
+    int ks = 0, k_par = 0, vs = 0, v_par = 0;     // slots and the parities of their phases
+    for (int j = 0; ok && j < w.n; ++j) {
+      if (++ks == PL::kK) {
+        ks = 0;
+        k_par ^= 1;
+      }
+      for (int wg = 0; wg <= last; ++wg) {
+        if (wg == 0) ok = wait_or_abort(&sh->v_full[vs], v_par, sh, A.err);
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          ok = ok && wait_or_abort(&sh->p_ready[wg][half], j & 1, sh, A.err);
+          ok = __all_sync(0xFFFFFFFFu, ok);
           if (!ok) break;
           tc_fence_after();
+          if (elected()) {
+            const uint64_t b = v_desc + vs * (PL::kTile / 16);
 #pragma unroll
-          for (int kc = 0; kc < kKv / 16; ++kc)
-            tc_mma_ts(tmem + 2 * kKv + wg * D, tmem + wg * kKv + kc * 8,
-                      tc_desc(v_addr + vs * PL::kTile + kc * 2048, 128 * 128), id_o,
-                      j > 0 || kc > 0);
-          tc_commit(&sh->o_done[wg]);
-          if (wg == (two ? 1 : 0)) tc_commit(&sh->v_empty[vs]);
-          if (j + 1 < w.n) {
-            if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], ((j + 1) / PL::kK) & 1, sh, A.err);
-            if (!ok) break;
-            tc_fence_after();
-            scores(wg, ks);
-            if (wg == (two ? 1 : 0)) tc_commit(&sh->k_empty[ks]);
+            for (int kc = half * 4; kc < half * 4 + 4; ++kc)
+              tc_mma_ts(tmem + 2 * kKv + wg * D, tmem + wg * kKv + kc * 8, b + kc * (2048 / 16),
+                        id_o, j > 0 || kc > 0);
+            if (half == 1) {
+              tc_commit(&sh->o_done[wg]);
+              if (wg == last) tc_commit(&sh->v_empty[vs]);
+            }
           }
+          __syncwarp();
+        }
+        if (!ok) break;
+        if (j + 1 < w.n) {
+          if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], k_par, sh, A.err);
+          ok = __all_sync(0xFFFFFFFFu, ok);
+          if (!ok) break;
+          tc_fence_after();
+          scores(wg, ks, wg == last);
         }
       }
-      // whatever was started has ended before the TMEM goes
-      tc_commit(&sh->drain);
-      mbar_wait_bounded(&sh->drain, 0);
+      if (++vs == PL::kV) {
+        vs = 0;
+        v_par ^= 1;
+      }
     }
+    // whatever was started has ended before the TMEM goes
+    if (elected()) tc_commit(&sh->drain);
     __syncwarp();
+    mbar_wait_bounded(&sh->drain, 0);
   } else if constexpr (!k8) {
-    if (warp == kLoadWarp) {
-      // ------------------------------------------------------------- K and V by TMA
+    if (warp < kPatchWarp) {
+      // ------------------------------------- K (first warp) or V (second) by TMA
+      const bool is_v = warp != kLoadWarp;
       const PoolDev& P = A.pool;
-      const int box = A.box_rows, per = kKv / box;       // boxes per 64 dims
-      const int nbox = per * (D / 64);
-      const int plane = 2 * w.li * static_cast<int>(P.num_pages * P.P);
+      const int box = A.box_rows, per = kKv / box;        // boxes per 64 dims
       const int vplane = static_cast<int>(P.num_pages * P.P);
-      bool ok = true;
-      int n_k = 0, n_v = 0;                               // tiles started
-      for (int j = 0; j < w.n; ++j) {
-        const int kt = w.tile(j);
-        const int b = lane;                               // at most 32 boxes a tile
-        const int rb = b % per, half = b / per;
-        const int pos = kt * kKv + rb * box;
-        const bool need = b < nbox && w.needed(pos, pos + box - 1);
-        int row = -1;
-        if (need) {
-          const int page = page_of(P, list.agent[w.x], pos);
-          if (page >= 0) row = plane + page * P.P + pos % P.P;
-          else atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
-        }
-        const uint32_t holes = __ballot_sync(0xFFFFFFFFu, need && row < 0 && half == 0);
-        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0)) * box * 128u;
-        const int ks = j % PL::kK, vs = j % PL::kV;
-        if (j >= PL::kK) ok = wait_or_abort(&sh->k_empty[ks], ((j / PL::kK) - 1) & 1, sh, A.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
+      const int plane = 2 * w.li * vplane + (is_v ? vplane : 0);
+      const int slots = is_v ? PL::kV : PL::kK;
+      const uint32_t ring = smem_u32(is_v ? s_v : s_k);
+      uint64_t* full = is_v ? sh->v_raw : sh->k_full;
+      uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
+      // lane b < per looks up box b of tile j: its row, -1 not needed, -2 unmapped
+      auto lookup = [&](int j) {
+        if (j >= w.n || lane >= per) return -1;
+        const int pos = w.tile(j) * kKv + lane * box;
+        if (!w.needed(pos, pos + box - 1)) return -1;
+        const int page = page_of(P, list.agent[w.x], pos);
+        return page < 0 ? -2 : plane + page * P.P + pos % P.P;
+      };
+      int slot = 0, parity = 1, n = 0;                    // n: tiles started
+      int row = lookup(0);
+      for (; n < w.n; ++n) {
+        const int next = lookup(n + 1);
+        const uint32_t holes = __ballot_sync(0xFFFFFFFFu, row == -2);
+        const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0)) * box * (D * 2u);
+        if (holes && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+        if (n >= slots &&
+            !__all_sync(0xFFFFFFFFu, wait_or_abort(&empty[slot], parity, sh, A.err)))
+          break;
+        // (both warps write a tile's facts, the same ones: each before its own barrier)
         if (lane < 4) {
           uint32_t v = 0xFFFFFFFFu;
           if (holes)
             for (int i = 0; i < 32; ++i)
               if ((holes >> ((lane * 32 + i) / box)) & 1u) v &= ~(1u << i);
-          sh->info[j % kInfo].valid[lane] = v;
+          sh->info[n % kInfo].valid[lane] = v;
+        }
+        int* rows = sh->box_row[is_v];
+        if (lane < 16) rows[lane] = row;
+        __syncwarp();
+        if (elected()) {
+          mbar_arrive_expect_tx(&full[slot], bytes + A.tx_pad);
+          const uint32_t dst = ring + slot * PL::kTile;
+          for (int b = 0; b < per; ++b) {
+            const int r = rows[b];
+            if (r < 0) continue;
+#pragma unroll
+            for (int half = 0; half < D / 64; ++half)
+              tma_box(dst + half * (128 * 128) + b * box * 128, &map, w.h * D + half * 64, r,
+                      &full[slot]);
+          }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive_expect_tx(&sh->k_full[ks], bytes + A.tx_pad);
-        __syncwarp();
-        const uint32_t off = half * (128 * 128) + rb * box * 128;
-        if (row >= 0)
-          tma_box(smem_u32(s_k) + ks * PL::kTile + off, &map, w.h * D + half * 64, row,
-                  &sh->k_full[ks]);
-        ++n_k;
-        if (j >= PL::kV) ok = wait_or_abort(&sh->v_empty[vs], ((j / PL::kV) - 1) & 1, sh, A.err);
-        ok = __all_sync(0xFFFFFFFFu, ok);
-        if (!ok) break;
-        if (lane == 0) mbar_arrive_expect_tx(&sh->v_raw[vs], bytes + A.tx_pad);
-        __syncwarp();
-        if (row >= 0)
-          tma_box(smem_u32(s_v) + vs * PL::kTile + off, &map, w.h * D + half * 64, row + vplane,
-                  &sh->v_raw[vs]);
-        ++n_v;
+        row = next;
+        if (++slot == slots) {
+          slot = 0;
+          parity ^= 1;
+        }
       }
       // the copies that were started land before the block goes, time-out or not
-      for (int i = max(0, n_k - PL::kK); i < n_k; ++i)
-        mbar_wait_bounded(&sh->k_full[i % PL::kK], (i / PL::kK) & 1);
-      for (int i = max(0, n_v - PL::kV); i < n_v; ++i)
-        mbar_wait_bounded(&sh->v_raw[i % PL::kV], (i / PL::kV) & 1);
+      for (int i = max(0, n - slots); i < n; ++i)
+        mbar_wait_bounded(&full[i % slots], (i / slots) & 1);
     } else {
       // ----------------------------------------------- V tiles patched where they must be
-      const int t = tid - kPatchWarp * 32;
+      int slot = 0, parity = 0;
       for (int j = 0; j < w.n; ++j) {
-        const int vs = j % PL::kV, kt = w.tile(j);
-        const bool ok = wait_or_abort(&sh->v_raw[vs], (j / PL::kV) & 1, sh, A.err);
-        if (!__all_sync(0xFFFFFFFFu, ok)) break;
+        const int t0 = w.tile(j) * kKv;
+        if (!__all_sync(0xFFFFFFFFu, wait_or_abort(&sh->v_raw[slot], parity, sh, A.err))) break;
         const uint4 in = sh->info[j % kInfo].load();
-        if (!w.whole(kt, w.p_first, w.p_last) || !no_holes(in)) {
-          unsigned char* tile = s_v + vs * PL::kTile;
+        if (!w.whole(w.tile(j), w.p_first, w.p_last) || !no_holes(in)) {
+          unsigned char* tile = s_v + slot * PL::kTile;
           bool bad = false;
-#pragma unroll 4
-          for (int i = t; i < kKv * (D / 8); i += 64) {
-            const int r = i / (D / 8), c = i % (D / 8);
-            const int pos = kt * kKv + r;
-            uint4* at = reinterpret_cast<uint4*>(tile + tile_at(r, c));
+          // a row a lane at a time: rows in every query row's sight stay, rows in nobody's
+          // (or of no page) are cleared, the others are looked through
+          for (int r = lane; r < kKv; r += 32) {
+            const int p = t0 + r;
             const uint32_t word = r < 64 ? (r < 32 ? in.x : in.y) : (r < 96 ? in.z : in.w);
-            if (!w.needed(pos, pos) || !((word >> (r & 31)) & 1u)) {
-              *at = make_uint4(0u, 0u, 0u, 0u);
+            const bool have = w.needed(p, p) && ((word >> lane) & 1u);
+            if (have && p <= w.p_first &&
+                (w.window == 0 || p > w.p_last - w.window || p < w.n_sink))
               continue;
-            }
-            uint4 v = *at;
-            uint32_t* u = reinterpret_cast<uint32_t*>(&v);
-            bool hit = false;
+            uint32_t top = 0;     // the largest magnitudes of the halves, as bits
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              if ((u[e] & 0x7F80u) == 0x7F80u) {
-                u[e] &= 0xFFFF0000u;
-                hit = true;
-              }
-              if ((u[e] & 0x7F800000u) == 0x7F800000u) {
-                u[e] &= 0x0000FFFFu;
-                hit = true;
+            for (int c = 0; c < D / 8; ++c) {
+              uint4* at = reinterpret_cast<uint4*>(tile + tile_at(r, c));
+              if (have) {
+                const uint4 v = *at;
+                top = __vmaxu2(__vmaxu2(top, __vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu)),
+                               __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+              } else {
+                *at = make_uint4(0u, 0u, 0u, 0u);
               }
             }
-            if (hit) *at = v;
-            bad |= hit;
+            if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) continue;
+            bad = true;           // (the slow rows read the pages: the tile's row may go)
+#pragma unroll
+            for (int c = 0; c < D / 8; ++c)
+              *reinterpret_cast<uint4*>(tile + tile_at(r, c)) = make_uint4(0u, 0u, 0u, 0u);
           }
           if (bad) *reinterpret_cast<volatile int*>(&sh->bad) = 1;
           fence_async_smem();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->v_full[vs]);
+        if (lane == 0) mbar_arrive(&sh->v_full[slot]);
+        if (++slot == PL::kV) {
+          slot = 0;
+          parity ^= 1;
+        }
       }
     }
   } else {
-    // --------------------------------------------------------- K and V from 8-bit codes
-    const int t = tid - kLoadWarp * 32;                   // 0 .. 127: a position of each tile
-    constexpr int kVec = D / 16;                          // 16-byte vectors per row
+    // ------------------------- K and V from 8-bit codes: warps 12-15 make K, 9-11 V
+    const bool is_v = warp < kConvertWarp;
+    const int t = is_v ? tid - kLoadWarp * 32 : tid - kConvertWarp * 32;
+    constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
+    constexpr int kMost = (kKv * kVec + 95) / 96;         // per thread, of V's 96
+    const int threads = is_v ? 96 : 128;
     const PoolDev& P = A.pool;
     const int64_t half = P.num_pages * P.P;
     const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * half;
-    const float kmul = fabsf(A.scale_log2);
-    // position t's page row of tile j: -1 not needed, -2 unmapped
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(P.base) +
+                         (plane + (is_v ? half : 0)) * A.g.E + w.h * D;
+    // K's threads look the positions up, one each: -1 not needed, -2 unmapped
     auto lookup = [&](int j) {
-      if (j >= w.n) return -1;
+      if (is_v || j >= w.n) return -1;
       const int pos = w.tile(j) * kKv + t;
       if (!w.needed(pos, pos)) return -1;
       const int page = page_of(P, list.agent[w.x], pos);
       return page < 0 ? -2 : page * P.P + pos % P.P;
     };
-    uint4 code[2][kVec];
-    auto load = [&](int kv, int j) {      // kVec threads a row, 128 / kVec rows a step
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(P.base) + (plane + kv * half) * A.g.E +
-                           w.h * D + (t % kVec) * 16;
+    uint4 code[kMost];
+    auto load = [&](int j) {
 #pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        const int row = s_rows[(j & 1) * kKv + i * (kKv / kVec) + t / kVec];
-        code[kv][i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                              : __ldg(reinterpret_cast<const uint4*>(
-                                    src + static_cast<int64_t>(row) * A.g.E));
+      for (int i = 0; i < kMost; ++i) {
+        const int v = t + i * threads;
+        const int row = v < kKv * kVec ? s_rows[(j & 1) * kKv + v / kVec] : -1;
+        code[i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
+                          : __ldg(reinterpret_cast<const uint4*>(
+                                src + static_cast<int64_t>(row) * A.g.E + (v % kVec) * 16));
       }
     };
     float ks = 0.0f, vs = 0.0f;
@@ -813,48 +942,71 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       ks = row < 0 ? 0.0f : __ldg(A.scale + (plane + row) * A.g.H + w.h);
       vs = row < 0 ? 0.0f : __ldg(A.scale + (plane + half + row) * A.g.H + w.h);
     };
-    auto group_sync = [] { asm volatile("bar.sync 1, 128;" ::: "memory"); };
+    auto group_sync = [] { asm volatile("bar.sync 1, 224;" ::: "memory"); };
+    // a scale that goes into the conversion's own factor: a power of two of at most 2^7
+    // (every scale that td_quantise_append writes for e4m3), or that of an absent row
+    auto folds = [](float s) {
+      return (__float_as_uint(s) & 0x007FFFFFu) == 0 && s >= 0.0f && s <= 128.0f;
+    };
     int row = lookup(0), next = lookup(1);
-    s_rows[t] = row;
+    if (!is_v) s_rows[t] = row;
     group_sync();
-    load(0, 0);
-    load(1, 0);
+    load(0);
     load_scales(row);
+    const int slots = is_v ? PL::kV : PL::kK;
+    uint64_t* full = is_v ? sh->v_full : sh->k_full;
+    uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
+    int slot = 0, parity = 1;
     bool ok = true;                       // after a time-out the group still meets its barriers
     for (int j = 0; j < w.n; ++j) {
-      const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
-      if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
-      if (lane == 0) sh->info[j % kInfo].valid[t >> 5] = ~hole;
-      s_scale[(j % kInfo) * 2 * kKv + t] = __fmul_rn(ks, kmul);
-      s_scale[(j % kInfo) * 2 * kKv + kKv + t] = vs;
-      row = next;
-      s_rows[((j + 1) & 1) * kKv + t] = row;
+      Info& info = sh->info[j % kInfo];
+      float* scales = s_scale + (j % kInfo) * 2 * kKv;
+      if (!is_v) {
+        const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
+        const bool fold = kKind == kCacheE4m3 &&
+                          __all_sync(0xFFFFFFFFu, folds(ks) && folds(vs));
+        if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+        if (lane == 0) {
+          info.valid[t >> 5] = ~hole;
+          info.folded[t >> 5] = fold;
+        }
+        scales[t] = ks;
+        scales[kKv + t] = vs;
+        row = next;
+        s_rows[((j + 1) & 1) * kKv + t] = row;
+      }
       group_sync();
       next = lookup(j + 2);
       load_scales(row);
+      if (ok && j >= slots) ok = wait_or_abort(&empty[slot], parity, sh, A.err);
+      if (ok) {
+        unsigned char* tile = (is_v ? s_v : s_k) + slot * PL::kTile;
+        const bool fold = kKind == kCacheE4m3 && info.all_folded();
 #pragma unroll
-      for (int kv = 0; kv < 2; ++kv) {
-        const int slots = kv ? PL::kV : PL::kK, slot = j % slots;
-        if (ok && j >= slots)
-          ok = wait_or_abort(kv ? &sh->v_empty[slot] : &sh->k_empty[slot], ((j / slots) - 1) & 1,
-                             sh, A.err);
-        if (ok) {
-          unsigned char* tile = (kv ? s_v : s_k) + slot * PL::kTile;
-#pragma unroll
-          for (int i = 0; i < kVec; ++i) {
-            const int r = i * (kKv / kVec) + t / kVec, c = (t % kVec) * 2;
-            const uint4 v = code[kv][i];
-            *reinterpret_cast<uint4*>(tile + tile_at(r, c)) =
-                make_uint4(word_bf16<kKind, false>(v.x), word_bf16<kKind, true>(v.x),
-                           word_bf16<kKind, false>(v.y), word_bf16<kKind, true>(v.y));
-            *reinterpret_cast<uint4*>(tile + tile_at(r, c + 1)) =
-                make_uint4(word_bf16<kKind, false>(v.z), word_bf16<kKind, true>(v.z),
-                           word_bf16<kKind, false>(v.w), word_bf16<kKind, true>(v.w));
+        for (int i = 0; i < kMost; ++i) {
+          const int v = t + i * threads;
+          if (v >= kKv * kVec) continue;
+          const int r = v / kVec, c = (v % kVec) * 2;
+          uint32_t f = kE4m3Factor;
+          if (fold) {
+            f = __float_as_uint(scales[(is_v ? kKv : 0) + r] * 0x1p120f) >> 16;
+            f |= f << 16;
           }
-          fence_async_smem();
-          mbar_arrive(kv ? &sh->v_full[slot] : &sh->k_full[slot]);
+          const uint4 q = code[i];
+          *reinterpret_cast<uint4*>(tile + tile_at(r, c)) =
+              make_uint4(word_bf16<kKind, false>(q.x, f), word_bf16<kKind, true>(q.x, f),
+                         word_bf16<kKind, false>(q.y, f), word_bf16<kKind, true>(q.y, f));
+          *reinterpret_cast<uint4*>(tile + tile_at(r, c + 1)) =
+              make_uint4(word_bf16<kKind, false>(q.z, f), word_bf16<kKind, true>(q.z, f),
+                         word_bf16<kKind, false>(q.w, f), word_bf16<kKind, true>(q.w, f));
         }
-        load(kv, j + 1);
+        fence_async_smem();
+        mbar_arrive(&full[slot]);
+      }
+      load(j + 1);
+      if (++slot == slots) {
+        slot = 0;
+        parity ^= 1;
       }
     }
   }
