@@ -57,9 +57,10 @@ struct Plan {
   static constexpr int kK = D == 64 ? 4 : (k8 ? 2 : 3);
   static constexpr int kV = D == 64 ? 4 : 2;
   static constexpr int kThreads = k8 ? 512 : 384;
-  // 8-bit pages: the last KV tiles' scales, two tiles' page rows
+  // 8-bit pages: the last KV tiles' scales, four tiles' page rows (a thread may write those of
+  // tile j + 2 while another still reads tile j's)
   static constexpr int kScales = k8 ? kInfo * 2 * kKv * 4 : 0;
-  static constexpr int kPageRows = k8 ? 2 * kKv * 4 : 0;
+  static constexpr int kPageRows = k8 ? 4 * kKv * 4 : 0;
   static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + 1024;
 };
 
@@ -84,7 +85,7 @@ struct Shared {
   uint64_t s_full[2], p_ready[2][2], o_done[2], drain;   // p_ready: halves of the weights
   uint32_t tmem;
   int abort, bad;
-  int box_row[2][16];    // K's and V's loader: rows of the tile's boxes
+  alignas(16) int box_row[2][16];    // K's and V's loader: rows of the tile's boxes
   Info info[kInfo];
 };
 static_assert(sizeof(Shared) <= 1024, "the block's bookkeeping has 1 KB");
@@ -277,8 +278,15 @@ struct Work {
   int i0, n;                    // the part: KV tiles i0 .. i0 + n - 1 of that list
   int window, n_sink;
 
+  // the part's j-th tile: under a window from the middle on, then the first ones, since those
+  // at the ends are masked and their V is patched, which takes a tile's time
   __device__ __forceinline__ int tile(int j) const {
-    const int i = i0 + j;
+    int i = j;
+    if (window) {
+      i += n >> 1;
+      if (i >= n) i -= n;
+    }
+    i += i0;
     return i < s_tiles ? i : t_lo + i - s_tiles;
   }
   // every row of tokens at positions pf .. pl sees all positions of the tile
@@ -333,11 +341,24 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& lis
   return w;
 }
 
-__device__ __forceinline__ int page_of(const PoolDev& P, int agent, int pos) {
+// A position's page, read ahead of its use: the table's entry (kNoPage: not looked up) and the
+// slot in the page.
+constexpr int kNoPage = INT32_MIN;
+struct PageRef {
+  int page, slot;
+  // page * P + slot; -1 where it was not looked up, -2 where it is unmapped
+  __device__ __forceinline__ int row(const PoolDev& P) const {
+    if (page == kNoPage) return -1;
+    return page < 0 || page >= P.num_pages ? -2 : page * P.P + slot;
+  }
+};
+__device__ __forceinline__ PageRef page_ref(const PoolDev& P, int agent, int pos, bool need) {
+  PageRef f;
   const int lp = P.p_shift >= 0 ? (pos >> P.p_shift) : pos / P.P;
-  int32_t page = -1;
-  if (lp < P.max_lp) page = __ldg(P.bt + static_cast<int64_t>(agent) * P.max_lp + lp);
-  return page >= 0 && page < P.num_pages ? page : -1;
+  f.slot = pos - lp * P.P;
+  f.page = !need ? kNoPage : -1;
+  if (need && lp < P.max_lp) f.page = __ldg(P.bt + static_cast<int64_t>(agent) * P.max_lp + lp);
+  return f;
 }
 
 // Output row (or partial) addresses of query row r (within the sequence).
@@ -456,6 +477,141 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
   return true;
 }
 
+// The K tiles (128 threads) or V tiles (96) of a CTA, from 8-bit codes. K's threads also look
+// the positions up, one each, and publish the tile's facts and scales.
+template <int D, int kKind, bool kV>
+__device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkList& list,
+                                              const Work& w, int t, unsigned char* ring,
+                                              float* s_scale, int* s_rows, Shared* sh) {
+  using PL = Plan<D, true>;
+  constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
+  constexpr int kThreads = kV ? 96 : 128;
+  constexpr int kAll = kKv * kVec;
+  // vectors are taken four a thread at a time, the next four on their way meanwhile; the loop
+  // over the groups stays a loop (unrolled, the two converters and the softmax together ran
+  // out of the instruction cache)
+  constexpr int kGroups = (kAll + 4 * kThreads - 1) / (4 * kThreads);
+  constexpr int kSlots = kV ? PL::kV : PL::kK;
+  const int lane = t & 31;
+  const PoolDev& P = A.pool;
+  const int64_t half = P.num_pages * P.P;
+  const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * half;
+  const uint8_t* src = reinterpret_cast<const uint8_t*>(P.base) +
+                       (plane + (kV ? half : 0)) * A.g.E + w.h * D;
+  uint64_t* full = kV ? sh->v_full : sh->k_full;
+  uint64_t* empty = kV ? sh->v_empty : sh->k_empty;
+  auto lookup = [&](int j) {
+    const int pos = w.tile(min(j, w.n - 1)) * kKv + t;
+    return page_ref(P, list.agent[w.x], pos, j < w.n && w.needed(pos, pos));
+  };
+  uint4 code[4];
+  auto load = [&](int j, int group) {
+    int row[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int v = t + (group * 4 + i) * kThreads;
+      row[i] = v < kAll ? s_rows[(j & 3) * kKv + v / kVec] : -1;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      code[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (row[i] >= 0)
+        code[i] = __ldg(reinterpret_cast<const uint4*>(
+            src + static_cast<int64_t>(row[i]) * A.g.E + (t % kVec) * 16));
+    }
+  };
+  float ks = 0.0f, vs = 0.0f;
+  auto load_scales = [&](int row) {
+    ks = vs = 0.0f;
+    if (row >= 0) {
+      ks = __ldg(A.scale + (plane + row) * A.g.H + w.h);
+      vs = __ldg(A.scale + (plane + half + row) * A.g.H + w.h);
+    }
+  };
+  auto group_sync = [] { asm volatile("bar.sync 1, 224;" ::: "memory"); };
+  // a scale that goes into the conversion's own factor: a power of two of at most 2^7 (as
+  // td_quantise_append writes e4m3's for rows up to 448 * 2^7), or that of an absent row
+  auto folds = [](float s) {
+    return (__float_as_uint(s) & 0x007FFFFFu) == 0 && s >= 0.0f && s <= 128.0f;
+  };
+  int row = -1;
+  PageRef next{kNoPage, 0};
+  if constexpr (!kV) {
+    row = lookup(0).row(P);
+    s_rows[t] = row;
+    next = lookup(1);
+  }
+  group_sync();
+  load(0, 0);
+  if constexpr (!kV) load_scales(row);
+  int slot = 0, parity = 1;
+  bool ok = true;                         // after a time-out the group still meets its barriers
+  for (int j = 0; j < w.n; ++j) {
+    Info& info = sh->info[j % kInfo];
+    float* scales = s_scale + (j % kInfo) * 2 * kKv;
+    if constexpr (!kV) {
+      const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
+      const bool fold = kKind == kCacheE4m3 && __all_sync(0xFFFFFFFFu, folds(ks) && folds(vs));
+      if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+      if (lane == 0) {
+        info.valid[t >> 5] = ~hole;
+        info.folded[t >> 5] = fold;
+      }
+      scales[t] = ks;
+      scales[kKv + t] = vs;
+      row = next.row(P);
+      s_rows[((j + 1) & 3) * kKv + t] = row;
+    }
+    group_sync();
+    if constexpr (!kV) {
+      next = lookup(j + 2);
+      load_scales(row);
+    }
+    if (ok && j >= kSlots) ok = wait_or_abort(&empty[slot], parity, sh, A.err);
+    unsigned char* tile = ring + slot * PL::kTile;
+    const bool fold = kKind == kCacheE4m3 && info.all_folded();
+    const int c = (t % kVec) * 2;
+    // D = 128: the lanes of the second 64 dims store their halves the other way round, so that
+    // eight lanes meet eight bank groups
+    const bool swap = D == 128 && (c & 8);
+#pragma unroll 1
+    for (int group = 0; group < kGroups; ++group) {
+      uint4 q[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[i] = code[i];
+      if (group + 1 < kGroups) load(j, group + 1);
+      else load(j + 1, 0);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int v = t + (group * 4 + i) * kThreads;
+        if (!ok || v >= kAll) break;
+        const int r = v / kVec;
+        uint32_t f = kE4m3Factor;
+        if constexpr (kKind == kCacheE4m3) {
+          const uint32_t g = __float_as_uint(scales[(kV ? kKv : 0) + r] * 0x1p120f) >> 16;
+          f = fold ? g | (g << 16) : f;
+        }
+        const uint4 a =
+            make_uint4(word_bf16<kKind, false>(q[i].x, f), word_bf16<kKind, true>(q[i].x, f),
+                       word_bf16<kKind, false>(q[i].y, f), word_bf16<kKind, true>(q[i].y, f));
+        const uint4 b =
+            make_uint4(word_bf16<kKind, false>(q[i].z, f), word_bf16<kKind, true>(q[i].z, f),
+                       word_bf16<kKind, false>(q[i].w, f), word_bf16<kKind, true>(q[i].w, f));
+        *reinterpret_cast<uint4*>(tile + tile_at(r, swap ? c + 1 : c)) = swap ? b : a;
+        *reinterpret_cast<uint4*>(tile + tile_at(r, swap ? c : c + 1)) = swap ? a : b;
+      }
+    }
+    if (ok) {
+      fence_async_smem();
+      mbar_arrive(&full[slot]);
+    }
+    if (++slot == kSlots) {
+      slot = 0;
+      parity ^= 1;
+    }
+  }
+}
+
 // The CTA's rows one by one, a warp a row, in float32 throughout: for tiles that hold
 // infinities or NaNs which some rows see and others do not.
 template <int D>
@@ -480,9 +636,8 @@ __device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list
       const int t0 = w.tile(j) * kKv;
       for (int p = t0; p < t0 + kKv && p <= pos; ++p) {
         if (w.window && p <= pos - w.window && p >= w.n_sink) continue;
-        const int page = page_of(P, list.agent[w.x], p);
-        if (page < 0) continue;
-        const int64_t row = static_cast<int64_t>(page) * P.P + p % P.P;
+        const int64_t row = page_ref(P, list.agent[w.x], p, true).row(P);
+        if (row < 0) continue;
         const uint16_t* k = P.base + (plane + row) * A.g.E + w.h * D + lane * N;
         const uint16_t* v = P.base + (vplane + row) * A.g.E + w.h * D + lane * N;
         float s = 0.0f;
@@ -807,18 +962,17 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const uint32_t ring = smem_u32(is_v ? s_v : s_k);
       uint64_t* full = is_v ? sh->v_raw : sh->k_full;
       uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
-      // lane b < per looks up box b of tile j: its row, -1 not needed, -2 unmapped
+      // lane b < per looks up box b of tile j
       auto lookup = [&](int j) {
-        if (j >= w.n || lane >= per) return -1;
-        const int pos = w.tile(j) * kKv + lane * box;
-        if (!w.needed(pos, pos + box - 1)) return -1;
-        const int page = page_of(P, list.agent[w.x], pos);
-        return page < 0 ? -2 : plane + page * P.P + pos % P.P;
+        const int pos = w.tile(min(j, w.n - 1)) * kKv + lane * box;
+        return page_ref(P, list.agent[w.x], pos,
+                        j < w.n && lane < per && w.needed(pos, pos + box - 1));
       };
       int slot = 0, parity = 1, n = 0;                    // n: tiles started
-      int row = lookup(0);
+      PageRef next = lookup(0);
       for (; n < w.n; ++n) {
-        const int next = lookup(n + 1);
+        const int row = next.row(P);
+        next = lookup(n + 1);
         const uint32_t holes = __ballot_sync(0xFFFFFFFFu, row == -2);
         const uint32_t bytes = __popc(__ballot_sync(0xFFFFFFFFu, row >= 0)) * box * (D * 2u);
         if (holes && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
@@ -834,22 +988,25 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           sh->info[n % kInfo].valid[lane] = v;
         }
         int* rows = sh->box_row[is_v];
-        if (lane < 16) rows[lane] = row;
+        if (lane < 16) rows[lane] = row < 0 ? row : plane + row;
         __syncwarp();
         if (elected()) {
           mbar_arrive_expect_tx(&full[slot], bytes + A.tx_pad);
           const uint32_t dst = ring + slot * PL::kTile;
-          for (int b = 0; b < per; ++b) {
-            const int r = rows[b];
-            if (r < 0) continue;
+          int r[16];
+#pragma unroll
+          for (int b = 0; b < 16; b += 4)
+            *reinterpret_cast<int4*>(r + b) = *reinterpret_cast<const int4*>(rows + b);
+#pragma unroll
+          for (int b = 0; b < 16; ++b) {
+            if (b >= per || r[b] < 0) continue;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half)
-              tma_box(dst + half * (128 * 128) + b * box * 128, &map, w.h * D + half * 64, r,
+              tma_box(dst + half * (128 * 128) + b * box * 128, &map, w.h * D + half * 64, r[b],
                       &full[slot]);
           }
         }
         __syncwarp();
-        row = next;
         if (++slot == slots) {
           slot = 0;
           parity ^= 1;
@@ -908,107 +1065,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     }
   } else {
     // ------------------------- K and V from 8-bit codes: warps 12-15 make K, 9-11 V
-    const bool is_v = warp < kConvertWarp;
-    const int t = is_v ? tid - kLoadWarp * 32 : tid - kConvertWarp * 32;
-    constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
-    constexpr int kMost = (kKv * kVec + 95) / 96;         // per thread, of V's 96
-    const int threads = is_v ? 96 : 128;
-    const PoolDev& P = A.pool;
-    const int64_t half = P.num_pages * P.P;
-    const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * half;
-    const uint8_t* src = reinterpret_cast<const uint8_t*>(P.base) +
-                         (plane + (is_v ? half : 0)) * A.g.E + w.h * D;
-    // K's threads look the positions up, one each: -1 not needed, -2 unmapped
-    auto lookup = [&](int j) {
-      if (is_v || j >= w.n) return -1;
-      const int pos = w.tile(j) * kKv + t;
-      if (!w.needed(pos, pos)) return -1;
-      const int page = page_of(P, list.agent[w.x], pos);
-      return page < 0 ? -2 : page * P.P + pos % P.P;
-    };
-    uint4 code[kMost];
-    auto load = [&](int j) {
-#pragma unroll
-      for (int i = 0; i < kMost; ++i) {
-        const int v = t + i * threads;
-        const int row = v < kKv * kVec ? s_rows[(j & 1) * kKv + v / kVec] : -1;
-        code[i] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                          : __ldg(reinterpret_cast<const uint4*>(
-                                src + static_cast<int64_t>(row) * A.g.E + (v % kVec) * 16));
-      }
-    };
-    float ks = 0.0f, vs = 0.0f;
-    auto load_scales = [&](int row) {
-      ks = row < 0 ? 0.0f : __ldg(A.scale + (plane + row) * A.g.H + w.h);
-      vs = row < 0 ? 0.0f : __ldg(A.scale + (plane + half + row) * A.g.H + w.h);
-    };
-    auto group_sync = [] { asm volatile("bar.sync 1, 224;" ::: "memory"); };
-    // a scale that goes into the conversion's own factor: a power of two of at most 2^7
-    // (every scale that td_quantise_append writes for e4m3), or that of an absent row
-    auto folds = [](float s) {
-      return (__float_as_uint(s) & 0x007FFFFFu) == 0 && s >= 0.0f && s <= 128.0f;
-    };
-    int row = lookup(0), next = lookup(1);
-    if (!is_v) s_rows[t] = row;
-    group_sync();
-    load(0);
-    load_scales(row);
-    const int slots = is_v ? PL::kV : PL::kK;
-    uint64_t* full = is_v ? sh->v_full : sh->k_full;
-    uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
-    int slot = 0, parity = 1;
-    bool ok = true;                       // after a time-out the group still meets its barriers
-    for (int j = 0; j < w.n; ++j) {
-      Info& info = sh->info[j % kInfo];
-      float* scales = s_scale + (j % kInfo) * 2 * kKv;
-      if (!is_v) {
-        const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
-        const bool fold = kKind == kCacheE4m3 &&
-                          __all_sync(0xFFFFFFFFu, folds(ks) && folds(vs));
-        if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
-        if (lane == 0) {
-          info.valid[t >> 5] = ~hole;
-          info.folded[t >> 5] = fold;
-        }
-        scales[t] = ks;
-        scales[kKv + t] = vs;
-        row = next;
-        s_rows[((j + 1) & 1) * kKv + t] = row;
-      }
-      group_sync();
-      next = lookup(j + 2);
-      load_scales(row);
-      if (ok && j >= slots) ok = wait_or_abort(&empty[slot], parity, sh, A.err);
-      if (ok) {
-        unsigned char* tile = (is_v ? s_v : s_k) + slot * PL::kTile;
-        const bool fold = kKind == kCacheE4m3 && info.all_folded();
-#pragma unroll
-        for (int i = 0; i < kMost; ++i) {
-          const int v = t + i * threads;
-          if (v >= kKv * kVec) continue;
-          const int r = v / kVec, c = (v % kVec) * 2;
-          uint32_t f = kE4m3Factor;
-          if (fold) {
-            f = __float_as_uint(scales[(is_v ? kKv : 0) + r] * 0x1p120f) >> 16;
-            f |= f << 16;
-          }
-          const uint4 q = code[i];
-          *reinterpret_cast<uint4*>(tile + tile_at(r, c)) =
-              make_uint4(word_bf16<kKind, false>(q.x, f), word_bf16<kKind, true>(q.x, f),
-                         word_bf16<kKind, false>(q.y, f), word_bf16<kKind, true>(q.y, f));
-          *reinterpret_cast<uint4*>(tile + tile_at(r, c + 1)) =
-              make_uint4(word_bf16<kKind, false>(q.z, f), word_bf16<kKind, true>(q.z, f),
-                         word_bf16<kKind, false>(q.w, f), word_bf16<kKind, true>(q.w, f));
-        }
-        fence_async_smem();
-        mbar_arrive(&full[slot]);
-      }
-      load(j + 1);
-      if (++slot == slots) {
-        slot = 0;
-        parity ^= 1;
-      }
-    }
+    if (warp < kConvertWarp)
+      convert_tiles<D, kKind, true>(A, list, w, tid - kLoadWarp * 32, s_v, s_scale, s_rows, sh);
+    else
+      convert_tiles<D, kKind, false>(A, list, w, tid - kConvertWarp * 32, s_k, s_scale, s_rows, sh);
   }
 
   __syncthreads();
