@@ -9,14 +9,16 @@
 //
 // One warp takes a unit = (layer, kv head, tile of 8 or 16 query rows, `span` of the tile's
 // visible positions), 16 positions a step; the rows of a tile are (token, head of the group)
-// pairs, so the group's heads share every read. It is bound by the pages' bytes, so nothing is
-// staged: each lane loads 16-byte vectors of K and V straight into the registers of its
-// fragments (mma.sync m16n8k16, positions or dims as the 16 rows, query rows as the 8
-// columns). That works because a dot product may take its dims in any order: the lane's
-// vector of 8 (or 16) neighbouring dims is read as the scattered dims of its fragment, the
-// query's fragments and the output's rows are permuted alike, and V's pairs of positions
-// are made with byte permutes. The next step's K is loaded once the scores have consumed
-// this one's, its V after the weighted sum, so a warp has 8 KB under way at all times.
+// pairs, so the group's heads share every read. It is bound by the pages' bytes. Products are
+// mma.sync m16n8k16, positions or dims as the 16 rows, query rows as the 8 columns. Each lane
+// copies exactly the 16-byte vectors of K and V that its own fragments are made of (cp.async,
+// rows out of sight zero-filled) into a ring of its own, and reads them back without any
+// barrier. That works because a dot product may take its dims in any order: the lane's vector
+// of 8 (or 16) neighbouring dims is read as the scattered dims of its fragment, the query's
+// fragments and the output's rows are permuted alike, and V's pairs of positions are made with
+// byte permutes. The ring keeps the next steps' copies under way during a step, and the block
+// table is read a step ahead of the copies (loads straight into registers, with the table read
+// in line, left a warp waiting some 6,000 cycles a step).
 // The scores of a column are over the warp's positions, so the running maximum takes three
 // shuffles and the weights turn into the next product's operand by two movmatrix. The
 // weights are split in two bf16 parts (16 bits kept), two products, which costs nothing here.
@@ -31,7 +33,6 @@ namespace td {
 
 namespace {
 
-constexpr int kWarps = 4;
 constexpr int kStep = 16;    // positions per step
 
 __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
@@ -51,6 +52,24 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return y;
 }
 
+// 16 (4) bytes into shared memory, or zeros where `live` is not set.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src),
+               "r"(live ? 4 : 0)
+               : "memory");
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 __device__ __forceinline__ bool nonfinite2(uint32_t w) {
   return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
 }
@@ -65,23 +84,29 @@ struct Layout {
   static constexpr int vDims = k8 ? D / 8 : 8;
   static constexpr int vChunks = D / (8 * vDims);
   static constexpr int vWords = k8 ? vDims / 4 : vDims / 2;
+  static constexpr int vBytes = vWords * 4;
+  // a step's bytes in shared memory: 2 rows of K, 4 of V, 4 scales per lane
+  static constexpr int kBytes = 2 * kChunks * 16 * 32;
+  static constexpr int stage = kBytes + 4 * vChunks * vBytes * 32 + (k8 ? 4 * 4 * 32 : 0);
+  // steps under way: up to 16 KB a warp, 12 warps an SM or more
+  static constexpr int depth = stage >= 8192 ? 2 : (stage >= 4096 ? 3 : 4);
 };
 
 }  // namespace
 
 template <int D, int kKind, int NB>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(32, NB == 1 ? 12 : 8)
 chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
                   const __grid_constant__ ChunkUnits units) {
   pdl_wait();
   using Y = Layout<D, kKind>;
   constexpr int KCH = D / 16;
   constexpr int R = 8 * NB;
-  const int lane = threadIdx.x & 31;
+  __shared__ __align__(16) unsigned char s_ring[Y::depth][Y::stage];
+  const int lane = threadIdx.x;
   const int gid = lane >> 2, tig = lane & 3;
   const int total = units.base[list.n];
-  const int64_t unit = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (unit >= static_cast<int64_t>(A.nl) * A.g.H * total) return;
+  const int64_t unit = blockIdx.x;
   const int c = static_cast<int>(unit % total);
   const int64_t lh = unit / total;
   const int h = static_cast<int>(lh % A.g.H), li = static_cast<int>(lh / A.g.H);
@@ -146,62 +171,58 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const float* vscale = Y::k8 ? A.scale + vplane * A.g.H + h : nullptr;
   const int row_bytes = E * (Y::k8 ? 1 : 2);
 
-  // position of index v, and lane l < 16's page row of index v + l (-1: not visible, unmapped)
   auto position = [&](int v) { return v < sinks ? v : lo + v - sinks; };
-  auto page_row = [&](int v) {
-    const int vi = v + (lane & 15);
-    if (vi >= v1) return -1;
-    const int pos = position(vi);
+  // lane l < 16 (and l + 16 alike) reads the table for the position of index v + l, ahead of
+  // its use; the page row is made from it when the copies start: -1 past the end or unmapped
+  int ref_page = -1, ref_slot = 0;
+  auto look_up = [&](int v) {
+    const int pos = position(min(v + (lane & 15), v1 - 1));
     const int lp = P.p_shift >= 0 ? (pos >> P.p_shift) : pos / P.P;
-    int32_t page = -1;
-    if (lp < P.max_lp) page = __ldg(P.bt + static_cast<int64_t>(list.agent[x]) * P.max_lp + lp);
-    if (page < 0 || page >= P.num_pages) {
-      atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
-      return -1;
-    }
-    return page * P.P + (pos - lp * P.P);
+    ref_slot = pos - lp * P.P;
+    ref_page = -1;
+    if (lp < P.max_lp) ref_page = __ldg(P.bt + static_cast<int64_t>(list.agent[x]) * P.max_lp + lp);
   };
-
-  uint4 kr[2][Y::kChunks];                 // rows gid, gid + 8
-  uint32_t vr[4][Y::vChunks][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-  float ks[2] = {1.0f, 1.0f}, vs[2] = {1.0f, 1.0f};   // scales of rows gid, gid + 8
-  auto load_k = [&](int rows_of) {
+  // starts the copies of the step at v (looked up before); returns its mapped positions' bits
+  const uint32_t ring = smem_u32(s_ring);
+  auto start_copies = [&](int v, int slot) {
+    const bool in = v + (lane & 15) < v1;
+    const bool mapped = in && ref_page >= 0 && ref_page < P.num_pages;
+    if (in && !mapped) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+    const int mine = mapped ? ref_page * P.P + ref_slot : -1;
+    const uint32_t dst = ring + slot * Y::stage + lane * 16;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const int row = __shfl_sync(0xFFFFFFFFu, rows_of, gid + 8 * i);
-      const uint8_t* p = kbase + static_cast<int64_t>(row) * row_bytes;
+      const int row = __shfl_sync(0xFFFFFFFFu, mine, gid + 8 * i);
+      const int64_t r = max(row, 0);
 #pragma unroll
       for (int j = 0; j < Y::kChunks; ++j)
-        kr[i][j] = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                           : __ldg(reinterpret_cast<const uint4*>(p) + j * 4 + tig);
+        copy16(dst + (i * Y::kChunks + j) * 512, kbase + r * row_bytes + (j * 4 + tig) * 16,
+               row >= 0);
       if constexpr (Y::k8) {
-        ks[i] = row < 0 ? 0.0f : __ldg(kscale + static_cast<int64_t>(row) * A.g.H);
-        vs[i] = row < 0 ? 0.0f : __ldg(vscale + static_cast<int64_t>(row) * A.g.H);
+        const uint32_t sc = ring + (slot + 1) * Y::stage - 4 * 4 * 32 + lane * 4;
+        copy4(sc + i * 128, kscale + r * A.g.H, row >= 0);
+        copy4(sc + (2 + i) * 128, vscale + r * A.g.H, row >= 0);
       }
     }
-  };
-  auto load_v = [&](int rows_of) {
+    const uint32_t dv = ring + slot * Y::stage + Y::kBytes;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int row = __shfl_sync(0xFFFFFFFFu, rows_of, 2 * tig + (i & 1) + 8 * (i >> 1));
-      const uint8_t* p = vbase + static_cast<int64_t>(row) * row_bytes;
+      const int row = __shfl_sync(0xFFFFFFFFu, mine, 2 * tig + (i & 1) + 8 * (i >> 1));
+      const int64_t r = max(row, 0);
 #pragma unroll
       for (int j = 0; j < Y::vChunks; ++j) {
-        if constexpr (Y::vWords == 4) {
-          const uint4 w = row < 0 ? make_uint4(0u, 0u, 0u, 0u)
-                                  : __ldg(reinterpret_cast<const uint4*>(p) + j * 8 + gid);
-          vr[i][j][0] = w.x;
-          vr[i][j][1] = w.y;
-          vr[i][j][2] = w.z;
-          vr[i][j][3] = w.w;
+        const uint8_t* src = vbase + r * row_bytes + (j * 8 + gid) * Y::vBytes;
+        if constexpr (Y::vBytes == 16) {
+          copy16(dv + (i * Y::vChunks + j) * 512 + lane * 16, src, row >= 0);
         } else {
-          const uint2 w = row < 0 ? make_uint2(0u, 0u)
-                                  : __ldg(reinterpret_cast<const uint2*>(p) + j * 8 + gid);
-          vr[i][j][0] = w.x;
-          vr[i][j][1] = w.y;
+          // 8 neighbouring codes (D = 64)
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dv + i * 256 + lane * 8),
+                       "l"(src), "r"(row >= 0 ? 8 : 0)
+                       : "memory");
         }
       }
     }
+    return __ballot_sync(0xFFFFFFFFu, mapped) & 0xFFFFu;
   };
 
   // O^T: acc[nb][mt] = dims (lane's dims 2 mt, 2 mt + 1) x rows 2 tig, 2 tig + 1
@@ -216,12 +237,40 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       acc[nb][mt][0] = acc[nb][mt][1] = acc[nb][mt][2] = acc[nb][mt][3] = 0.0f;
   }
 
-  int cur = page_row(v0), nxt = page_row(v0 + kStep);
-  if (v0 < v1) {
-    load_k(cur);
-    load_v(cur);
+  // the ring: steps s .. s + depth - 1 are under way or in use
+  uint32_t bits[Y::depth];      // mapped positions of the steps in the ring, the oldest first
+  if (v0 < v1) look_up(v0);
+#pragma unroll
+  for (int i = 0; i < Y::depth - 1; ++i) {
+    bits[i] = 0;
+    if (v0 + i * kStep < v1) {
+      bits[i] = start_copies(v0 + i * kStep, i);
+      look_up(v0 + (i + 1) * kStep);
+    }
+    cp_async_commit();
   }
+  int slot = 0;
   for (int v = v0; v < v1; v += kStep) {
+    {
+      const int ahead = v + (Y::depth - 1) * kStep;
+      const int into = slot == 0 ? Y::depth - 1 : slot - 1;
+      uint32_t b = 0;
+      if (ahead < v1) {
+        b = start_copies(ahead, into);
+        look_up(ahead + kStep);
+      }
+      cp_async_commit();
+      bits[Y::depth - 1] = b;
+    }
+    cp_async_wait<Y::depth - 1>();
+    const uint32_t mapped_bits = bits[0];
+    const unsigned char* st = s_ring[slot];
+    uint4 kr[2][Y::kChunks];                 // rows gid, gid + 8
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int j = 0; j < Y::kChunks; ++j)
+        kr[i][j] = *reinterpret_cast<const uint4*>(st + (i * Y::kChunks + j) * 512 + lane * 16);
     // scores of positions gid, gid + 8 against rows 2 tig, 2 tig + 1
     float s[NB][4];
 #pragma unroll
@@ -249,26 +298,36 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       for (int nb = 0; nb < NB; ++nb)
         mma_bf16(s[nb], a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
     }
-    const float kse[2] = {ks[0], ks[1]}, vse[2] = {vs[0], vs[1]};
-    const int mapped[2] = {__shfl_sync(0xFFFFFFFFu, cur, gid),
-                           __shfl_sync(0xFFFFFFFFu, cur, gid + 8)};
-    const int nn = page_row(v + 2 * kStep);
-    if (v + kStep < v1) load_k(nxt);
-    // the weights: masked, in base 2 under the running maximum
-    const int pos[2] = {position(v + gid), position(v + gid + 8)};
-    bool masks = false;
+    [[maybe_unused]] float ks[2], vs[2];     // scales of rows gid, gid + 8
+    if constexpr (Y::k8) {
+      const float* sc = reinterpret_cast<const float*>(st + Y::stage - 4 * 4 * 32) + lane;
+      ks[0] = sc[0];
+      ks[1] = sc[32];
+      vs[0] = sc[64];
+      vs[1] = sc[96];
+    }
+    // does every row of the tile see every position of the step?
+    const int pa = position(v), pb = position(v + kStep - 1);
+    const bool whole = mapped_bits == 0xFFFFu && pb <= p_first &&
+                       (A.window == 0 || pa > p_last - A.window || v + kStep <= sinks);
+    // the weights, in base 2 under the running maximum; p = the weight on V
     float p[NB][4], fac[NB][2];
+    const int pos[2] = {position(v + gid), position(v + gid + 8)};
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int pq = pos_q[nb][i & 1], pp = pos[i >> 1];
-        const bool ok = mapped[i >> 1] >= 0 && pp <= pq &&
-                        (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
-        masks |= !ok && pq >= 0;
-        const float k = Y::k8 ? __fmul_rn(s[nb][i], kse[i >> 1]) : s[nb][i];
-        s[nb][i] = ok ? __fmul_rn(k, A.scale_log2) : -INFINITY;
-        p[nb][i] = ok ? 1.0f : 0.0f;
+        const float k = Y::k8 ? __fmul_rn(s[nb][i], ks[i >> 1]) : s[nb][i];
+        s[nb][i] = __fmul_rn(k, A.scale_log2);
+      }
+      if (!whole) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int pq = pos_q[nb][i & 1], pp = pos[i >> 1];
+          const bool ok = ((mapped_bits >> (gid + 8 * (i >> 1))) & 1u) && pp <= pq &&
+                          (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
+          if (!ok) s[nb][i] = -INFINITY;
+        }
       }
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
@@ -277,20 +336,39 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         const float m_new = fmaxf(m_run[nb][e], mx);
-        fac[nb][e] = m_run[nb][e] == -INFINITY ? 0.0f : exp2f(m_run[nb][e] - m_new);
+        // (nothing seen so far: -infinity minus 0, so that the weights come out 0)
+        const float sub = m_new == -INFINITY ? 0.0f : m_new;
+        fac[nb][e] = ex2(__fsub_rn(m_run[nb][e], sub));
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float w = s[nb][e + 2 * i] == -INFINITY ? 0.0f : exp2f(s[nb][e + 2 * i] - m_new);
-          s[nb][e + 2 * i] = w;
-        }
-        l_part[nb][e] = __fmaf_rn(l_part[nb][e], fac[nb][e], s[nb][e] + s[nb][e + 2]);
+        for (int i = 0; i < 2; ++i) p[nb][e + 2 * i] = ex2(__fsub_rn(s[nb][e + 2 * i], sub));
+        l_part[nb][e] = __fmaf_rn(l_part[nb][e], fac[nb][e], p[nb][e] + p[nb][e + 2]);
         m_run[nb][e] = m_new;
       }
-      // the weight on V: with the row's scale, 0 where the row is not seen
+      if constexpr (Y::k8) {
+        // (a row out of sight has the score -infinity and keeps the weight 0 whatever its scale)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        p[nb][i] = p[nb][i] == 0.0f ? 0.0f : (Y::k8 ? __fmul_rn(s[nb][i], vse[i >> 1]) : s[nb][i]);
+        for (int i = 0; i < 4; ++i)
+          p[nb][i] = s[nb][i] == -INFINITY ? 0.0f : __fmul_rn(p[nb][i], vs[i >> 1]);
+      }
     }
+    uint32_t vr[4][Y::vChunks][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < Y::vChunks; ++j) {
+        const unsigned char* at = st + Y::kBytes + (i * Y::vChunks + j) * (Y::vBytes * 32) + lane * Y::vBytes;
+        if constexpr (Y::vBytes == 16) {
+          const uint4 w = *reinterpret_cast<const uint4*>(at);
+          vr[i][j][0] = w.x;
+          vr[i][j][1] = w.y;
+          vr[i][j][2] = w.z;
+          vr[i][j][3] = w.w;
+        } else {
+          const uint2 w = *reinterpret_cast<const uint2*>(at);
+          vr[i][j][0] = w.x;
+          vr[i][j][1] = w.y;
+        }
+      }
     uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb)
@@ -302,18 +380,23 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
         ph[nb][i] = transpose8(hi);
         pl[nb][i] = transpose8(lo2);
       }
+    bool grew = false;
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
+    for (int nb = 0; nb < NB; ++nb) grew |= fac[nb][0] != 1.0f || fac[nb][1] != 1.0f;
+    if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
-      for (int mt = 0; mt < KCH; ++mt) {
-        acc[nb][mt][0] *= fac[nb][0];
-        acc[nb][mt][1] *= fac[nb][1];
-        acc[nb][mt][2] *= fac[nb][0];
-        acc[nb][mt][3] *= fac[nb][1];
-      }
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int mt = 0; mt < KCH; ++mt) {
+          acc[nb][mt][0] *= fac[nb][0];
+          acc[nb][mt][1] *= fac[nb][1];
+          acc[nb][mt][2] *= fac[nb][0];
+          acc[nb][mt][3] *= fac[nb][1];
+        }
+    }
     if constexpr (!Y::k8) {
       // values that must not meet a zero weight (rare: a step that masks, with such a value)
-      if (__any_sync(0xFFFFFFFFu, masks)) {
+      if (!whole) {
         bool bad = false;
 #pragma unroll
         for (int i = 0; i < 4; ++i)
@@ -388,9 +471,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
         mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
       }
     }
-    if (v + kStep < v1) load_v(nxt);
-    cur = nxt;
-    nxt = nn;
+#pragma unroll
+    for (int i = 0; i + 1 < Y::depth; ++i) bits[i] = bits[i + 1];
+    slot = slot + 1 == Y::depth ? 0 : slot + 1;
   }
 
   // the lane's dims: vector j holds dims (j * 8 + gid) * vDims + 0 .. vDims - 1
@@ -445,21 +528,24 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     }
 }
 
-// One warp per (layer, token, query head): the row's parts joined. A part that saw nothing has
-// the maximum -inf and weight 0, and is not read.
+// A CTA of four warps per (layer, token, query head): the row's parts joined, warp w taking
+// parts w, w + 4, ..., its loads all under way together. A part that saw nothing has the
+// maximum -inf and weight 0, and is not read.
+constexpr int kJoinWarps = 4;
+
 template <int D>
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(kJoinWarps * 32)
 chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
                   const __grid_constant__ ChunkUnits units, int R) {
   pdl_wait();
   constexpr int DPL = D / 32;
-  const int lane = threadIdx.x & 31;
+  __shared__ float s_acc[kJoinWarps][D];
+  __shared__ float s_l[kJoinWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_tok = list.row[list.n];
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  if (w >= static_cast<int64_t>(A.nl) * n_tok * A.nq) return;
-  const int gq = static_cast<int>(w % A.nq);
-  const int t = static_cast<int>((w / A.nq) % n_tok);
-  const int li = static_cast<int>(w / (static_cast<int64_t>(A.nq) * n_tok));
+  const int gq = static_cast<int>(blockIdx.x % A.nq);
+  const int lt = static_cast<int>(blockIdx.x / A.nq);
+  const int t = lt % n_tok, li = lt / n_tok;
   int x = 0;
   for (int hi = list.n - 1; x < hi;) {
     const int mid = (x + hi + 1) >> 1;
@@ -472,54 +558,63 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const int ns = units.nsplit[x];
   const int64_t u0 = (static_cast<int64_t>(li) * A.g.H + h) * units.base[list.n] + units.base[x] +
                      static_cast<int64_t>(tile) * ns;
+  // every warp finds the row's maximum itself
   float mx = -INFINITY;
   bool nan = false;
   for (int i = lane; i < ns; i += 32) {
-    const float m = A.part_ml[((u0 + i) * R + rt) * 2];
-    mx = fmaxf(mx, m);
+    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + ((u0 + i) * R + rt) * 2);
+    mx = fmaxf(mx, ml.x);
+    nan |= ml.y != ml.y;      // scores that are NaN leave the maximum and make the sum NaN
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, o));
   float l = 0.0f, acc[DPL];
 #pragma unroll
   for (int d = 0; d < DPL; ++d) acc[d] = 0.0f;
-  for (int i0 = 0; i0 < ns; i0 += 32) {
-    float wgt = 0.0f;
-    if (i0 + lane < ns) {
-      const float* ml = A.part_ml + ((u0 + i0 + lane) * R + rt) * 2;
-      // a part whose scores are NaN keeps the maximum -inf but a sum that is NaN
-      nan |= ml[1] != ml[1];
-      wgt = ml[0] == -INFINITY ? 0.0f : exp2f(ml[0] - mx);
-      l = wgt == 0.0f ? l : __fmaf_rn(ml[1], wgt, l);
+#pragma unroll 8
+  for (int i = warp; i < ns; i += kJoinWarps) {
+    const int64_t pr = (u0 + i) * R + rt;
+    const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + pr * 2);
+    const bool some = ml.x != -INFINITY;
+    const float w = some ? exp2f(ml.x - mx) : 0.0f;
+    const float* po = A.part_o + pr * D + lane * DPL;
+    float q[DPL];
+    if constexpr (DPL == 4) {
+      const float4 f = some ? *reinterpret_cast<const float4*>(po) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      q[0] = f.x;
+      q[1] = f.y;
+      q[2] = f.z;
+      q[3] = f.w;
+    } else {
+      const float2 f = some ? *reinterpret_cast<const float2*>(po) : make_float2(0.0f, 0.0f);
+      q[0] = f.x;
+      q[1] = f.y;
     }
-    const int nb = min(32, ns - i0);
-#pragma unroll 4
-    for (int j = 0; j < nb; ++j) {
-      const float wj = __shfl_sync(0xFFFFFFFFu, wgt, j);
-      if (wj == 0.0f) continue;
-      const float* po = A.part_o + ((u0 + i0 + j) * R + rt) * D + lane * DPL;
-      if constexpr (DPL == 4) {
-        const float4 q = *reinterpret_cast<const float4*>(po);
-        acc[0] = __fmaf_rn(q.x, wj, acc[0]);
-        acc[1] = __fmaf_rn(q.y, wj, acc[1]);
-        acc[2] = __fmaf_rn(q.z, wj, acc[2]);
-        acc[3] = __fmaf_rn(q.w, wj, acc[3]);
-      } else {
-        const float2 q = *reinterpret_cast<const float2*>(po);
-        acc[0] = __fmaf_rn(q.x, wj, acc[0]);
-        acc[1] = __fmaf_rn(q.y, wj, acc[1]);
-      }
-    }
+    if (some) l = __fmaf_rn(ml.y, w, l);
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) acc[d] = __fmaf_rn(q[d], w, acc[d]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, o);
-  if (__any_sync(0xFFFFFFFFu, nan)) l = __uint_as_float(0x7FC00000u);
+  for (int d = 0; d < DPL; ++d) s_acc[warp][lane * DPL + d] = acc[d];
+  if (lane == 0) s_l[warp] = l;
+  const bool any_nan = __syncthreads_or(nan);
+  if (warp != 0) return;
+  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+  if (any_nan) l = __uint_as_float(0x7FC00000u);
   const int64_t row =
       (static_cast<int64_t>(li) * A.tokens + list.tok[x] + t - list.row[x]) * A.nq + gq;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D + lane * DPL);
 #pragma unroll
-  for (int d = 0; d < DPL; d += 2) out[d / 2] = pack_bf2(acc[d] * inv, acc[d + 1] * inv);
+  for (int d = 0; d < DPL; d += 2) {
+    float y[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int c = lane * DPL + d + e;
+      y[e] = ((s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c])) * inv;
+    }
+    out[d / 2] = pack_bf2(y[0], y[1]);
+  }
   if (lane == 0 && A.lse)
     A.lse[row] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
 }
@@ -529,10 +624,10 @@ static cudaError_t run_rows(const ChunkArgs& a, const ChunkList& list, const Chu
                             int rows_per_tile, cudaStream_t st) {
   const int64_t n = static_cast<int64_t>(a.nl) * a.g.H * units.base[list.n];
   if (n == 0) return cudaSuccess;
-  const unsigned grid = static_cast<unsigned>((n + kWarps - 1) / kWarps);
+  const unsigned grid = static_cast<unsigned>(n);
   if (rows_per_tile == 8)
-    return launch_after(chunk_rows_kernel<D, kKind, 1>, grid, kWarps * 32, 0, st, a, list, units);
-  return launch_after(chunk_rows_kernel<D, kKind, 2>, grid, kWarps * 32, 0, st, a, list, units);
+    return launch_after(chunk_rows_kernel<D, kKind, 1>, grid, 32, 0, st, a, list, units);
+  return launch_after(chunk_rows_kernel<D, kKind, 2>, grid, 32, 0, st, a, list, units);
 }
 
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
@@ -555,11 +650,12 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
 
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st) {
-  const int64_t rows = static_cast<int64_t>(a.nl) * list.row[list.n] * a.nq;
-  const unsigned grid = static_cast<unsigned>((rows + 3) / 4);
+  const unsigned grid = static_cast<unsigned>(a.nl) * list.row[list.n] * a.nq;
   if (a.g.D == 128)
-    return launch_after(chunk_join_kernel<128>, grid, 128, 0, st, a, list, units, rows_per_tile);
-  return launch_after(chunk_join_kernel<64>, grid, 128, 0, st, a, list, units, rows_per_tile);
+    return launch_after(chunk_join_kernel<128>, grid, kJoinWarps * 32, 0, st, a, list, units,
+                        rows_per_tile);
+  return launch_after(chunk_join_kernel<64>, grid, kJoinWarps * 32, 0, st, a, list, units,
+                      rows_per_tile);
 }
 
 }  // namespace td

@@ -245,7 +245,7 @@ int64_t plan_rows(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUni
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = most <= 8 ? 8 : 16;
   return cut(
-      list, static_cast<int64_t>(c->sm_count) * 8, static_cast<int64_t>(a->g.H) * a->nl, 4, 8,
+      list, static_cast<int64_t>(c->sm_count) * 12, static_cast<int64_t>(a->g.H) * a->nl, 8, 8,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
       [&](int x) { return (seen_positions(list, *a, x, R) + 15) / 16; }, 16, a, units);
 }
@@ -281,7 +281,7 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   if (s != TD_OK) return s;
   if (tokens == 0) return TD_OK;
   if (!q || !out || !aligned16(q) || !aligned16(out) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || tokens > INT32_MAX / n_q_heads)
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || tokens > INT32_MAX / n_q_heads / (layer_end - layer_begin))
     return TD_ERR_INVALID_ARG;
   ChunkArgs a{};
   CUtensorMap map{};
