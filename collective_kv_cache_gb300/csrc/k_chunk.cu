@@ -8,7 +8,7 @@
 // go through the same products, with ks_p on the score and vs_p on the weight.
 //
 // One warp takes a unit = (layer, kv head, tile of 8 or 16 query rows, `span` of the tile's
-// visible positions), 16 positions a step; the rows of a tile are (token, head of the group)
+// visible positions), 16 or 32 positions a step; the rows of a tile are (token, head of the group)
 // pairs, so the group's heads share every read. It is bound by the pages' bytes. Products are
 // mma.sync m16n8k16, positions or dims as the 16 rows, query rows as the 8 columns. Each lane
 // copies exactly the 16-byte vectors of K and V that its own fragments are made of (cp.async,
@@ -33,7 +33,6 @@ namespace td {
 
 namespace {
 
-constexpr int kStep = 16;    // positions per step
 
 __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -85,11 +84,16 @@ struct Layout {
   static constexpr int vChunks = D / (8 * vDims);
   static constexpr int vWords = k8 ? vDims / 4 : vDims / 2;
   static constexpr int vBytes = vWords * 4;
-  // a step's bytes in shared memory: 2 rows of K, 4 of V, 4 scales per lane
+  // a step takes `subs` times 16 positions; its bytes in shared memory: per sub-step and lane
+  // 2 rows of K and 4 of V, then the positions' scales
+  static constexpr int subs = !k8 && D == 128 ? 1 : 2;
+  static constexpr int step = 16 * subs;
   static constexpr int kBytes = 2 * kChunks * 16 * 32;
-  static constexpr int stage = kBytes + 4 * vChunks * vBytes * 32 + (k8 ? 4 * 4 * 32 : 0);
-  // steps under way: up to 16 KB a warp, 12 warps an SM or more
-  static constexpr int depth = stage >= 8192 ? 2 : (stage >= 4096 ? 3 : 4);
+  static constexpr int vAll = 4 * vChunks * vBytes * 32;
+  static constexpr int codes = subs * (kBytes + vAll);
+  static constexpr int stage = codes + (k8 ? 2 * step * 4 : 0);
+  // steps under way: 16 KB a warp or a little more, 12 warps an SM
+  static constexpr int depth = stage >= 8192 ? 2 : 4;
 };
 
 }  // namespace
@@ -132,6 +136,99 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const int v0 = split * A.span;
   const int v1 = min(v0 + A.span, n_vis);
 
+  const PoolDev& P = A.pool;
+  const int64_t plane = (static_cast<int64_t>(A.layer_begin + li) * 2) * P.num_pages * P.P;
+  const int64_t vplane = plane + P.num_pages * P.P;
+  const int E = A.g.E;
+  // bytes of an element: 2 or 1
+  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(P.base) +
+                         (plane * E + h * D) * (Y::k8 ? 1 : 2);
+  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(P.base) +
+                         (vplane * E + h * D) * (Y::k8 ? 1 : 2);
+  const float* kscale = Y::k8 ? A.scale + plane * A.g.H + h : nullptr;
+  const float* vscale = Y::k8 ? A.scale + vplane * A.g.H + h : nullptr;
+  const int row_bytes = E * (Y::k8 ? 1 : 2);
+
+  auto position = [&](int v) { return v < sinks ? v : lo + v - sinks; };
+  // lane l reads the table for the position of index v + l (16 positions a step: lanes l and
+  // l + 16 the same), ahead of its use; the page row is made from it when the copies start
+  constexpr int kStep = Y::step;
+  constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
+  int ref_page = -1, ref_slot = 0;
+  auto look_up = [&](int v) {
+    const int pos = position(min(v + (lane & (kStep - 1)), v1 - 1));
+    const int lp = P.p_shift >= 0 ? (pos >> P.p_shift) : pos / P.P;
+    ref_slot = pos - lp * P.P;
+    ref_page = -1;
+    if (lp < P.max_lp) ref_page = __ldg(P.bt + static_cast<int64_t>(list.agent[x]) * P.max_lp + lp);
+  };
+  // starts the copies of the step at v (looked up before); returns its mapped positions' bits
+  const uint32_t ring = smem_u32(s_ring);
+  const uint8_t* klane = kbase + tig * 16;
+  const uint8_t* vlane = vbase + gid * Y::vBytes;
+  auto start_copies = [&](int v, int slot) {
+    const bool in = v + (lane & (kStep - 1)) < v1;
+    const bool mapped = in && ref_page >= 0 && ref_page < P.num_pages;
+    const uint32_t have = __ballot_sync(0xFFFFFFFFu, mapped) & kAll;
+    const int mine = mapped ? ref_page * P.P + ref_slot : 0;
+    if (in && !mapped) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
+    const uint32_t base = ring + slot * Y::stage;
+    if constexpr (Y::k8) {
+      const uint32_t sc = base + Y::codes + lane * 4;
+      copy4(sc, kscale + static_cast<int64_t>(mine) * A.g.H, mapped);
+      copy4(sc + kStep * 4, vscale + static_cast<int64_t>(mine) * A.g.H, mapped);
+    }
+#pragma unroll
+    for (int sub = 0; sub < Y::subs; ++sub) {
+      const uint32_t dk = base + sub * (Y::kBytes + Y::vAll) + lane * 16;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int at = sub * 16 + gid + 8 * i;
+        const int row = __shfl_sync(0xFFFFFFFFu, mine, at);
+        const uint8_t* src = klane + static_cast<int64_t>(row) * row_bytes;
+        const bool live = (have >> at) & 1u;
+#pragma unroll
+        for (int j = 0; j < Y::kChunks; ++j)
+          copy16(dk + (i * Y::kChunks + j) * 512, src + j * 64, live);
+      }
+      const uint32_t dv = base + sub * (Y::kBytes + Y::vAll) + Y::kBytes + lane * Y::vBytes;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = sub * 16 + 2 * tig + (i & 1) + 8 * (i >> 1);
+        const int row = __shfl_sync(0xFFFFFFFFu, mine, at);
+        const uint8_t* src = vlane + static_cast<int64_t>(row) * row_bytes;
+        const bool live = (have >> at) & 1u;
+#pragma unroll
+        for (int j = 0; j < Y::vChunks; ++j) {
+          const uint32_t to = dv + (i * Y::vChunks + j) * (Y::vBytes * 32);
+          if constexpr (Y::vBytes == 16) {
+            copy16(to, src + j * 128, live);
+          } else {
+            // 8 neighbouring codes (D = 64)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(to), "l"(src),
+                         "r"(live ? 8 : 0)
+                         : "memory");
+          }
+        }
+      }
+    }
+    return have;
+  };
+
+  // the ring: the copies of the first steps start before anything else is loaded
+  uint32_t bits[Y::depth];      // mapped positions of the steps in the ring, the oldest first
+  if (v0 < v1) look_up(v0);
+#pragma unroll
+  for (int i = 0; i < Y::depth - 1; ++i) {
+    bits[i] = 0;
+    if (v0 + i * kStep < v1) {
+      bits[i] = start_copies(v0 + i * kStep, i);
+      look_up(v0 + (i + 1) * kStep);
+    }
+    cp_async_commit();
+  }
+  pdl_trigger();
+
   // this lane's query rows: as a B-operand column (gid), and as accumulator columns
   int pos_q[NB][2];          // positions of columns 2 tig, 2 tig + 1; -1 past the last row
   uint32_t qf[NB][KCH][2];
@@ -158,73 +255,6 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       }
   }
 
-  const PoolDev& P = A.pool;
-  const int64_t plane = (static_cast<int64_t>(A.layer_begin + li) * 2) * P.num_pages * P.P;
-  const int64_t vplane = plane + P.num_pages * P.P;
-  const int E = A.g.E;
-  // bytes of an element: 2 or 1
-  const uint8_t* kbase = reinterpret_cast<const uint8_t*>(P.base) +
-                         (plane * E + h * D) * (Y::k8 ? 1 : 2);
-  const uint8_t* vbase = reinterpret_cast<const uint8_t*>(P.base) +
-                         (vplane * E + h * D) * (Y::k8 ? 1 : 2);
-  const float* kscale = Y::k8 ? A.scale + plane * A.g.H + h : nullptr;
-  const float* vscale = Y::k8 ? A.scale + vplane * A.g.H + h : nullptr;
-  const int row_bytes = E * (Y::k8 ? 1 : 2);
-
-  auto position = [&](int v) { return v < sinks ? v : lo + v - sinks; };
-  // lane l < 16 (and l + 16 alike) reads the table for the position of index v + l, ahead of
-  // its use; the page row is made from it when the copies start: -1 past the end or unmapped
-  int ref_page = -1, ref_slot = 0;
-  auto look_up = [&](int v) {
-    const int pos = position(min(v + (lane & 15), v1 - 1));
-    const int lp = P.p_shift >= 0 ? (pos >> P.p_shift) : pos / P.P;
-    ref_slot = pos - lp * P.P;
-    ref_page = -1;
-    if (lp < P.max_lp) ref_page = __ldg(P.bt + static_cast<int64_t>(list.agent[x]) * P.max_lp + lp);
-  };
-  // starts the copies of the step at v (looked up before); returns its mapped positions' bits
-  const uint32_t ring = smem_u32(s_ring);
-  auto start_copies = [&](int v, int slot) {
-    const bool in = v + (lane & 15) < v1;
-    const bool mapped = in && ref_page >= 0 && ref_page < P.num_pages;
-    if (in && !mapped) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
-    const int mine = mapped ? ref_page * P.P + ref_slot : -1;
-    const uint32_t dst = ring + slot * Y::stage + lane * 16;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int row = __shfl_sync(0xFFFFFFFFu, mine, gid + 8 * i);
-      const int64_t r = max(row, 0);
-#pragma unroll
-      for (int j = 0; j < Y::kChunks; ++j)
-        copy16(dst + (i * Y::kChunks + j) * 512, kbase + r * row_bytes + (j * 4 + tig) * 16,
-               row >= 0);
-      if constexpr (Y::k8) {
-        const uint32_t sc = ring + (slot + 1) * Y::stage - 4 * 4 * 32 + lane * 4;
-        copy4(sc + i * 128, kscale + r * A.g.H, row >= 0);
-        copy4(sc + (2 + i) * 128, vscale + r * A.g.H, row >= 0);
-      }
-    }
-    const uint32_t dv = ring + slot * Y::stage + Y::kBytes;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int row = __shfl_sync(0xFFFFFFFFu, mine, 2 * tig + (i & 1) + 8 * (i >> 1));
-      const int64_t r = max(row, 0);
-#pragma unroll
-      for (int j = 0; j < Y::vChunks; ++j) {
-        const uint8_t* src = vbase + r * row_bytes + (j * 8 + gid) * Y::vBytes;
-        if constexpr (Y::vBytes == 16) {
-          copy16(dv + (i * Y::vChunks + j) * 512 + lane * 16, src, row >= 0);
-        } else {
-          // 8 neighbouring codes (D = 64)
-          asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dv + i * 256 + lane * 8),
-                       "l"(src), "r"(row >= 0 ? 8 : 0)
-                       : "memory");
-        }
-      }
-    }
-    return __ballot_sync(0xFFFFFFFFu, mapped) & 0xFFFFu;
-  };
-
   // O^T: acc[nb][mt] = dims (lane's dims 2 mt, 2 mt + 1) x rows 2 tig, 2 tig + 1
   float acc[NB][KCH][4];
   float m_run[NB][2], l_part[NB][2];
@@ -237,24 +267,13 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       acc[nb][mt][0] = acc[nb][mt][1] = acc[nb][mt][2] = acc[nb][mt][3] = 0.0f;
   }
 
-  // the ring: steps s .. s + depth - 1 are under way or in use
-  uint32_t bits[Y::depth];      // mapped positions of the steps in the ring, the oldest first
-  if (v0 < v1) look_up(v0);
-#pragma unroll
-  for (int i = 0; i < Y::depth - 1; ++i) {
-    bits[i] = 0;
-    if (v0 + i * kStep < v1) {
-      bits[i] = start_copies(v0 + i * kStep, i);
-      look_up(v0 + (i + 1) * kStep);
-    }
-    cp_async_commit();
-  }
   int slot = 0;
   for (int v = v0; v < v1; v += kStep) {
     {
       const int ahead = v + (Y::depth - 1) * kStep;
       const int into = slot == 0 ? Y::depth - 1 : slot - 1;
       uint32_t b = 0;
+      if constexpr (Y::k8) __syncwarp();     // the slot's scales have been read by all lanes
       if (ahead < v1) {
         b = start_copies(ahead, into);
         look_up(ahead + kStep);
@@ -263,126 +282,104 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       bits[Y::depth - 1] = b;
     }
     cp_async_wait<Y::depth - 1>();
-    const uint32_t mapped_bits = bits[0];
+    if constexpr (Y::k8) __syncwarp();       // (the scales are the other lanes' copies)
+    const uint32_t have = bits[0];
     const unsigned char* st = s_ring[slot];
-    uint4 kr[2][Y::kChunks];                 // rows gid, gid + 8
+    const float* scales = reinterpret_cast<const float*>(st + Y::codes);
+    // scores: s[sub][nb][i] of position sub * 16 + gid + 8 * (i >> 1), column 2 tig + (i & 1)
+    float s[Y::subs][NB][4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int sub = 0; sub < Y::subs; ++sub) {
+      const unsigned char* sk = st + sub * (Y::kBytes + Y::vAll) + lane * 16;
+      uint4 kr[2][Y::kChunks];               // rows gid, gid + 8
 #pragma unroll
-      for (int j = 0; j < Y::kChunks; ++j)
-        kr[i][j] = *reinterpret_cast<const uint4*>(st + (i * Y::kChunks + j) * 512 + lane * 16);
-    // scores of positions gid, gid + 8 against rows 2 tig, 2 tig + 1
-    float s[NB][4];
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
-#pragma unroll
-    for (int kc = 0; kc < KCH; ++kc) {
-      uint32_t a[4];
-      if constexpr (Y::k8) {
-        const int j = kc >> 2;
-        const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kr[0][j])[kc & 3];
-        const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kr[1][j])[kc & 3];
-        a[0] = word_bf16<kKind, false>(w0);
-        a[1] = word_bf16<kKind, false>(w1);
-        a[2] = word_bf16<kKind, true>(w0);
-        a[3] = word_bf16<kKind, true>(w1);
-      } else {
-        const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kr[0][kc >> 1]) + (kc & 1) * 2;
-        const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kr[1][kc >> 1]) + (kc & 1) * 2;
-        a[0] = w0[0];
-        a[1] = w1[0];
-        a[2] = w0[1];
-        a[3] = w1[1];
-      }
+        for (int j = 0; j < Y::kChunks; ++j)
+          kr[i][j] = *reinterpret_cast<const uint4*>(sk + (i * Y::kChunks + j) * 512);
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        mma_bf16(s[nb], a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
-    }
-    [[maybe_unused]] float ks[2], vs[2];     // scales of rows gid, gid + 8
-    if constexpr (Y::k8) {
-      const float* sc = reinterpret_cast<const float*>(st + Y::stage - 4 * 4 * 32) + lane;
-      ks[0] = sc[0];
-      ks[1] = sc[32];
-      vs[0] = sc[64];
-      vs[1] = sc[96];
+        s[sub][nb][0] = s[sub][nb][1] = s[sub][nb][2] = s[sub][nb][3] = 0.0f;
+#pragma unroll
+      for (int kc = 0; kc < KCH; ++kc) {
+        uint32_t a[4];
+        if constexpr (Y::k8) {
+          const int j = kc >> 2;
+          const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kr[0][j])[kc & 3];
+          const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kr[1][j])[kc & 3];
+          a[0] = word_bf16<kKind, false>(w0);
+          a[1] = word_bf16<kKind, false>(w1);
+          a[2] = word_bf16<kKind, true>(w0);
+          a[3] = word_bf16<kKind, true>(w1);
+        } else {
+          const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kr[0][kc >> 1]) + (kc & 1) * 2;
+          const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kr[1][kc >> 1]) + (kc & 1) * 2;
+          a[0] = w0[0];
+          a[1] = w1[0];
+          a[2] = w0[1];
+          a[3] = w1[1];
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+          mma_bf16(s[sub][nb], a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
+      }
     }
     // does every row of the tile see every position of the step?
     const int pa = position(v), pb = position(v + kStep - 1);
-    const bool whole = mapped_bits == 0xFFFFu && pb <= p_first &&
+    const bool whole = have == kAll && pb <= p_first &&
                        (A.window == 0 || pa > p_last - A.window || v + kStep <= sinks);
-    // the weights, in base 2 under the running maximum; p = the weight on V
-    float p[NB][4], fac[NB][2];
-    const int pos[2] = {position(v + gid), position(v + gid + 8)};
 #pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float k = Y::k8 ? __fmul_rn(s[nb][i], ks[i >> 1]) : s[nb][i];
-        s[nb][i] = __fmul_rn(k, A.scale_log2);
+    for (int sub = 0; sub < Y::subs; ++sub) {
+      float m[2] = {A.scale_log2, A.scale_log2};      // rows gid, gid + 8
+      if constexpr (Y::k8) {
+        m[0] = __fmul_rn(m[0], scales[sub * 16 + gid]);
+        m[1] = __fmul_rn(m[1], scales[sub * 16 + gid + 8]);
       }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[sub][nb][i] = __fmul_rn(s[sub][nb][i], m[i >> 1]);
       if (!whole) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int pq = pos_q[nb][i & 1], pp = pos[i >> 1];
-          const bool ok = ((mapped_bits >> (gid + 8 * (i >> 1))) & 1u) && pp <= pq &&
-                          (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
-          if (!ok) s[nb][i] = -INFINITY;
-        }
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int at = sub * 16 + gid + 8 * (i >> 1);
+            const int pq = pos_q[nb][i & 1], pp = position(v + at);
+            const bool ok = ((have >> at) & 1u) && pp <= pq &&
+                            (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
+            if (!ok) s[sub][nb][i] = -INFINITY;
+          }
       }
+    }
+    // the weights, in base 2 under the running maximum
+    float fac[NB][2], w[Y::subs][NB][4];
+    bool grew = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float mx = fmaxf(s[nb][e], s[nb][e + 2]);
+        float mx = fmaxf(s[0][nb][e], s[0][nb][e + 2]);
+        if constexpr (Y::subs == 2) mx = fmaxf(mx, fmaxf(s[1][nb][e], s[1][nb][e + 2]));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 4));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 8));
         mx = fmaxf(mx, __shfl_xor_sync(0xFFFFFFFFu, mx, 16));
         const float m_new = fmaxf(m_run[nb][e], mx);
         // (nothing seen so far: -infinity minus 0, so that the weights come out 0)
-        const float sub = m_new == -INFINITY ? 0.0f : m_new;
-        fac[nb][e] = ex2(__fsub_rn(m_run[nb][e], sub));
-#pragma unroll
-        for (int i = 0; i < 2; ++i) p[nb][e + 2 * i] = ex2(__fsub_rn(s[nb][e + 2 * i], sub));
-        l_part[nb][e] = __fmaf_rn(l_part[nb][e], fac[nb][e], p[nb][e] + p[nb][e + 2]);
+        const float sub0 = m_new == -INFINITY ? 0.0f : m_new;
+        fac[nb][e] = ex2(__fsub_rn(m_run[nb][e], sub0));
+        grew |= m_new != m_run[nb][e];
         m_run[nb][e] = m_new;
+        float sum = 0.0f;
+#pragma unroll
+        for (int sub = 0; sub < Y::subs; ++sub)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            w[sub][nb][e + 2 * i] = ex2(__fsub_rn(s[sub][nb][e + 2 * i], sub0));
+            sum = __fadd_rn(sum, w[sub][nb][e + 2 * i]);
+          }
+        l_part[nb][e] = __fmaf_rn(l_part[nb][e], fac[nb][e], sum);
       }
-      if constexpr (Y::k8) {
-        // (a row out of sight has the score -infinity and keeps the weight 0 whatever its scale)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          p[nb][i] = s[nb][i] == -INFINITY ? 0.0f : __fmul_rn(p[nb][i], vs[i >> 1]);
-      }
-    }
-    uint32_t vr[4][Y::vChunks][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < Y::vChunks; ++j) {
-        const unsigned char* at = st + Y::kBytes + (i * Y::vChunks + j) * (Y::vBytes * 32) + lane * Y::vBytes;
-        if constexpr (Y::vBytes == 16) {
-          const uint4 w = *reinterpret_cast<const uint4*>(at);
-          vr[i][j][0] = w.x;
-          vr[i][j][1] = w.y;
-          vr[i][j][2] = w.z;
-          vr[i][j][3] = w.w;
-        } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(at);
-          vr[i][j][0] = w.x;
-          vr[i][j][1] = w.y;
-        }
-      }
-    uint32_t ph[NB][2], pl[NB][2];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const uint32_t hi = pack_bf2(p[nb][2 * i], p[nb][2 * i + 1]);
-        const uint32_t lo2 = pack_bf2(__fsub_rn(p[nb][2 * i], bf_lo(hi)),
-                                      __fsub_rn(p[nb][2 * i + 1], bf_hi(hi)));
-        ph[nb][i] = transpose8(hi);
-        pl[nb][i] = transpose8(lo2);
-      }
-    bool grew = false;
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) grew |= fac[nb][0] != 1.0f || fac[nb][1] != 1.0f;
     if (__any_sync(0xFFFFFFFFu, grew)) {
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -394,81 +391,132 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           acc[nb][mt][3] *= fac[nb][1];
         }
     }
-    if constexpr (!Y::k8) {
-      // values that must not meet a zero weight (rare: a step that masks, with such a value)
-      if (!whole) {
-        bool bad = false;
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+    for (int sub = 0; sub < Y::subs; ++sub) {
+      // p: the weight on V, with the row's scale
+      float p[NB][4];
 #pragma unroll
-          for (int j = 0; j < Y::vChunks; ++j)
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-            for (int w = 0; w < Y::vWords; ++w) bad |= nonfinite2(vr[i][j][w]);
-        if (__any_sync(0xFFFFFFFFu, bad)) {
+        for (int i = 0; i < 4; ++i) p[nb][i] = w[sub][nb][i];
+      if constexpr (Y::k8) {
+        const float vs[2] = {scales[kStep + sub * 16 + gid], scales[kStep + sub * 16 + gid + 8]};
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            for (int t = 0; t < 4; ++t) {
-              // position k of the step: its V is held by the quad's lane t
-              const int k = 2 * t + (i & 1) + 8 * (i >> 1);
-              float pk[NB][2];
+        for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-              for (int nb = 0; nb < NB; ++nb)
+          for (int i = 0; i < 4; ++i) {
+            p[nb][i] = __fmul_rn(p[nb][i], vs[i >> 1]);
+            // (a row out of sight keeps the weight 0 whatever its scale)
+            if (!whole && s[sub][nb][i] == -INFINITY) p[nb][i] = 0.0f;
+          }
+      }
+      uint32_t vr[4][Y::vChunks][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+      const unsigned char* sv =
+          st + sub * (Y::kBytes + Y::vAll) + Y::kBytes + lane * Y::vBytes;
 #pragma unroll
-                for (int e = 0; e < 2; ++e)
-                  pk[nb][e] = __shfl_sync(0xFFFFFFFFu, p[nb][e + 2 * (i >> 1)], (k & 7) * 4 + tig);
+      for (int i = 0; i < 4; ++i)
 #pragma unroll
-              for (int j = 0; j < Y::vChunks; ++j)
+        for (int j = 0; j < Y::vChunks; ++j) {
+          const unsigned char* at = sv + (i * Y::vChunks + j) * (Y::vBytes * 32);
+          if constexpr (Y::vBytes == 16) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(at);
+            vr[i][j][0] = q4.x;
+            vr[i][j][1] = q4.y;
+            vr[i][j][2] = q4.z;
+            vr[i][j][3] = q4.w;
+          } else {
+            const uint2 q2 = *reinterpret_cast<const uint2*>(at);
+            vr[i][j][0] = q2.x;
+            vr[i][j][1] = q2.y;
+          }
+        }
+      uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
-                for (int w = 0; w < Y::vWords; ++w) {
-                  const uint32_t vw = __shfl_sync(0xFFFFFFFFu, vr[i][j][w], (lane & ~3) | t);
-                  const int mt = j * Y::vWords + w;
+      for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                  for (int half = 0; half < 2; ++half) {
-                    const float val = half ? bf_hi(vw) : bf_lo(vw);
-                    if ((__float_as_uint(val) & 0x7F800000u) != 0x7F800000u) continue;
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                      for (int e = 0; e < 2; ++e)
-                        if (pk[nb][e] != 0.0f)
-                          acc[nb][mt][half * 2 + e] = __fmaf_rn(pk[nb][e], val, acc[nb][mt][half * 2 + e]);
-                  }
-                }
-            }
+        for (int i = 0; i < 2; ++i) {
+          const uint32_t hi = pack_bf2(p[nb][2 * i], p[nb][2 * i + 1]);
+          const uint32_t lo2 = pack_bf2(__fsub_rn(p[nb][2 * i], bf_lo(hi)),
+                                        __fsub_rn(p[nb][2 * i + 1], bf_hi(hi)));
+          ph[nb][i] = transpose8(hi);
+          pl[nb][i] = transpose8(lo2);
+        }
+      if constexpr (!Y::k8) {
+        // values that must not meet a zero weight (rare: a step that masks, with such a value)
+        if (!whole) {
+          bool bad = false;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < Y::vChunks; ++j)
 #pragma unroll
-              for (int w = 0; w < Y::vWords; ++w) {
-                uint32_t z = vr[i][j][w];
-                if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
-                if ((z & 0x7F800000u) == 0x7F800000u) z &= 0x0000FFFFu;
-                vr[i][j][w] = z;
+              for (int w = 0; w < Y::vWords; ++w) bad |= nonfinite2(vr[i][j][w]);
+          if (__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              for (int t = 0; t < 4; ++t) {
+                // position k of the step: its V is held by the quad's lane t
+                const int k = 2 * t + (i & 1) + 8 * (i >> 1);
+                float pk[NB][2];
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                  for (int e = 0; e < 2; ++e)
+                    pk[nb][e] = __shfl_sync(0xFFFFFFFFu, p[nb][e + 2 * (i >> 1)], (k & 7) * 4 + tig);
+#pragma unroll
+                for (int j = 0; j < Y::vChunks; ++j)
+#pragma unroll
+                  for (int w = 0; w < Y::vWords; ++w) {
+                    const uint32_t vw = __shfl_sync(0xFFFFFFFFu, vr[i][j][w], (lane & ~3) | t);
+                    const int mt = j * Y::vWords + w;
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                      const float val = half ? bf_hi(vw) : bf_lo(vw);
+                      if ((__float_as_uint(val) & 0x7F800000u) != 0x7F800000u) continue;
+#pragma unroll
+                      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                          if (pk[nb][e] != 0.0f)
+                            acc[nb][mt][half * 2 + e] = __fmaf_rn(pk[nb][e], val, acc[nb][mt][half * 2 + e]);
+                    }
+                  }
               }
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int j = 0; j < Y::vChunks; ++j)
+#pragma unroll
+                for (int w = 0; w < Y::vWords; ++w) {
+                  uint32_t z = vr[i][j][w];
+                  if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
+                  if ((z & 0x7F800000u) == 0x7F800000u) z &= 0x0000FFFFu;
+                  vr[i][j][w] = z;
+                }
+          }
         }
       }
-    }
 #pragma unroll
-    for (int mt = 0; mt < KCH; ++mt) {
-      uint32_t a[4];
-      if constexpr (Y::k8) {
-        const int w = mt >> 1, i0 = (mt & 1) * 2;   // word and first byte of dims 2 mt, 2 mt + 1
-        a[0] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0);
-        a[1] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0 + 1);
-        a[2] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0);
-        a[3] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0 + 1);
-      } else {
-        const int j = mt / Y::vWords, w = mt % Y::vWords;
-        a[0] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x5410);
-        a[1] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x7632);
-        a[2] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x5410);
-        a[3] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x7632);
-      }
+      for (int mt = 0; mt < KCH; ++mt) {
+        uint32_t a[4];
+        if constexpr (Y::k8) {
+          const int w = mt >> 1, i0 = (mt & 1) * 2;   // word and first byte of dims 2 mt, 2 mt + 1
+          a[0] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0);
+          a[1] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0 + 1);
+          a[2] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0);
+          a[3] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0 + 1);
+        } else {
+          const int j = mt / Y::vWords, w = mt % Y::vWords;
+          a[0] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x5410);
+          a[1] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x7632);
+          a[2] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x5410);
+          a[3] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x7632);
+        }
 #pragma unroll
-      for (int nb = 0; nb < NB; ++nb) {
-        mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], ph[nb][0], ph[nb][1]);
-        mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+        for (int nb = 0; nb < NB; ++nb) {
+          mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], ph[nb][0], ph[nb][1]);
+          mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+        }
       }
     }
 #pragma unroll
@@ -528,12 +576,13 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     }
 }
 
-// A CTA of four warps per (layer, token, query head): the row's parts joined, warp w taking
-// parts w, w + 4, ..., its loads all under way together. A part that saw nothing has the
+// The parts of every (layer, token, query head) row joined. kSplit: a CTA of four warps a row,
+// warp w taking parts w, w + 4, ..., their loads all under way together (few rows: latency);
+// else a warp a row, four rows a CTA (many rows: bandwidth). A part that saw nothing has the
 // maximum -inf and weight 0, and is not read.
 constexpr int kJoinWarps = 4;
 
-template <int D>
+template <int D, bool kSplit>
 __global__ void __launch_bounds__(kJoinWarps * 32)
 chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
                   const __grid_constant__ ChunkUnits units, int R) {
@@ -543,8 +592,10 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   __shared__ float s_l[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int n_tok = list.row[list.n];
-  const int gq = static_cast<int>(blockIdx.x % A.nq);
-  const int lt = static_cast<int>(blockIdx.x / A.nq);
+  const unsigned n = kSplit ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
+  const int gq = static_cast<int>(n % A.nq);
+  const int lt = static_cast<int>(n / A.nq);
+  if (!kSplit && lt >= A.nl * n_tok) return;
   const int t = lt % n_tok, li = lt / n_tok;
   int x = 0;
   for (int hi = list.n - 1; x < hi;) {
@@ -572,7 +623,7 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
   for (int d = 0; d < DPL; ++d) acc[d] = 0.0f;
 #pragma unroll 8
-  for (int i = warp; i < ns; i += kJoinWarps) {
+  for (int i = kSplit ? warp : 0; i < ns; i += kSplit ? kJoinWarps : 1) {
     const int64_t pr = (u0 + i) * R + rt;
     const float2 ml = *reinterpret_cast<const float2*>(A.part_ml + pr * 2);
     const bool some = ml.x != -INFINITY;
@@ -594,27 +645,27 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
     for (int d = 0; d < DPL; ++d) acc[d] = __fmaf_rn(q[d], w, acc[d]);
   }
+  nan = __any_sync(0xFFFFFFFFu, nan);
+  if constexpr (kSplit) {
 #pragma unroll
-  for (int d = 0; d < DPL; ++d) s_acc[warp][lane * DPL + d] = acc[d];
-  if (lane == 0) s_l[warp] = l;
-  const bool any_nan = __syncthreads_or(nan);
-  if (warp != 0) return;
-  l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
-  if (any_nan) l = __uint_as_float(0x7FC00000u);
+    for (int d = 0; d < DPL; ++d) s_acc[warp][lane * DPL + d] = acc[d];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    if (warp != 0) return;
+    l = (s_l[0] + s_l[1]) + (s_l[2] + s_l[3]);
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) {
+      const int c = lane * DPL + d;
+      acc[d] = (s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c]);
+    }
+  }
+  if (nan) l = __uint_as_float(0x7FC00000u);
   const int64_t row =
       (static_cast<int64_t>(li) * A.tokens + list.tok[x] + t - list.row[x]) * A.nq + gq;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
   uint32_t* out = reinterpret_cast<uint32_t*>(A.out + row * D + lane * DPL);
 #pragma unroll
-  for (int d = 0; d < DPL; d += 2) {
-    float y[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int c = lane * DPL + d + e;
-      y[e] = ((s_acc[0][c] + s_acc[1][c]) + (s_acc[2][c] + s_acc[3][c])) * inv;
-    }
-    out[d / 2] = pack_bf2(y[0], y[1]);
-  }
+  for (int d = 0; d < DPL; d += 2) out[d / 2] = pack_bf2(acc[d] * inv, acc[d + 1] * inv);
   if (lane == 0 && A.lse)
     A.lse[row] = l == 0.0f ? -INFINITY : (mx + log2f(l)) * 0.69314718055994530942f;
 }
@@ -650,11 +701,13 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
 
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st) {
-  const unsigned grid = static_cast<unsigned>(a.nl) * list.row[list.n] * a.nq;
-  if (a.g.D == 128)
-    return launch_after(chunk_join_kernel<128>, grid, kJoinWarps * 32, 0, st, a, list, units,
-                        rows_per_tile);
-  return launch_after(chunk_join_kernel<64>, grid, kJoinWarps * 32, 0, st, a, list, units,
+  const unsigned rows = static_cast<unsigned>(a.nl) * list.row[list.n] * a.nq;
+  // a warp a row from 8192 rows on (the machine holds 152 x 64 warps)
+  const bool split = rows < 8192;
+  const unsigned grid = split ? rows : (rows + kJoinWarps - 1) / kJoinWarps;
+  auto* wide = split ? chunk_join_kernel<128, true> : chunk_join_kernel<128, false>;
+  auto* narrow = split ? chunk_join_kernel<64, true> : chunk_join_kernel<64, false>;
+  return launch_after(a.g.D == 128 ? wide : narrow, grid, kJoinWarps * 32, 0, st, a, list, units,
                       rows_per_tile);
 }
 

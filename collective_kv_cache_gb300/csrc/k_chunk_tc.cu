@@ -732,6 +732,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     tc_fence_before();
   }
   __syncthreads();
+  pdl_trigger();
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&sh->tmem);
 

@@ -193,28 +193,53 @@ bool bf16_map(const td_ctx* c, const ChunkArgs& a, const PoolDev& pool, int* box
 
 // Cuts every tile's visible positions (in steps of `step` positions) into parts of one length
 // and fills base, nsplit, span and direct; the number of units, or -1. tiles(x), seen(x): a
-// sequence's tiles of query rows and the steps that one of them sees at most. `slots` units
-// run at once; a unit costs its steps and `fixed` more. The length is the one with the least
-// waves x cost among the divisions of the longest tile.
+// sequence's tiles of query rows and the steps that one of them sees at most. The length is
+// the one with the least estimated time among the divisions of the longest tile.
+struct Cost {
+  int64_t slots;     // units that run at once
+  int64_t heads;     // kv heads x layers
+  double step_us;    // a step of a unit, with all slots in use
+  int fixed;         // what a unit costs besides its steps, in steps
+  int least;         // steps per unit, at least
+  double row_bytes;  // of partial results per part, over all rows of the launch
+};
+
 template <typename Tiles, typename Seen>
-int64_t cut(const ChunkList& list, int64_t slots, int64_t heads, int fixed, int least, Tiles tiles,
-            Seen seen, int step, ChunkArgs* a, ChunkUnits* units) {
-  int64_t longest = 1;
-  for (int x = 0; x < list.n; ++x) longest = std::max<int64_t>(longest, seen(x));
-  int64_t best = 0, best_cost = INT64_MAX, last = 0;
+int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int step,
+            ChunkArgs* a, ChunkUnits* units) {
+  int64_t longest = 1, total = 0;
+  for (int x = 0; x < list.n; ++x) {
+    longest = std::max<int64_t>(longest, seen(x));
+    total += tiles(x) * seen(x);
+  }
+  int64_t best = longest, last = 0;
+  double best_us = 0.0;
   for (int64_t k = 1; k <= 256; k = k < 16 ? k + 1 : k + k / 8) {
-    const int64_t span = std::max<int64_t>((longest + k - 1) / k, std::min<int64_t>(least, longest));
+    const int64_t span = std::max<int64_t>((longest + k - 1) / k,
+                                           std::min<int64_t>(cost.least, longest));
     if (span == last) continue;
     last = span;
-    int64_t n = 0;
-    for (int x = 0; x < list.n; ++x) n += tiles(x) * ((seen(x) + span - 1) / span);
-    n *= heads;
-    const int64_t cost = (n + slots - 1) / slots * (span + fixed) + (k > 1 ? fixed : 0);
-    if (cost < best_cost) {
-      best_cost = cost;
+    int64_t n = 0, most = 1;
+    for (int x = 0; x < list.n; ++x) {
+      const int64_t ns = (seen(x) + span - 1) / span;
+      n += tiles(x) * ns;
+      most = std::max(most, ns);
+    }
+    n *= cost.heads;
+    // one wave: its longest unit; more: the slots' share of the work and half a unit of tail
+    const double unit = static_cast<double>(span + cost.fixed);
+    double us = cost.step_us *
+                (n <= cost.slots
+                     ? unit
+                     : std::max(unit, (static_cast<double>(total) * cost.heads +
+                                       static_cast<double>(n) * cost.fixed) / cost.slots + unit / 2));
+    // joining: a launch, and the parts written and read once
+    if (most > 1) us += 4.0 + 2.0 * cost.row_bytes * most / 5e6;
+    if (k == 1 || us < best_us) {
+      best_us = us;
       best = span;
     }
-    if (span <= least) break;
+    if (span <= cost.least) break;
   }
   a->span = static_cast<int>(best * step);
   a->direct = 1;
@@ -228,7 +253,7 @@ int64_t cut(const ChunkList& list, int64_t slots, int64_t heads, int fixed, int 
     units->nsplit[x] = static_cast<int32_t>(ns);
     units->base[x + 1] = static_cast<int32_t>(sum);
   }
-  return sum * heads > INT32_MAX ? -1 : sum * heads;
+  return sum * cost.heads > INT32_MAX ? -1 : sum * cost.heads;
 }
 
 // Positions that a tile of `rows` query rows of sequence x sees, at most.
@@ -238,16 +263,26 @@ int64_t seen_positions(const ChunkList& list, const ChunkArgs& a, int x, int row
   return std::min<int64_t>(all, static_cast<int64_t>(a.window) + a.n_sink + (rows - 1) / a.G + 1);
 }
 
+// Bytes of one part of every query row's partial result.
+double partial_bytes(const ChunkList& list, const ChunkArgs& a) {
+  return 4.0 * (a.g.D + 2) * a.nl * a.nq * list.row[list.n];
+}
+
 int64_t plan_rows(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
                   int* rows) {
   int64_t most = 0;
   for (int x = 0; x < list.n; ++x)
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = most <= 8 ? 8 : 16;
+  // 12 warps an SM; a step of 32 positions of K and V (16 KB in bf16 at D = 128) at 6 TB/s
+  const double bytes = 2.0 * 32 * a->g.D * (a->scale ? 1 : 2);
+  const int64_t slots = static_cast<int64_t>(c->sm_count) * 12;
+  const Cost cost{slots, static_cast<int64_t>(a->g.H) * a->nl, bytes * slots / 6e6, 4, 4,
+                  partial_bytes(list, *a)};
   return cut(
-      list, static_cast<int64_t>(c->sm_count) * 12, static_cast<int64_t>(a->g.H) * a->nl, 8, 8,
+      list, cost,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
-      [&](int x) { return (seen_positions(list, *a, x, R) + 15) / 16; }, 16, a, units);
+      [&](int x) { return (seen_positions(list, *a, x, R) + 31) / 32; }, 32, a, units);
 }
 
 int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
@@ -256,8 +291,11 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
   for (int x = 0; x < list.n; ++x)
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = a->rows_cta = most <= 128 ? 128 : 256;
+  // one CTA an SM; a KV tile's products and softmax (1.4 us at D = 128)
+  const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, a->g.D == 128 ? 1.4 : 0.8, 3,
+                  2, partial_bytes(list, *a)};
   return cut(
-      list, c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, 2, 2,
+      list, cost,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
       // a window's positions may straddle one tile more, the first ones' another
       [&](int x) {
