@@ -63,6 +63,14 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, bool live) 
                : "memory");
 }
 
+// Four 8 x 8 matrices of 16-bit values, transposed: lane l names row l & 7 of matrix l >> 3.
+__device__ __forceinline__ void ldmatrix_x4_trans(uint32_t* r, uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -102,11 +110,10 @@ template <int D, int kKind, int NB>
 __global__ void __launch_bounds__(32, NB == 1 ? 12 : 8)
 chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
                   const __grid_constant__ ChunkUnits units) {
-  pdl_wait();
   using Y = Layout<D, kKind>;
   constexpr int KCH = D / 16;
   constexpr int R = 8 * NB;
-  __shared__ __align__(16) unsigned char s_ring[Y::depth][Y::stage];
+  __shared__ __align__(128) unsigned char s_ring[Y::depth][Y::stage];
   const int lane = threadIdx.x;
   const int gid = lane >> 2, tig = lane & 3;
   const int total = units.base[list.n];
@@ -149,6 +156,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const float* vscale = Y::k8 ? A.scale + vplane * A.g.H + h : nullptr;
   const int row_bytes = E * (Y::k8 ? 1 : 2);
 
+  pdl_wait();     // (above, the kernel's own arguments only)
   auto position = [&](int v) { return v < sinks ? v : lo + v - sinks; };
   // lane l reads the table for the position of index v + l (16 positions a step: lanes l and
   // l + 16 the same), ahead of its use; the page row is made from it when the copies start
@@ -201,7 +209,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
         for (int j = 0; j < Y::vChunks; ++j) {
           const uint32_t to = dv + (i * Y::vChunks + j) * (Y::vBytes * 32);
-          if constexpr (Y::vBytes == 16) {
+          if constexpr (!Y::k8) {
+            copy16(to ^ ((i & 1) << 6), src + j * 128, live);
+          } else if constexpr (Y::vBytes == 16) {
             copy16(to, src + j * 128, live);
           } else {
             // 8 neighbouring codes (D = 64)
@@ -273,7 +283,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       const int ahead = v + (Y::depth - 1) * kStep;
       const int into = slot == 0 ? Y::depth - 1 : slot - 1;
       uint32_t b = 0;
-      if constexpr (Y::k8) __syncwarp();     // the slot's scales have been read by all lanes
+      __syncwarp();                          // the slot has been read by all lanes
       if (ahead < v1) {
         b = start_copies(ahead, into);
         look_up(ahead + kStep);
@@ -282,7 +292,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       bits[Y::depth - 1] = b;
     }
     cp_async_wait<Y::depth - 1>();
-    if constexpr (Y::k8) __syncwarp();       // (the scales are the other lanes' copies)
+    __syncwarp();                            // scales and bf16 V: the other lanes' copies too
     const uint32_t have = bits[0];
     const unsigned char* st = s_ring[slot];
     const float* scales = reinterpret_cast<const float*>(st + Y::codes);
@@ -297,9 +307,11 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
         for (int j = 0; j < Y::kChunks; ++j)
           kr[i][j] = *reinterpret_cast<const uint4*>(sk + (i * Y::kChunks + j) * 512);
+      float s2[NB][4];                       // every other product: two chains
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
-        s[sub][nb][0] = s[sub][nb][1] = s[sub][nb][2] = s[sub][nb][3] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[sub][nb][i] = s2[nb][i] = 0.0f;
 #pragma unroll
       for (int kc = 0; kc < KCH; ++kc) {
         uint32_t a[4];
@@ -321,8 +333,13 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
         }
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)
-          mma_bf16(s[sub][nb], a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
+          mma_bf16(kc & 1 ? s2[nb] : s[sub][nb], a[0], a[1], a[2], a[3], qf[nb][kc][0],
+                   qf[nb][kc][1]);
       }
+#pragma unroll
+      for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[sub][nb][i] = __fadd_rn(s[sub][nb][i], s2[nb][i]);
     }
     // does every row of the tile see every position of the step?
     const int pa = position(v), pb = position(v + kStep - 1);
@@ -410,26 +427,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
             if (!whole && s[sub][nb][i] == -INFINITY) p[nb][i] = 0.0f;
           }
       }
-      uint32_t vr[4][Y::vChunks][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
-      const unsigned char* sv =
-          st + sub * (Y::kBytes + Y::vAll) + Y::kBytes + lane * Y::vBytes;
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < Y::vChunks; ++j) {
-          const unsigned char* at = sv + (i * Y::vChunks + j) * (Y::vBytes * 32);
-          if constexpr (Y::vBytes == 16) {
-            const uint4 q4 = *reinterpret_cast<const uint4*>(at);
-            vr[i][j][0] = q4.x;
-            vr[i][j][1] = q4.y;
-            vr[i][j][2] = q4.z;
-            vr[i][j][3] = q4.w;
-          } else {
-            const uint2 q2 = *reinterpret_cast<const uint2*>(at);
-            vr[i][j][0] = q2.x;
-            vr[i][j][1] = q2.y;
-          }
-        }
+      const unsigned char* sv = st + sub * (Y::kBytes + Y::vAll) + Y::kBytes;
       uint32_t ph[NB][2], pl[NB][2];
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -442,80 +440,100 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           pl[nb][i] = transpose8(lo2);
         }
       if constexpr (!Y::k8) {
-        // values that must not meet a zero weight (rare: a step that masks, with such a value)
+        // element (position k, dim d) of V in the ring
+        auto v_at = [&](int k, int d) {
+          const int i = (k & 1) + 2 * (k >> 3), ch = d >> 3;
+          return const_cast<unsigned char*>(sv) + (i * Y::vChunks + (ch >> 3)) * 512 +
+                 ((((ch & 7) * 4 + ((k & 7) >> 1)) * 16) ^ ((i & 1) << 6)) + (d & 7) * 2;
+        };
+        // values that must not meet a zero weight (rare: a step that masks, with such a value):
+        // their terms are added to the rows that see them, and they leave the product
         if (!whole) {
           bool bad = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-#pragma unroll
-            for (int j = 0; j < Y::vChunks; ++j)
-#pragma unroll
-              for (int w = 0; w < Y::vWords; ++w) bad |= nonfinite2(vr[i][j][w]);
+          for (int i = 0; i < 4 * Y::vChunks; ++i) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(sv + i * 512 + lane * 16);
+            bad |= nonfinite2(q4.x) || nonfinite2(q4.y) || nonfinite2(q4.z) || nonfinite2(q4.w);
+          }
           if (__any_sync(0xFFFFFFFFu, bad)) {
+#pragma unroll 1
+            for (int k = 0; k < 16; ++k) {
+              float pk[NB][2];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-              for (int t = 0; t < 4; ++t) {
-                // position k of the step: its V is held by the quad's lane t
-                const int k = 2 * t + (i & 1) + 8 * (i >> 1);
-                float pk[NB][2];
+              for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                  for (int e = 0; e < 2; ++e)
-                    pk[nb][e] = __shfl_sync(0xFFFFFFFFu, p[nb][e + 2 * (i >> 1)], (k & 7) * 4 + tig);
-#pragma unroll
-                for (int j = 0; j < Y::vChunks; ++j)
-#pragma unroll
-                  for (int w = 0; w < Y::vWords; ++w) {
-                    const uint32_t vw = __shfl_sync(0xFFFFFFFFu, vr[i][j][w], (lane & ~3) | t);
-                    const int mt = j * Y::vWords + w;
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                      const float val = half ? bf_hi(vw) : bf_lo(vw);
-                      if ((__float_as_uint(val) & 0x7F800000u) != 0x7F800000u) continue;
-#pragma unroll
-                      for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                          if (pk[nb][e] != 0.0f)
-                            acc[nb][mt][half * 2 + e] = __fmaf_rn(pk[nb][e], val, acc[nb][mt][half * 2 + e]);
-                    }
-                  }
-              }
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-#pragma unroll
-              for (int j = 0; j < Y::vChunks; ++j)
-#pragma unroll
-                for (int w = 0; w < Y::vWords; ++w) {
-                  uint32_t z = vr[i][j][w];
-                  if ((z & 0x7F80u) == 0x7F80u) z &= 0xFFFF0000u;
-                  if ((z & 0x7F800000u) == 0x7F800000u) z &= 0x0000FFFFu;
-                  vr[i][j][w] = z;
+                for (int e = 0; e < 2; ++e) {
+                  const float mine = k < 8 ? p[nb][e] : p[nb][e + 2];
+                  pk[nb][e] = __shfl_sync(0xFFFFFFFFu, mine, (k & 7) * 4 + tig);
                 }
+#pragma unroll
+              for (int mt = 0; mt < KCH; ++mt)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                  const uint32_t b = *reinterpret_cast<const uint16_t*>(v_at(k, mt * 16 + half * 8 + gid));
+                  if ((b & 0x7F80u) != 0x7F80u) continue;
+#pragma unroll
+                  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                      if (pk[nb][e] != 0.0f)
+                        acc[nb][mt][half * 2 + e] =
+                            __fmaf_rn(pk[nb][e], __uint_as_float(b << 16), acc[nb][mt][half * 2 + e]);
+                }
+            }
+            __syncwarp();
+            uint16_t* mine = reinterpret_cast<uint16_t*>(const_cast<unsigned char*>(sv)) + lane * 8;
+#pragma unroll 1
+            for (int i = 0; i < 4 * Y::vChunks * 8; ++i) {
+              uint16_t* at = mine + (i >> 3) * 256 + (i & 7);
+              if ((*at & 0x7F80u) == 0x7F80u) *at = 0;
+            }
+            __syncwarp();
           }
         }
-      }
+        // V^T's fragments: dims as rows, transposed as they are read. Lane l names a row of 8
+        // dims: position (l & 7) + 8 (l >> 4), dims 16 mt + 8 ((l >> 3) & 1)
+        const uint32_t v0a = smem_u32(v_at((lane & 7) + 8 * (lane >> 4), 8 * ((lane >> 3) & 1)));
 #pragma unroll
-      for (int mt = 0; mt < KCH; ++mt) {
-        uint32_t a[4];
-        if constexpr (Y::k8) {
-          const int w = mt >> 1, i0 = (mt & 1) * 2;   // word and first byte of dims 2 mt, 2 mt + 1
-          a[0] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0);
-          a[1] = pair_bf16<kKind>(vr[0][0][w], vr[1][0][w], i0 + 1);
-          a[2] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0);
-          a[3] = pair_bf16<kKind>(vr[2][0][w], vr[3][0][w], i0 + 1);
-        } else {
-          const int j = mt / Y::vWords, w = mt % Y::vWords;
-          a[0] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x5410);
-          a[1] = __byte_perm(vr[0][j][w], vr[1][j][w], 0x7632);
-          a[2] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x5410);
-          a[3] = __byte_perm(vr[2][j][w], vr[3][j][w], 0x7632);
+        for (int mt = 0; mt < KCH; ++mt) {
+          uint32_t a[4];
+          // 16 dims are two vectors on: 128 bytes, 512 for every 64 dims
+          ldmatrix_x4_trans(a, v0a + (mt >> 2) * 512 + (mt & 3) * 128);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], ph[nb][0], ph[nb][1]);
+            mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+          }
+        }
+      } else {
+        uint32_t vr[4][Y::vWords];   // rows 2 tig, 2 tig + 1, 2 tig + 8, 2 tig + 9
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const unsigned char* at = sv + lane * Y::vBytes + i * (Y::vBytes * 32);
+          if constexpr (Y::vBytes == 16) {
+            const uint4 q4 = *reinterpret_cast<const uint4*>(at);
+            vr[i][0] = q4.x;
+            vr[i][1] = q4.y;
+            vr[i][2] = q4.z;
+            vr[i][3] = q4.w;
+          } else {
+            const uint2 q2 = *reinterpret_cast<const uint2*>(at);
+            vr[i][0] = q2.x;
+            vr[i][1] = q2.y;
+          }
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) {
-          mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], ph[nb][0], ph[nb][1]);
-          mma_bf16(acc[nb][mt], a[0], a[1], a[2], a[3], pl[nb][0], pl[nb][1]);
+        for (int mt = 0; mt < KCH; ++mt) {
+          const int w8 = mt >> 1, i0 = (mt & 1) * 2;   // word and first byte of dims 2 mt, 2 mt + 1
+          const uint32_t a0 = pair_bf16<kKind>(vr[0][w8], vr[1][w8], i0);
+          const uint32_t a1 = pair_bf16<kKind>(vr[0][w8], vr[1][w8], i0 + 1);
+          const uint32_t a2 = pair_bf16<kKind>(vr[2][w8], vr[3][w8], i0);
+          const uint32_t a3 = pair_bf16<kKind>(vr[2][w8], vr[3][w8], i0 + 1);
+#pragma unroll
+          for (int nb = 0; nb < NB; ++nb) {
+            mma_bf16(acc[nb][mt], a0, a1, a2, a3, ph[nb][0], ph[nb][1]);
+            mma_bf16(acc[nb][mt], a0, a1, a2, a3, pl[nb][0], pl[nb][1]);
+          }
         }
       }
     }
@@ -524,7 +542,8 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     slot = slot + 1 == Y::depth ? 0 : slot + 1;
   }
 
-  // the lane's dims: vector j holds dims (j * 8 + gid) * vDims + 0 .. vDims - 1
+  // The lane's dims of acc[mt]: bf16 16 mt + gid and 16 mt + gid + 8; 8-bit gid vDims + 2 mt
+  // and the next one.
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -535,39 +554,53 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
       const int rt = nb * 8 + 2 * tig + e;
       const int r = r0 + rt;
-      if (r >= rows) continue;
+      const bool live = r < rows;
       if (A.direct) {
         const int tok = r / A.G;
         const int64_t row =
             (static_cast<int64_t>(li) * A.tokens + list.tok[x] + tok) * A.nq + h * A.G +
             (r - tok * A.G);
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;    // a row that sees nothing: zeros
+        uint16_t* out = A.out + row * D;
+        if constexpr (Y::k8) {
 #pragma unroll
-        for (int j = 0; j < Y::vChunks; ++j)
-#pragma unroll
-          for (int w = 0; w < Y::vDims / 8; ++w) {
+          for (int w8 = 0; w8 < Y::vDims / 8; ++w8) {
             uint32_t o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int mt = j * (Y::vDims / 2) + w * 4 + i;
-              o[i] = pack_bf2(acc[nb][mt][e] * inv, acc[nb][mt][2 + e] * inv);
-            }
-            st16(A.out + row * D + (j * 8 + gid) * Y::vDims + w * 8,
-                 make_uint4(o[0], o[1], o[2], o[3]));
+            for (int i = 0; i < 4; ++i)
+              o[i] = pack_bf2(acc[nb][w8 * 4 + i][e] * inv, acc[nb][w8 * 4 + i][2 + e] * inv);
+            if (live) st16(out + gid * Y::vDims + w8 * 8, make_uint4(o[0], o[1], o[2], o[3]));
           }
-        if (gid == 0 && A.lse)
+        } else {
+          // neighbouring dims are in the neighbouring quad: even ones take the pair of the
+          // first 8 dims, odd ones that of the second
+          const bool odd = gid & 1;
+#pragma unroll
+          for (int mt = 0; mt < KCH; ++mt) {
+            const float f0 = acc[nb][mt][e] * inv, f1 = acc[nb][mt][2 + e] * inv;
+            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f0 : f1, 4);
+            const uint32_t o = odd ? pack_bf2(got, f1) : pack_bf2(f0, got);
+            if (live)
+              *reinterpret_cast<uint32_t*>(out + mt * 16 + (odd ? 7 + gid : gid)) = o;
+          }
+        }
+        if (live && gid == 0 && A.lse)
           A.lse[row] = l == 0.0f ? -INFINITY : (m_run[nb][e] + log2f(l)) * 0.69314718055994530942f;
-      } else {
+      } else if (live) {
         float* po = A.part_o + (unit * R + rt) * D;
+        if constexpr (Y::k8) {
 #pragma unroll
-        for (int j = 0; j < Y::vChunks; ++j)
+          for (int w8 = 0; w8 < Y::vDims / 4; ++w8)
+            *reinterpret_cast<float4*>(po + gid * Y::vDims + w8 * 4) =
+                make_float4(acc[nb][w8 * 2][e], acc[nb][w8 * 2][2 + e], acc[nb][w8 * 2 + 1][e],
+                            acc[nb][w8 * 2 + 1][2 + e]);
+        } else {
 #pragma unroll
-          for (int w = 0; w < Y::vDims / 4; ++w) {
-            const int mt = j * (Y::vDims / 2) + w * 2;
-            *reinterpret_cast<float4*>(po + (j * 8 + gid) * Y::vDims + w * 4) =
-                make_float4(acc[nb][mt][e], acc[nb][mt][2 + e], acc[nb][mt + 1][e],
-                            acc[nb][mt + 1][2 + e]);
+          for (int mt = 0; mt < KCH; ++mt) {
+            po[mt * 16 + gid] = acc[nb][mt][e];
+            po[mt * 16 + gid + 8] = acc[nb][mt][2 + e];
           }
+        }
         if (gid == 0) {
           A.part_ml[(unit * R + rt) * 2] = m_run[nb][e];
           A.part_ml[(unit * R + rt) * 2 + 1] = l;

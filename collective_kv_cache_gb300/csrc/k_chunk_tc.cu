@@ -683,11 +683,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   constexpr bool k8 = kKind != kCacheBf16;
   using PL = Plan<D, k8>;
   extern __shared__ unsigned char s_dyn[];
-  pdl_wait();
   const Work w = work_of(A, list, units);
   const int tid = threadIdx.x, lane = tid & 31;
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);    // known to be the warp's
   if (w.n <= 0) {           // a part past the visible positions of its rows: empty
+    pdl_wait();
     for (int rr = tid; rr < w.nrows; rr += PL::kThreads) {
       A.part_ml[(w.unit * A.rows_cta + rr) * 2] = -INFINITY;
       A.part_ml[(w.unit * A.rows_cta + rr) * 2 + 1] = 0.0f;
@@ -731,6 +731,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
   }
+  pdl_wait();               // (above, the kernel's own arguments and the block's own memory)
   __syncthreads();
   pdl_trigger();
   tc_fence_after();
