@@ -7,9 +7,11 @@
 // 8-bit pages hold k = ks_p * code and v = vs_p * code: the codes are exact in bf16, so they
 // go through the same products, with ks_p on the score and vs_p on the weight.
 //
-// One warp takes a unit = (layer, kv head, tile of 8 or 16 query rows, `span` of the tile's
-// visible positions), 16 or 32 positions a step; the rows of a tile are (token, head of the group)
-// pairs, so the group's heads share every read. It is bound by the pages' bytes. Products are
+// A block takes a unit = (layer, kv head, tile of 8 or 16 query rows, `span` of the tile's
+// visible positions), its four warps every fourth step of 16 or 32 positions each; they are
+// joined in shared memory at the end, so that a unit leaves one partial result (a warp a unit
+// left four times as many, whose join took 7.5 us of a 31 us call). The rows of a tile are
+// (token, head of the group) pairs, so the group's heads share every read. It is bound by the pages' bytes. Products are
 // mma.sync m16n8k16, positions or dims as the 16 rows, query rows as the 8 columns. Each lane
 // copies exactly the 16-byte vectors of K and V that its own fragments are made of (cp.async,
 // rows out of sight zero-filled) into a ring of its own, and reads them back without any
@@ -106,15 +108,19 @@ struct Layout {
 
 }  // namespace
 
+constexpr int kWarps = 4;
+
 template <int D, int kKind, int NB>
-__global__ void __launch_bounds__(32, NB == 1 ? 12 : 8)
+__global__ void __launch_bounds__(kWarps * 32, NB == 1 ? 3 : 2)
 chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
                   const __grid_constant__ ChunkUnits units) {
   using Y = Layout<D, kKind>;
   constexpr int KCH = D / 16;
   constexpr int R = 8 * NB;
-  __shared__ __align__(128) unsigned char s_ring[Y::depth][Y::stage];
-  const int lane = threadIdx.x;
+  extern __shared__ __align__(128) unsigned char s_dyn[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  unsigned char (*s_ring)[Y::stage] =
+      reinterpret_cast<unsigned char (*)[Y::stage]>(s_dyn + warp * (Y::depth * Y::stage));
   const int gid = lane >> 2, tig = lane & 3;
   const int total = units.base[list.n];
   const int64_t unit = blockIdx.x;
@@ -140,8 +146,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const int lo = A.window ? max(0, p_first - A.window + 1) : 0;
   const int sinks = A.window ? min(A.n_sink, lo) : 0;
   const int n_vis = sinks + p_last + 1 - lo;
-  const int v0 = split * A.span;
-  const int v1 = min(v0 + A.span, n_vis);
+  constexpr int kStep = Y::step, kHop = kWarps * Y::step;
+  const int v1 = min((split + 1) * A.span, n_vis);
+  const int v0 = split * A.span + warp * kStep;      // this warp's first step
 
   const PoolDev& P = A.pool;
   const int64_t plane = (static_cast<int64_t>(A.layer_begin + li) * 2) * P.num_pages * P.P;
@@ -160,7 +167,6 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   auto position = [&](int v) { return v < sinks ? v : lo + v - sinks; };
   // lane l reads the table for the position of index v + l (16 positions a step: lanes l and
   // l + 16 the same), ahead of its use; the page row is made from it when the copies start
-  constexpr int kStep = Y::step;
   constexpr uint32_t kAll = kStep == 32 ? 0xFFFFFFFFu : 0xFFFFu;
   int ref_page = -1, ref_slot = 0;
   auto look_up = [&](int v) {
@@ -171,7 +177,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     if (lp < P.max_lp) ref_page = __ldg(P.bt + static_cast<int64_t>(list.agent[x]) * P.max_lp + lp);
   };
   // starts the copies of the step at v (looked up before); returns its mapped positions' bits
-  const uint32_t ring = smem_u32(s_ring);
+  const uint32_t ring = smem_u32(s_ring);   // (128-byte aligned: V's rows are swizzled in it)
   const uint8_t* klane = kbase + tig * 16;
   const uint8_t* vlane = vbase + gid * Y::vBytes;
   auto start_copies = [&](int v, int slot) {
@@ -231,9 +237,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
   for (int i = 0; i < Y::depth - 1; ++i) {
     bits[i] = 0;
-    if (v0 + i * kStep < v1) {
-      bits[i] = start_copies(v0 + i * kStep, i);
-      look_up(v0 + (i + 1) * kStep);
+    if (v0 + i * kHop < v1) {
+      bits[i] = start_copies(v0 + i * kHop, i);
+      look_up(v0 + (i + 1) * kHop);
     }
     cp_async_commit();
   }
@@ -278,15 +284,15 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   }
 
   int slot = 0;
-  for (int v = v0; v < v1; v += kStep) {
+  for (int v = v0; v < v1; v += kHop) {
     {
-      const int ahead = v + (Y::depth - 1) * kStep;
+      const int ahead = v + (Y::depth - 1) * kHop;
       const int into = slot == 0 ? Y::depth - 1 : slot - 1;
       uint32_t b = 0;
       __syncwarp();                          // the slot has been read by all lanes
       if (ahead < v1) {
         b = start_copies(ahead, into);
-        look_up(ahead + kStep);
+        look_up(ahead + kHop);
       }
       cp_async_commit();
       bits[Y::depth - 1] = b;
@@ -542,8 +548,12 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     slot = slot + 1 == Y::depth ? 0 : slot + 1;
   }
 
-  // The lane's dims of acc[mt]: bf16 16 mt + gid and 16 mt + gid + 8; 8-bit gid vDims + 2 mt
-  // and the next one.
+  // The warps' results joined. The lane's dims of acc[mt]: bf16 16 mt + gid and 16 mt + gid + 8;
+  // 8-bit gid vDims + 2 mt and the next one.
+  constexpr int kLd = D + 4;                       // floats per row: a quad's rows 8 banks apart
+  float* s_o = reinterpret_cast<float*>(s_dyn);    // [kWarps][R][kLd], over the rings
+  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+  cp_async_wait<0>();
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -552,61 +562,75 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 4);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 8);
       l += __shfl_xor_sync(0xFFFFFFFFu, l, 16);
+      if (gid == 0) {
+        s_m[warp][nb * 8 + 2 * tig + e] = m_run[nb][e];
+        s_l[warp][nb * 8 + 2 * tig + e] = l;
+      }
+    }
+  __syncthreads();                                 // (and no ring is read any more)
+#pragma unroll
+  for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
       const int rt = nb * 8 + 2 * tig + e;
-      const int r = r0 + rt;
-      const bool live = r < rows;
-      if (A.direct) {
-        const int tok = r / A.G;
-        const int64_t row =
-            (static_cast<int64_t>(li) * A.tokens + list.tok[x] + tok) * A.nq + h * A.G +
-            (r - tok * A.G);
-        const float inv = l == 0.0f ? 0.0f : 1.0f / l;    // a row that sees nothing: zeros
-        uint16_t* out = A.out + row * D;
+      const float top = fmaxf(fmaxf(s_m[0][rt], s_m[1][rt]), fmaxf(s_m[2][rt], s_m[3][rt]));
+      const float f = ex2(__fsub_rn(m_run[nb][e], top == -INFINITY ? 0.0f : top));
+      float* o = s_o + (warp * R + rt) * kLd;
+#pragma unroll
+      for (int mt = 0; mt < KCH; ++mt) {
         if constexpr (Y::k8) {
-#pragma unroll
-          for (int w8 = 0; w8 < Y::vDims / 8; ++w8) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[i] = pack_bf2(acc[nb][w8 * 4 + i][e] * inv, acc[nb][w8 * 4 + i][2 + e] * inv);
-            if (live) st16(out + gid * Y::vDims + w8 * 8, make_uint4(o[0], o[1], o[2], o[3]));
-          }
+          *reinterpret_cast<float2*>(o + gid * Y::vDims + 2 * mt) =
+              make_float2(acc[nb][mt][e] * f, acc[nb][mt][2 + e] * f);
         } else {
-          // neighbouring dims are in the neighbouring quad: even ones take the pair of the
-          // first 8 dims, odd ones that of the second
-          const bool odd = gid & 1;
-#pragma unroll
-          for (int mt = 0; mt < KCH; ++mt) {
-            const float f0 = acc[nb][mt][e] * inv, f1 = acc[nb][mt][2 + e] * inv;
-            const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? f0 : f1, 4);
-            const uint32_t o = odd ? pack_bf2(got, f1) : pack_bf2(f0, got);
-            if (live)
-              *reinterpret_cast<uint32_t*>(out + mt * 16 + (odd ? 7 + gid : gid)) = o;
-          }
-        }
-        if (live && gid == 0 && A.lse)
-          A.lse[row] = l == 0.0f ? -INFINITY : (m_run[nb][e] + log2f(l)) * 0.69314718055994530942f;
-      } else if (live) {
-        float* po = A.part_o + (unit * R + rt) * D;
-        if constexpr (Y::k8) {
-#pragma unroll
-          for (int w8 = 0; w8 < Y::vDims / 4; ++w8)
-            *reinterpret_cast<float4*>(po + gid * Y::vDims + w8 * 4) =
-                make_float4(acc[nb][w8 * 2][e], acc[nb][w8 * 2][2 + e], acc[nb][w8 * 2 + 1][e],
-                            acc[nb][w8 * 2 + 1][2 + e]);
-        } else {
-#pragma unroll
-          for (int mt = 0; mt < KCH; ++mt) {
-            po[mt * 16 + gid] = acc[nb][mt][e];
-            po[mt * 16 + gid + 8] = acc[nb][mt][2 + e];
-          }
-        }
-        if (gid == 0) {
-          A.part_ml[(unit * R + rt) * 2] = m_run[nb][e];
-          A.part_ml[(unit * R + rt) * 2 + 1] = l;
+          o[mt * 16 + gid] = acc[nb][mt][e] * f;
+          o[mt * 16 + gid + 8] = acc[nb][mt][2 + e] * f;
         }
       }
     }
+  __syncthreads();
+  // 8 dims a thread
+  for (int i = threadIdx.x; i < R * (D / 8); i += kWarps * 32) {
+    const int rt = i / (D / 8), d = (i % (D / 8)) * 8;
+    const int r = r0 + rt;
+    if (r >= rows) continue;
+    const float top = fmaxf(fmaxf(s_m[0][rt], s_m[1][rt]), fmaxf(s_m[2][rt], s_m[3][rt]));
+    float l = 0.0f, y[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) y[k] = 0.0f;
+#pragma unroll
+    for (int wp = 0; wp < kWarps; ++wp) {
+      l = __fmaf_rn(s_l[wp][rt], ex2(__fsub_rn(s_m[wp][rt], top == -INFINITY ? 0.0f : top)), l);
+      const float* o = s_o + (wp * R + rt) * kLd + d;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4) {
+        const float4 q4 = *reinterpret_cast<const float4*>(o + k);
+        y[k] += q4.x;
+        y[k + 1] += q4.y;
+        y[k + 2] += q4.z;
+        y[k + 3] += q4.w;
+      }
+    }
+    if (A.direct) {
+      const int tok = r / A.G;
+      const int64_t row = (static_cast<int64_t>(li) * A.tokens + list.tok[x] + tok) * A.nq +
+                          h * A.G + (r - tok * A.G);
+      const float inv = l == 0.0f ? 0.0f : 1.0f / l;      // a row that sees nothing: zeros
+#pragma unroll
+      for (int k = 0; k < 8; ++k) y[k] *= inv;
+      st16(A.out + row * D + d, pack8(y));
+      if (d == 0 && A.lse)
+        A.lse[row] = l == 0.0f ? -INFINITY : (top + log2f(l)) * 0.69314718055994530942f;
+    } else {
+      float* po = A.part_o + (unit * R + rt) * D + d;
+#pragma unroll
+      for (int k = 0; k < 8; k += 4)
+        *reinterpret_cast<float4*>(po + k) = make_float4(y[k], y[k + 1], y[k + 2], y[k + 3]);
+      if (d == 0) {
+        A.part_ml[(unit * R + rt) * 2] = top;
+        A.part_ml[(unit * R + rt) * 2 + 1] = l;
+      }
+    }
+  }
 }
 
 // The parts of every (layer, token, query head) row joined. kSplit: a CTA of four warps a row,
@@ -709,9 +733,14 @@ static cudaError_t run_rows(const ChunkArgs& a, const ChunkList& list, const Chu
   const int64_t n = static_cast<int64_t>(a.nl) * a.g.H * units.base[list.n];
   if (n == 0) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(n);
-  if (rows_per_tile == 8)
-    return launch_after(chunk_rows_kernel<D, kKind, 1>, grid, 32, 0, st, a, list, units);
-  return launch_after(chunk_rows_kernel<D, kKind, 2>, grid, 32, 0, st, a, list, units);
+  using Y = Layout<D, kKind>;
+  constexpr int kSmem = kWarps * Y::depth * Y::stage;
+  static_assert(kSmem >= kWarps * 16 * (D + 4) * 4, "the rings' space takes the warps' results");
+  auto* kernel = rows_per_tile == 8 ? chunk_rows_kernel<D, kKind, 1> : chunk_rows_kernel<D, kKind, 2>;
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_after(kernel, grid, kWarps * 32, kSmem, st, a, list, units);
 }
 
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,

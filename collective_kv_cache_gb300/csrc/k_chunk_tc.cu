@@ -396,26 +396,39 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
   tc_wait_ld(x[0]);
 #pragma unroll
   for (int c = 1; c < 4; ++c) tc_loaded(x[c]);
+  // Masked tiles, a chunk of 32 columns at a time: in sight of every row of the warp (as an
+  // unmasked tile's), of none (no work), or of some
+  uint32_t none = 0, part = 0;           // bit c: chunk c
+  if constexpr (kMask) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      if (!__any_sync(0xFFFFFFFFu, seen[c] != 0u)) none |= 1u << c;
+      else if (!__all_sync(0xFFFFFFFFu, seen[c] == 0xFFFFFFFFu)) part |= 1u << c;
+    }
+  }
   float mx[4];
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     mx[c] = -INFINITY;
+    if (kMask && (none >> c & 1u)) continue;
     [[maybe_unused]] float4 k4;
+    if constexpr (kScaled) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      if constexpr (kScaled) {
+      for (int i = 0; i < 32; i += 2) {
         if (i % 4 == 0) k4 = *reinterpret_cast<const float4*>(ks + c * 32 + i);
         const float2 v = mul2(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])),
                               i % 4 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w));
         x[c][i] = __float_as_uint(v.x);
         x[c][i + 1] = __float_as_uint(v.y);
       }
-      if constexpr (kMask) {
-        x[c][i] = (seen[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
-        x[c][i + 1] = (seen[c] >> (i + 1)) & 1u ? x[c][i + 1] : 0xFF800000u;
-      }
-      mx[c] = max3(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
     }
+    if (kMask && (part >> c & 1u)) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) x[c][i] = (seen[c] >> i) & 1u ? x[c][i] : 0xFF800000u;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i += 2)
+      mx[c] = max3(mx[c], __uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
   }
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const float m_tile = top == -INFINITY ? top : __fmul_rn(top, scale);
@@ -443,27 +456,32 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
   }
   const float nm = m_ref == -INFINITY ? 0.0f : -m_ref;
   const float2 nm2 = make_float2(nm, nm), sc2 = make_float2(scale, scale);
-  float2 part = make_float2(0.0f, 0.0f);
+  float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     uint32_t p[16];
     [[maybe_unused]] float4 v4;
+    if (kMask && (none >> c & 1u)) {
 #pragma unroll
-    for (int i = 0; i < 32; i += 2) {
-      float2 s = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
-      s = fma2(s, sc2, nm2);
-      float2 w = make_float2(ex2(s.x), ex2(s.y));
-      if (c & 1) sum = add2(sum, w);
-      else part = add2(part, w);
-      if constexpr (kScaled) {
-        if (i % 4 == 0) v4 = *reinterpret_cast<const float4*>(vs + c * 32 + i);
-        w = mul2(w, i % 4 == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
-        if constexpr (kMask) {      // a scale out of sight may be a NaN
-          w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
-          w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
+      for (int i = 0; i < 16; ++i) p[i] = 0u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 32; i += 2) {
+        float2 s = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+        s = fma2(s, sc2, nm2);
+        float2 w = make_float2(ex2(s.x), ex2(s.y));
+        if (c & 1) sum = add2(sum, w);
+        else sum2 = add2(sum2, w);
+        if constexpr (kScaled) {
+          if (i % 4 == 0) v4 = *reinterpret_cast<const float4*>(vs + c * 32 + i);
+          w = mul2(w, i % 4 == 0 ? make_float2(v4.x, v4.y) : make_float2(v4.z, v4.w));
+          if constexpr (kMask) {      // a scale out of sight may be a NaN
+            w.x = (seen[c] >> i) & 1u ? w.x : 0.0f;
+            w.y = (seen[c] >> (i + 1)) & 1u ? w.y : 0.0f;
+          }
         }
+        p[i / 2] = pack_bf2(w.x, w.y);
       }
-      p[i / 2] = pack_bf2(w.x, w.y);
     }
     tc_st16(t_s + c * 16, p);
     if (c & 1) {
@@ -473,7 +491,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
       if ((threadIdx.x & 31) == 0) mbar_arrive(p_ready + (c >> 1));
     }
   }
-  sum = add2(sum, part);
+  sum = add2(sum, sum2);
   return true;
 }
 

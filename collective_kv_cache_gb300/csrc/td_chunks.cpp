@@ -196,12 +196,13 @@ bool bf16_map(const td_ctx* c, const ChunkArgs& a, const PoolDev& pool, int* box
 // sequence's tiles of query rows and the steps that one of them sees at most. The length is
 // the one with the least estimated time among the divisions of the longest tile.
 struct Cost {
-  int64_t slots;     // units that run at once
-  int64_t heads;     // kv heads x layers
-  double step_us;    // a step of a unit, with all slots in use
-  int fixed;         // what a unit costs besides its steps, in steps
-  int least;         // steps per unit, at least
-  double row_bytes;  // of partial results per part, over all rows of the launch
+  int64_t slots;      // units that run at once
+  int64_t heads;      // kv heads x layers
+  double step_us;     // a step of a unit, with the others beside it
+  double fixed_us;    // what a unit costs besides its steps
+  double step_bytes;  // that a step reads, at 6.5 TB/s for all units together
+  int least;          // steps per unit, at least
+  double row_bytes;   // of partial results per part, over all rows of the launch
 };
 
 template <typename Tiles, typename Seen>
@@ -226,13 +227,14 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
       most = std::max(most, ns);
     }
     n *= cost.heads;
-    // one wave: its longest unit; more: the slots' share of the work and half a unit of tail
-    const double unit = static_cast<double>(span + cost.fixed);
-    double us = cost.step_us *
-                (n <= cost.slots
-                     ? unit
-                     : std::max(unit, (static_cast<double>(total) * cost.heads +
-                                       static_cast<double>(n) * cost.fixed) / cost.slots + unit / 2));
+    // one wave: its longest unit; more: the slots' share of the work and half a unit of tail;
+    // or the bytes
+    const double unit = span * cost.step_us + cost.fixed_us;
+    const double work = static_cast<double>(total) * cost.heads;
+    double us = n <= cost.slots
+                    ? unit
+                    : std::max(unit, (work * cost.step_us + n * cost.fixed_us) / cost.slots + unit / 2);
+    us = std::max(us, work * cost.step_bytes / 6.5e6);
     // joining: a launch, and the parts written and read once
     if (most > 1) us += 4.0 + 2.0 * cost.row_bytes * most / 5e6;
     if (k == 1 || us < best_us) {
@@ -274,15 +276,16 @@ int64_t plan_rows(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUni
   for (int x = 0; x < list.n; ++x)
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = most <= 8 ? 8 : 16;
-  // 12 warps an SM; a step of 32 positions of K and V (16 KB in bf16 at D = 128) at 6 TB/s
-  const double bytes = 2.0 * 32 * a->g.D * (a->scale ? 1 : 2);
-  const int64_t slots = static_cast<int64_t>(c->sm_count) * 12;
-  const Cost cost{slots, static_cast<int64_t>(a->g.H) * a->nl, bytes * slots / 6e6, 4, 4,
-                  partial_bytes(list, *a)};
+  // three blocks an SM (two with 16 rows a tile); a step of 128 positions of the block's four
+  // warps took 3.1 us in bf16 at D = 128, 2 us otherwise, with all blocks in place
+  const int64_t slots = static_cast<int64_t>(c->sm_count) * (R == 8 ? 3 : 2);
+  const double bytes = 2.0 * 128 * a->g.D * (a->scale ? 1 : 2);
+  const Cost cost{slots, static_cast<int64_t>(a->g.H) * a->nl,
+                  !a->scale && a->g.D == 128 ? 3.1 : 2.0, 4.0, bytes, 2, partial_bytes(list, *a)};
   return cut(
       list, cost,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
-      [&](int x) { return (seen_positions(list, *a, x, R) + 31) / 32; }, 32, a, units);
+      [&](int x) { return (seen_positions(list, *a, x, R) + 127) / 128; }, 128, a, units);
 }
 
 int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
@@ -291,9 +294,10 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
   for (int x = 0; x < list.n; ++x)
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = a->rows_cta = most <= 128 ? 128 : 256;
-  // one CTA an SM; a KV tile's products and softmax (1.4 us at D = 128)
-  const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, a->g.D == 128 ? 1.4 : 0.8, 3,
-                  2, partial_bytes(list, *a)};
+  // one CTA an SM; a KV tile's products and softmax
+  const double step = a->scale ? 2.4 : (a->g.D == 128 ? 1.4 : 0.8);
+  const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, step, 4.0,
+                  2.0 * 128 * a->g.D * (a->scale ? 1 : 2) / 8, 2, partial_bytes(list, *a)};
   return cut(
       list, cost,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },

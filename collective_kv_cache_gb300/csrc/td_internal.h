@@ -254,7 +254,7 @@ struct ChunkArgs {
   int nl, layer_begin;
   int window, n_sink;        // 0: every earlier position is seen
   int span;                  // per unit: visible positions (streaming kernel; a multiple of
-                             // 32) or KV tiles of 128 positions (tensor-core kernel)
+                             // 128) or KV tiles of 128 positions (tensor-core kernel)
   int rows_cta;              // tensor-core kernel: query rows per unit, 128 or 256
   int box_rows;              // ... and rows per box of its tensor map
   uint32_t tx_pad;           // ... extra bytes every tile expects (fault injection; 0 normally)

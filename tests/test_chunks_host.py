@@ -25,7 +25,9 @@ def td():
 def lib(td, tmp_path_factory):
     from collective_kv_cache_gb300 import build
     out = str(tmp_path_factory.mktemp("chunk_host") / "libchunk_host.so")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-Wall", "-I", build.INC, "-I",
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fPIC", "-shared", "-Wall",
+                    # its own stand-ins, not a CUDA runtime that the process has loaded
+                    "-Wl,-Bsymbolic", "-I", build.INC, "-I",
                     build.CSRC, "-I", os.path.join(build.CUDA_HOME, "include"),
                     os.path.join(build.CSRC, "td_chunks.cpp"),
                     os.path.join(ROOT, "tests", "chunk_host.cpp"), "-o", out], check=True)
