@@ -6,7 +6,7 @@
 // The query rows of a kv head are the pairs (token, head of the group): a CTA takes up to 256
 // of them as two tiles of 128 and walks the KV tiles of 128 positions that any of them sees:
 //   S_w = Q_w K^T        (128 x 128, float32 in TMEM; operands in shared memory)
-//   P_w = 2^(S_w - m)    (bf16, written over S_w in TMEM)
+//   P_w = 2^(S_w - m)    (bf16, in TMEM: over S_w at D = 128, beside it at D = 64)
 //   O_w += P_w V         (float32 in TMEM; A operand from TMEM, V as stored: dims-major)
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that no statistic
 // crosses threads; one thread issues all products; the two tiles alternate, so that the tensor
@@ -56,6 +56,10 @@ struct Plan {
   // room for more, and must take more than half of the shared memory
   static constexpr int kK = D == 64 ? 4 : (k8 ? 2 : 3);
   static constexpr int kV = D == 64 ? 4 : 2;
+  // TMEM columns: two S, two O, and at D = 64 two P of their own: the next scores may then be
+  // computed while the softmax still works on the last ones (at D = 128 P lies over S)
+  static constexpr bool kOwnP = D == 64;
+  static constexpr uint32_t kColO = 2 * kKv, kColP = 2 * kKv + 2 * D;
   static constexpr int kThreads = k8 ? 512 : 384;
   // 8-bit pages: the last KV tiles' scales, four tiles' page rows (a thread may write those of
   // tile j + 2 while another still reads tile j's)
@@ -82,7 +86,7 @@ __device__ __forceinline__ bool no_holes(const uint4& v) { return (v.x & v.y & v
 
 struct Shared {
   uint64_t q_full, k_full[4], k_empty[4], v_raw[4], v_full[4], v_empty[4];
-  uint64_t s_full[2], p_ready[2][2], o_done[2], drain;   // p_ready: halves of the weights
+  uint64_t s_full[2], s_empty[2], p_ready[2][2], o_done[2], drain;   // p_ready: the weights' halves
   uint32_t tmem;
   int abort, bad;
   alignas(16) int box_row[2][16];    // K's and V's loader: rows of the tile's boxes
@@ -385,7 +389,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // products may start on the first half of the weights while the second is computed: each half
 // has its barrier. `seen`: the columns in sight, 4 words.
 template <int D, bool kScaled, bool kMask>
-__device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const uint32_t* seen,
+__device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_t t_p,
+                                             uint64_t* s_empty, const uint32_t* seen,
                                              float scale, const float* ks, const float* vs,
                                              bool first, uint64_t* o_done, unsigned o_parity,
                                              uint64_t* p_ready, float& m_ref, float2& sum,
@@ -396,6 +401,12 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
   tc_wait_ld(x[0]);
 #pragma unroll
   for (int c = 1; c < 4; ++c) tc_loaded(x[c]);
+  constexpr bool kOwnP = Plan<D, false>::kOwnP;
+  if constexpr (kOwnP) {
+    tc_fence_before();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(s_empty);
+  }
   // Masked tiles, a chunk of 32 columns at a time: in sight of every row of the warp (as an
   // unmasked tile's), of none (no work), or of some
   uint32_t none = 0, part = 0;           // bit c: chunk c
@@ -454,6 +465,10 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
       tc_st16(t_o + c * 16, o);
     }
   }
+  if constexpr (kOwnP) {        // the last weights have been used
+    if (!first && !__all_sync(0xFFFFFFFFu, wait_or_abort(o_done, o_parity, sh, err))) return false;
+    tc_fence_after();
+  }
   const float nm = m_ref == -INFINITY ? 0.0f : -m_ref;
   const float2 nm2 = make_float2(nm, nm), sc2 = make_float2(scale, scale);
   float2 sum2 = make_float2(0.0f, 0.0f);
@@ -483,7 +498,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, const u
         p[i / 2] = pack_bf2(w.x, w.y);
       }
     }
-    tc_st16(t_s + c * 16, p);
+    tc_st16(t_p + c * 16, p);
     if (c & 1) {
       tc_wait_st();
       tc_fence_before();
@@ -734,6 +749,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh->s_full[i], 1);
+      mbar_init(&sh->s_empty[i], 4);
       mbar_init(&sh->p_ready[i][0], 4);
       mbar_init(&sh->p_ready[i][1], 4);
       mbar_init(&sh->o_done[i], 1);
@@ -809,7 +825,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const int pf = w.start + (w.r0 + wg * kRows) / A.G;
       const int pl = w.start + (w.r0 + min(wg * kRows + kRows, w.nrows) - 1) / A.G;
       const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-      const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + 2 * kKv + wg * D;
+      const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + PL::kColO + wg * D;
+      const uint32_t t_p = PL::kOwnP ? tmem + lanes + PL::kColP + wg * (kKv / 2) : t_s;
+      uint64_t* s_empty = &sh->s_empty[wg];
       // (never 0, which would turn the -infinity of a masked score into a NaN)
       const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f);
       float m_ref = -INFINITY;
@@ -834,17 +852,17 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             if (w.window) b &= ~first_bits(hi - w.window + 1 - c * 32) | first_bits(sk - c * 32);
             seen[c] = b & in[c];
           }
-          ok = scaled ? softmax_tile<D, k8, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
+          ok = scaled ? softmax_tile<D, k8, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv, j == 0,
                                                   &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
                                                   m_ref, sum, sh, A.err)
-                      : softmax_tile<D, false, true>(t_s, t_o, seen, scale, ks, ks + kKv, j == 0,
+                      : softmax_tile<D, false, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv, j == 0,
                                                      &sh->o_done[wg], (j - 1) & 1,
                                                      sh->p_ready[wg], m_ref, sum, sh, A.err);
         } else {
-          ok = scaled ? softmax_tile<D, k8, false>(t_s, t_o, nullptr, scale, ks, ks + kKv, j == 0,
+          ok = scaled ? softmax_tile<D, k8, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks, ks + kKv, j == 0,
                                                    &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
                                                    m_ref, sum, sh, A.err)
-                      : softmax_tile<D, false, false>(t_s, t_o, nullptr, scale, ks, ks + kKv,
+                      : softmax_tile<D, false, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks, ks + kKv,
                                                       j == 0, &sh->o_done[wg], (j - 1) & 1,
                                                       sh->p_ready[wg], m_ref, sum, sh, A.err);
         }
@@ -856,22 +874,33 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         tc_fence_after();
         const float l = sum.x + sum.y;
         if (A.direct) {
-          const int64_t row = live ? out_row(A, list, w, w.r0 + rr) : 0;
+          const int64_t row = live ? out_row(A, list, w, w.r0 + rr) : -1;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;      // a row that sees nothing: zeros
+          // through the query tile's place (its products have ended), so that a warp writes
+          // whole rows: lane by lane a row's 16-byte pieces took 3.8 us at D = 128
+          unsigned char* mine = s_q + wg * (PL::kQ / 2);
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
             tc_ld32(x, t_o + c * 32);
             tc_wait_ld(x);
-            if (live) {
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                float y[8];
+            for (int i = 0; i < 4; ++i) {
+              float y[8];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[i * 8 + e]) * inv;
-                st16(A.out + row * D + c * 32 + i * 8, pack8(y));
-              }
+              for (int e = 0; e < 8; ++e) y[e] = __uint_as_float(x[i * 8 + e]) * inv;
+              *reinterpret_cast<uint4*>(mine + tile_at(t, c * 4 + i)) = pack8(y);
             }
+          }
+          __syncwarp();
+          constexpr int kVec = D / 8, kPer = 32 / kVec;       // rows a step
+#pragma unroll 4
+          for (int i = 0; i < kVec; ++i) {
+            const int from = i * kPer + lane / kVec;
+            const int64_t to = __shfl_sync(0xFFFFFFFFu, row, from);
+            if (to >= 0)
+              st16(A.out + to * D + (lane % kVec) * 8,
+                   *reinterpret_cast<const uint4*>(mine + tile_at((warp & 3) * 32 + from, lane % kVec)));
           }
           if (live && A.lse)
             A.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994530942f;
@@ -931,8 +960,21 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         ks = 0;
         k_par ^= 1;
       }
-      for (int wg = 0; wg <= last; ++wg) {
+      // the next scores of a query tile: once its S is free
+      auto next_scores = [&](int wg) {
+        if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], k_par, sh, A.err);
+        if constexpr (PL::kOwnP) ok = ok && wait_or_abort(&sh->s_empty[wg], j & 1, sh, A.err);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        if (!ok) return;
+        tc_fence_after();
+        scores(wg, ks, wg == last);
+      };
+      if constexpr (PL::kOwnP) {
+        for (int wg = 0; ok && j + 1 < w.n && wg <= last; ++wg) next_scores(wg);
+      }
+      for (int wg = 0; ok && wg <= last; ++wg) {
         if (wg == 0) ok = wait_or_abort(&sh->v_full[vs], v_par, sh, A.err);
+        const uint32_t t_p = PL::kOwnP ? tmem + PL::kColP + wg * (kKv / 2) : tmem + wg * kKv;
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
           ok = ok && wait_or_abort(&sh->p_ready[wg][half], j & 1, sh, A.err);
@@ -943,8 +985,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             const uint64_t b = v_desc + vs * (PL::kTile / 16);
 #pragma unroll
             for (int kc = half * 4; kc < half * 4 + 4; ++kc)
-              tc_mma_ts(tmem + 2 * kKv + wg * D, tmem + wg * kKv + kc * 8, b + kc * (2048 / 16),
-                        id_o, j > 0 || kc > 0);
+              tc_mma_ts(tmem + PL::kColO + wg * D, t_p + kc * 8, b + kc * (2048 / 16), id_o,
+                        j > 0 || kc > 0);
             if (half == 1) {
               tc_commit(&sh->o_done[wg]);
               if (wg == last) tc_commit(&sh->v_empty[vs]);
@@ -952,13 +994,8 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           }
           __syncwarp();
         }
-        if (!ok) break;
-        if (j + 1 < w.n) {
-          if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], k_par, sh, A.err);
-          ok = __all_sync(0xFFFFFFFFu, ok);
-          if (!ok) break;
-          tc_fence_after();
-          scores(wg, ks, wg == last);
+        if constexpr (!PL::kOwnP) {
+          if (ok && j + 1 < w.n) next_scores(wg);
         }
       }
       if (++vs == PL::kV) {
