@@ -9,8 +9,10 @@
 // exact residual x - n s (below). Reading back: bf16(fl32(code * s)).
 //
 // Both kernels move 2 + 1 + 4/D bytes an element once and are bound by HBM. A group of lanes
-// (D / 8, rounded up to a power of two) holds one head row, 8 elements a lane in one 16-byte
-// vector, so the row's maximum is a few shuffles and no row is read twice. A CTA takes up to
+// holds one head row, so the row's maximum is a few shuffles and no row is read twice. The
+// write takes 16 elements a lane: with 8 the shuffles, scales and addresses cost twice as much
+// an element and it ran at 80% of the copy rate, bound by their issue. The read takes 8 (one
+// 16-byte store a lane, whole lines a warp): with 16 it ran at 92%. A CTA takes up to
 // 32 tokens of one layer and K or V; their page rows are looked up once, by one thread each.
 #include "td_device.cuh"
 
@@ -19,7 +21,6 @@ namespace td {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;   // vectors in flight per thread
 constexpr float kScaleMin = 7.8886090522101181e-31f;   // 2^-100: keeps 1 / s finite
 
 // Row (page * P + slot) of the launch's token t, or -1 and the error bit.
@@ -40,6 +41,12 @@ __device__ __forceinline__ int token_row(const ChunkList& list, const PoolDev& p
     return -1;
   }
   return page * p.P + (pos - lp * p.P);
+}
+
+// The larger magnitudes of 8 bf16, as bits, by the halves of a word.
+__device__ __forceinline__ uint32_t magnitude8(const uint4& v) {
+  return __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu),
+                  __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
 }
 
 // Scale of a row whose largest magnitude is the bf16 pattern `top` (finite).
@@ -116,9 +123,14 @@ __device__ __forceinline__ void values4(uint32_t w, float* y) {
 
 }  // namespace
 
-template <int kKind, bool kWrite>
+// kShift: log2 of the lanes per head row, known for D = 64 and 128, else -1. A
+// thread's vectors are kThreads apart, so their (token, head) advance by a fixed step: no
+// division per vector.
+template <int kKind, bool kWrite, int kShift>
 __global__ void __launch_bounds__(kThreads)
 quant_kernel(const __grid_constant__ QuantArgs A, const __grid_constant__ ChunkList list) {
+  constexpr int kPer = kWrite ? 16 : 8;      // elements per lane
+  constexpr int kUnroll = kWrite ? 2 : 4;    // vectors in flight per thread
   pdl_wait();
   __shared__ int s_row[kQuantTokens];
   const int t0 = blockIdx.x * A.per_cta;
@@ -126,78 +138,109 @@ quant_kernel(const __grid_constant__ QuantArgs A, const __grid_constant__ ChunkL
   if (static_cast<int>(threadIdx.x) < nt)
     s_row[threadIdx.x] = token_row(list, A.cache.pool, t0 + threadIdx.x, A.err);
   __syncthreads();
+  pdl_trigger();
   const int li = blockIdx.y >> 1, kv = blockIdx.y & 1;
-  const int H = A.g.H, D = A.g.D;
-  // head rows of this layer and K or V in the pages; this CTA's first dense row
+  constexpr bool kKnown = kShift > 0;
+  const int shift = kKnown ? kShift : A.lane_shift;
+  const int lanes = 1 << shift;
+  const int H = A.g.H, D = kKnown ? kPer << kShift : A.g.D, E = A.g.E;
+  // this layer's K or V in the pages; this CTA's first dense row
   const int64_t plane = (static_cast<int64_t>(A.layer_begin + li) * 2 + kv) *
-                        A.cache.pool.num_pages * A.cache.pool.P * H;
-  uint8_t* codes = reinterpret_cast<uint8_t*>(A.cache.pool.base) + plane * D;
-  float* scale = A.cache.scale + plane;
-  uint16_t* dense = (kv ? A.v : A.k) + (static_cast<int64_t>(li) * A.tokens + A.tok0 + t0) * A.g.E;
-  const int lanes = 1 << A.lane_shift;
-  const int total = nt * H << A.lane_shift;
-  for (int base = 0; base < total; base += kThreads * kUnroll) {
-    int64_t at[kUnroll];     // head row in the pages, -1: nothing to do
-    int src[kUnroll];        // element offset of the vector from the CTA's first dense row
-    int e0[kUnroll];         // element offset within the head row
-    uint4 x[kUnroll];
+                        A.cache.pool.num_pages * A.cache.pool.P;
+  uint8_t* codes = reinterpret_cast<uint8_t*>(A.cache.pool.base) + plane * E;
+  float* scale = A.cache.scale + plane * H;
+  uint16_t* dense = (kv ? A.v : A.k) + (static_cast<int64_t>(li) * A.tokens + A.tok0 + t0) * E;
+  const int rows = nt * H;                       // head rows of the CTA
+  const int e0 = (threadIdx.x & (lanes - 1)) * kPer;  // elements of the thread's vectors
+  const bool in_row = kKnown || e0 < D;
+  int r = threadIdx.x >> shift;                  // the head row, its token and head
+  int tok = static_cast<int>((static_cast<uint32_t>(r) * A.head_mul) >> 20);
+  int h = r - tok * H;
+  const int step = kThreads >> shift;
+  const int step_tok = static_cast<int>((static_cast<uint32_t>(step) * A.head_mul) >> 20);
+  const int step_h = step - step_tok * H;
+  for (; r - (static_cast<int>(threadIdx.x) >> shift) < rows; ) {
+    int row[kUnroll], hd[kUnroll], rr[kUnroll];  // page row (-1: unmapped, -2: nothing), head
+    uint4 x[kUnroll][2];
     uint2 cw[kUnroll];
     float sc[kUnroll];
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + threadIdx.x;
-      e0[u] = (i & (lanes - 1)) * 8;
-      at[u] = -1;
-      src[u] = 0;
-      x[u] = make_uint4(0u, 0u, 0u, 0u);
+      row[u] = r < rows && in_row ? s_row[tok] : -2;
+      hd[u] = h;
+      rr[u] = r;
+      x[u][0] = x[u][1] = make_uint4(0u, 0u, 0u, 0u);
       cw[u] = make_uint2(0u, 0u);
       sc[u] = 0.0f;
-      if (i >= total || e0[u] >= D) continue;
-      const int r = i >> A.lane_shift;
-      const int tok = static_cast<int>((static_cast<uint32_t>(r) * A.head_mul) >> 20);
-      const int h = r - tok * H;
-      src[u] = r * D + e0[u];
-      const int row = s_row[tok];
-      at[u] = row < 0 ? -1 : static_cast<int64_t>(row) * H + h;
       if constexpr (kWrite) {
-        x[u] = ldg16(dense + src[u]);
-      } else if (row >= 0) {
-        cw[u] = __ldg(reinterpret_cast<const uint2*>(codes + at[u] * D + e0[u]));
-        sc[u] = __ldg(scale + at[u]);
+        if (row[u] > -2) {
+          x[u][0] = ldg16(dense + r * D + e0);
+          x[u][1] = ldg16(dense + r * D + e0 + 8);
+        }
+      } else if (row[u] >= 0) {
+        cw[u] = __ldg(reinterpret_cast<const uint2*>(codes + static_cast<int64_t>(row[u]) * E +
+                                                     (h * D + e0)));
+        sc[u] = __ldg(scale + static_cast<int64_t>(row[u]) * H + h);
+      }
+      r += step;
+      tok += step_tok;
+      h += step_h;
+      if (h >= H) {
+        h -= H;
+        ++tok;
       }
     }
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u) {
-      const int i = base + u * kThreads + threadIdx.x;
       if constexpr (kWrite) {
-        uint32_t m = __vmaxu2(__vmaxu2(x[u].x & 0x7FFF7FFFu, x[u].y & 0x7FFF7FFFu),
-                              __vmaxu2(x[u].z & 0x7FFF7FFFu, x[u].w & 0x7FFF7FFFu));
-        for (int o = lanes >> 1; o > 0; o >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-        const uint32_t top = max(m & 0xFFFFu, m >> 16);
-        if (at[u] < 0) continue;
-        float s = row_scale<kKind>(top);
-        uint2 c = make_uint2(0u, 0u);
-        if (top < 0x7F80u) {
-          float f[8];
-          unpack8(x[u], f);
-          c = codes8<kKind>(f, s);
-        } else {             // a NaN or an infinity: the row reads back as NaN
-          s = __uint_as_float(0x7FC00000u);
-          if (e0[u] == 0) atomicOr(A.err, err_bit(TD_ERR_NONFINITE));
+        uint32_t m = __vmaxu2(magnitude8(x[u][0]), magnitude8(x[u][1]));
+        if constexpr (kKnown) {
+#pragma unroll
+          for (int o = 1 << (kShift - 1); o > 0; o >>= 1)
+            m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+        } else {
+          for (int o = lanes >> 1; o > 0; o >>= 1)
+            m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
         }
-        *reinterpret_cast<uint2*>(codes + at[u] * D + e0[u]) = c;
-        if (e0[u] == 0) scale[at[u]] = s;
+        const uint32_t top = max(m & 0xFFFFu, m >> 16);
+        if (row[u] >= 0) {
+          float s = row_scale<kKind>(top);
+          uint4 c = make_uint4(0u, 0u, 0u, 0u);
+          if (top < 0x7F80u) {
+            float f[8];
+            unpack8(x[u][0], f);
+            const uint2 a = codes8<kKind>(f, s);
+            unpack8(x[u][1], f);
+            const uint2 b = codes8<kKind>(f, s);
+            c = make_uint4(a.x, a.y, b.x, b.y);
+          } else {             // a NaN or an infinity: the row reads back as NaN
+            s = __uint_as_float(0x7FC00000u);
+            if (e0 == 0) atomicOr(A.err, err_bit(TD_ERR_NONFINITE));
+          }
+          *reinterpret_cast<uint4*>(codes + static_cast<int64_t>(row[u]) * E + (hd[u] * D + e0)) = c;
+          if (e0 == 0) scale[static_cast<int64_t>(row[u]) * H + hd[u]] = s;
+        }
       } else {
-        if (i >= total || e0[u] >= D) continue;
-        float y[8];          // an unmapped row reads as zeros
+        if (row[u] == -2) continue;
+        // (an unmapped row: codes 0 and the scale 0, zeros)
+        float y[8];
         values4<kKind>(cw[u].x, y);
         values4<kKind>(cw[u].y, y + 4);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = at[u] < 0 ? 0.0f : __fmul_rn(y[j], sc[u]);
-        st16(dense + src[u], pack8(y));
+        for (int j = 0; j < 8; ++j) y[j] = __fmul_rn(y[j], sc[u]);
+        st16(dense + rr[u] * D + e0, pack8(y));
       }
     }
   }
+}
+
+template <int kKind, bool kWrite>
+static cudaError_t run_kind(const QuantArgs& a, const ChunkList& list, dim3 grid,
+                            cudaStream_t st) {
+  constexpr int k64 = kWrite ? 2 : 3;
+  if (a.g.D == 128) return launch_after(quant_kernel<kKind, kWrite, k64 + 1>, grid, kThreads, 0, st, a, list);
+  if (a.g.D == 64) return launch_after(quant_kernel<kKind, kWrite, k64>, grid, kThreads, 0, st, a, list);
+  return launch_after(quant_kernel<kKind, kWrite, -1>, grid, kThreads, 0, st, a, list);
 }
 
 template <bool kWrite>
@@ -206,8 +249,8 @@ static cudaError_t run(const QuantArgs& a, const ChunkList& list, CacheKind kind
   const int tokens = list.row[list.n];
   if (tokens == 0) return cudaSuccess;
   const dim3 grid((tokens + a.per_cta - 1) / a.per_cta, a.nl * 2);
-  if (kind == kCacheInt8) return launch_after(quant_kernel<kCacheInt8, kWrite>, grid, kThreads, 0, st, a, list);
-  return launch_after(quant_kernel<kCacheE4m3, kWrite>, grid, kThreads, 0, st, a, list);
+  if (kind == kCacheInt8) return run_kind<kCacheInt8, kWrite>(a, list, grid, st);
+  return run_kind<kCacheE4m3, kWrite>(a, list, grid, st);
 }
 
 cudaError_t launch_quantise(const QuantArgs& a, const ChunkList& list, CacheKind kind,

@@ -109,7 +109,7 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   if (!c || !same_device(c) || !cache || !layers_ok(c, layer_begin, layer_end))
     return TD_ERR_INVALID_ARG;
   const int D = c->g.D;
-  if (D > 256) return TD_ERR_INVALID_ARG;   // a warp holds a head row, 8 elements a lane
+  if (D > 256) return TD_ERR_INVALID_ARG;   // (a warp would hold a head row of 512)
   QuantArgs a{};
   CacheKind kind;
   td_status s = pages8_dev(c, cache, &a.cache, &kind);
@@ -126,7 +126,7 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   a.tokens = tokens;
   a.nl = layer_end - layer_begin;
   a.layer_begin = layer_begin;
-  a.lane_shift = log2i((D + 7) / 8);
+  a.lane_shift = log2i(write ? D / 16 : D / 8);
   a.head_mul = ((1 << 20) + c->g.H - 1) / c->g.H;
   a.err = c->d_err;
   // tokens per CTA: 32, fewer where the grid would leave SMs without a CTA

@@ -228,7 +228,8 @@ struct QuantArgs {
   int64_t tokens;            // tokens of the whole call
   int64_t tok0;              // this launch's first (its sequences follow one another)
   int nl, layer_begin;
-  int lane_shift;            // lanes per head row = 1 << lane_shift (>= D / 8, at most 32)
+  int lane_shift;            // lanes per head row = 1 << lane_shift: D / 16 (write) or
+                             // D / 8 (read), up to a power of two, at most 32
   int head_mul;              // ceil(2^20 / H): row / H without a division
   int per_cta;               // tokens per CTA, at most kQuantTokens
   uint32_t* err;

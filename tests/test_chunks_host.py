@@ -205,7 +205,8 @@ def test_plans_of_the_quantising_kernels(td, lib):
                 assert call.run(op, chunks=[(0, 3, T)]) == td.TD_OK
                 (l,) = call.launches()
                 lanes = 1 << l["lane_shift"]
-                assert D // 8 <= lanes <= 32 and lanes < 2 * max(1, D // 8) or D == 16
+                need = D // (16 if op == "write" else 8)       # elements a lane
+                assert need <= lanes <= 32 and lanes < 2 * need
                 assert 1 <= l["per_cta"] <= 32
                 rows = np.arange(l["per_cta"] * H, dtype=np.int64)
                 prod = rows * l["head_mul"]
