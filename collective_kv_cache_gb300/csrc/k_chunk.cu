@@ -4,8 +4,9 @@
 // Token u of a sequence's chunk sits at position pos = start + u and sees the positions
 // p <= pos; under a window W only p > pos - W and the first n_sink positions. With
 // s_p = scale q . k_p over the visible p: out = sum_p softmax(s)_p v_p, lse = ln sum_p e^{s_p}.
-// 8-bit pages hold k = ks_p * code and v = vs_p * code: the codes are exact in bf16, so they
-// go through the same products, with ks_p on the score and vs_p on the weight.
+// 8-bit pages hold k = ks_p * code and v = vs_p * code: the codes are exact in f16 and bf16, so
+// they go through the same products (K in f16, V in bf16), with ks_p on the score and vs_p on
+// the weight.
 //
 // A block takes a unit = (layer, kv head, tile of 8 or 16 query rows, `span` of the tile's
 // visible positions), its four warps every fourth step of 16 or 32 positions each; they are
@@ -40,6 +41,15 @@ __device__ __forceinline__ void mma_bf16(float* d, uint32_t a0, uint32_t a1, uin
                                          uint32_t a3, uint32_t b0, uint32_t b1) {
   asm volatile(
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+      "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ void mma_f16(float* d, uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
       "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -248,6 +258,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   // this lane's query rows: as a B-operand column (gid), and as accumulator columns
   int pos_q[NB][2];          // positions of columns 2 tig, 2 tig + 1; -1 past the last row
   uint32_t qf[NB][KCH][2];
+  [[maybe_unused]] float row_scale[NB][2];   // 8-bit pages: scale * log2(e) of the columns
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -269,6 +280,24 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
                               : ((kc >> 1) * 4 + tig) * 8 + (kc & 1) * 4 + e * 2;
         qf[nb][kc][e] = live ? __ldg(reinterpret_cast<const unsigned int*>(q + dim)) : 0u;
       }
+    if constexpr (Y::k8) {       // f16 fragments, the row's factor kept for its scores
+      uint32_t m = 0;
+#pragma unroll
+      for (int kc = 0; kc < KCH; ++kc)
+        m = __vmaxu2(m, __vmaxu2(qf[nb][kc][0] & 0x7FFF7FFFu, qf[nb][kc][1] & 0x7FFF7FFFu));
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      float inverse;
+      const float f = f16_scale(max(m & 0xFFFFu, m >> 16), &inverse);
+#pragma unroll
+      for (int kc = 0; kc < KCH; ++kc)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          qf[nb][kc][e] = pack_f16(bf_lo(qf[nb][kc][e]) * f, bf_hi(qf[nb][kc][e]) * f);
+#pragma unroll
+      for (int e = 0; e < 2; ++e)      // (row c's is in the lanes 4 c .. 4 c + 3)
+        row_scale[nb][e] = __shfl_sync(0xFFFFFFFFu, inverse, (2 * tig + e) * 4) * A.scale_log2;
+    }
   }
 
   // O^T: acc[nb][mt] = dims (lane's dims 2 mt, 2 mt + 1) x rows 2 tig, 2 tig + 1
@@ -325,10 +354,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           const int j = kc >> 2;
           const uint32_t w0 = reinterpret_cast<const uint32_t*>(&kr[0][j])[kc & 3];
           const uint32_t w1 = reinterpret_cast<const uint32_t*>(&kr[1][j])[kc & 3];
-          a[0] = word_bf16<kKind, false>(w0);
-          a[1] = word_bf16<kKind, false>(w1);
-          a[2] = word_bf16<kKind, true>(w0);
-          a[3] = word_bf16<kKind, true>(w1);
+          a[0] = word_f16<kKind, false>(w0);
+          a[1] = word_f16<kKind, false>(w1);
+          a[2] = word_f16<kKind, true>(w0);
+          a[3] = word_f16<kKind, true>(w1);
         } else {
           const uint32_t* w0 = reinterpret_cast<const uint32_t*>(&kr[0][kc >> 1]) + (kc & 1) * 2;
           const uint32_t* w1 = reinterpret_cast<const uint32_t*>(&kr[1][kc >> 1]) + (kc & 1) * 2;
@@ -338,9 +367,11 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           a[3] = w1[1];
         }
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb)
-          mma_bf16(kc & 1 ? s2[nb] : s[sub][nb], a[0], a[1], a[2], a[3], qf[nb][kc][0],
-                   qf[nb][kc][1]);
+        for (int nb = 0; nb < NB; ++nb) {
+          float* d = kc & 1 ? s2[nb] : s[sub][nb];
+          if constexpr (Y::k8) mma_f16(d, a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
+          else mma_bf16(d, a[0], a[1], a[2], a[3], qf[nb][kc][0], qf[nb][kc][1]);
+        }
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
@@ -353,15 +384,17 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
                        (A.window == 0 || pa > p_last - A.window || v + kStep <= sinks);
 #pragma unroll
     for (int sub = 0; sub < Y::subs; ++sub) {
-      float m[2] = {A.scale_log2, A.scale_log2};      // rows gid, gid + 8
+      [[maybe_unused]] float ks[2];      // rows gid, gid + 8
       if constexpr (Y::k8) {
-        m[0] = __fmul_rn(m[0], scales[sub * 16 + gid]);
-        m[1] = __fmul_rn(m[1], scales[sub * 16 + gid + 8]);
+        ks[0] = scales[sub * 16 + gid];
+        ks[1] = scales[sub * 16 + gid + 8];
       }
 #pragma unroll
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[sub][nb][i] = __fmul_rn(s[sub][nb][i], m[i >> 1]);
+        for (int i = 0; i < 4; ++i)
+          s[sub][nb][i] = __fmul_rn(s[sub][nb][i], Y::k8 ? __fmul_rn(ks[i >> 1], row_scale[nb][i & 1])
+                                                         : A.scale_log2);
       if (!whole) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)

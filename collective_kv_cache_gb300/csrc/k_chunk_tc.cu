@@ -26,8 +26,9 @@
 // does not see, they clear the rows that none sees (their bytes may be anything) and watch for
 // infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
 // value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
-// 8-bit pages: four warps load K's codes and three V's, turn them into bf16 (exact) and store
-// them as the same tiles. The scale of K's row goes on the score's column, that of V's on the
+// 8-bit pages: three warps load K's codes and four V's, turn them into f16 and bf16 (exact) and
+// store them as the same tiles; the queries become f16 too, each row with a power of two that
+// brings it to f16's range. The scale of K's row goes on the score's column, that of V's on the
 // weight's; powers of two (e4m3 as td_quantise_append writes it) go into the conversion
 // itself, exactly, and cost the softmax nothing.
 //
@@ -45,7 +46,7 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kMmaWarp = 8;
 constexpr int kLoadWarp = 9;          // bf16: K by TMA; V: the next warp
 constexpr int kPatchWarp = 11;
-constexpr int kConvertWarp = 12;      // 8-bit: the first of four that convert K (9-11: V)
+constexpr int kConvertWarp = 12;      // 8-bit: the first of four that convert V (9-11: K)
 constexpr int kInfo = 8;              // KV tiles whose facts are kept
 
 template <int D, bool k8>
@@ -65,7 +66,8 @@ struct Plan {
   // tile j + 2 while another still reads tile j's)
   static constexpr int kScales = k8 ? kInfo * 2 * kKv * 4 : 0;
   static constexpr int kPageRows = k8 ? 4 * kKv * 4 : 0;
-  static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + 1024;
+  static constexpr int kRowScales = k8 ? 2 * kRows * 4 : 0;     // and the query rows' factors
+  static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + kRowScales + 1024;
 };
 
 // A KV tile's facts. Bit p of `valid`: position p's page is mapped, or nobody needs it.
@@ -211,10 +213,10 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t next) {
          (1ull << 46) | (2ull << 61);
 }
 
-// Instruction descriptor: bf16 operands, float32 accumulators, 128 x n; b_dims: B is stored
-// with its n index contiguous.
-__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_dims) {
-  return (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(b_dims) << 16) |
+// Instruction descriptor: bf16 (or f16) operands, float32 accumulators, 128 x n; b_dims: B is
+// stored with its n index contiguous.
+__host__ __device__ constexpr uint32_t tc_idesc(int n, bool b_dims, bool f16) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (static_cast<uint32_t>(b_dims) << 16) |
          (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 }
 
@@ -246,6 +248,12 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
       "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(d.x), "=f"(d.y)
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+__device__ __forceinline__ uint32_t mul2_f16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
@@ -510,15 +518,15 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_
   return true;
 }
 
-// The K tiles (128 threads) or V tiles (96) of a CTA, from 8-bit codes. K's threads also look
-// the positions up, one each, and publish the tile's facts and scales.
+// The K tiles (96 threads; f16) or V tiles (128; bf16) of a CTA, from 8-bit codes. V's threads
+// also look the positions up, one each, and publish the tile's facts and scales.
 template <int D, int kKind, bool kV>
 __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkList& list,
                                               const Work& w, int t, unsigned char* ring,
                                               float* s_scale, int* s_rows, Shared* sh) {
   using PL = Plan<D, true>;
   constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
-  constexpr int kThreads = kV ? 96 : 128;
+  constexpr int kThreads = kV ? 128 : 96;
   constexpr int kAll = kKv * kVec;
   // vectors are taken four a thread at a time, the next four on their way meanwhile; the loop
   // over the groups stays a loop (unrolled, the two converters and the softmax together ran
@@ -562,29 +570,30 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
     }
   };
   auto group_sync = [] { asm volatile("bar.sync 1, 224;" ::: "memory"); };
-  // a scale that goes into the conversion's own factor: a power of two of at most 2^7 (as
-  // td_quantise_append writes e4m3's for rows up to 448 * 2^7), or that of an absent row
+  // a scale that goes into the converted values: a power of two of at most 2^7 and, for K in
+  // f16, at least 2^-15 (as td_quantise_append writes e4m3's for rows with amax from 448 * 2^-15
+  // to 448 * 2^7), or that of an absent row
   auto folds = [](float s) {
     return (__float_as_uint(s) & 0x007FFFFFu) == 0 && s >= 0.0f && s <= 128.0f;
   };
   int row = -1;
   PageRef next{kNoPage, 0};
-  if constexpr (!kV) {
+  if constexpr (kV) {
     row = lookup(0).row(P);
     s_rows[t] = row;
     next = lookup(1);
   }
   group_sync();
   load(0, 0);
-  if constexpr (!kV) load_scales(row);
+  if constexpr (kV) load_scales(row);
   int slot = 0, parity = 1;
   bool ok = true;                         // after a time-out the group still meets its barriers
   for (int j = 0; j < w.n; ++j) {
     Info& info = sh->info[j % kInfo];
     float* scales = s_scale + (j % kInfo) * 2 * kKv;
-    if constexpr (!kV) {
+    if constexpr (kV) {
       const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
-      const bool fold = kKind == kCacheE4m3 && __all_sync(0xFFFFFFFFu, folds(ks) && folds(vs));
+      const bool fold = kKind == kCacheE4m3 && __all_sync(0xFFFFFFFFu, folds(ks) && (ks == 0.0f || ks >= 0x1p-15f) && folds(vs));
       if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
       if (lane == 0) {
         info.valid[t >> 5] = ~hole;
@@ -596,7 +605,7 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
       s_rows[((j + 1) & 3) * kKv + t] = row;
     }
     group_sync();
-    if constexpr (!kV) {
+    if constexpr (kV) {
       next = lookup(j + 2);
       load_scales(row);
     }
@@ -619,17 +628,29 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
         const int v = t + (group * 4 + i) * kThreads;
         if (!ok || v >= kAll) break;
         const int r = v / kVec;
-        uint32_t f = kE4m3Factor;
-        if constexpr (kKind == kCacheE4m3) {
-          const uint32_t g = __float_as_uint(scales[(kV ? kKv : 0) + r] * 0x1p120f) >> 16;
-          f = fold ? g | (g << 16) : f;
+        uint4 a, b;
+        if constexpr (kV) {
+          uint32_t f = kE4m3Factor;
+          if constexpr (kKind == kCacheE4m3) {
+            const uint32_t g = __float_as_uint(scales[kKv + r] * 0x1p120f) >> 16;
+            f = fold ? g | (g << 16) : f;
+          }
+          a = make_uint4(word_bf16<kKind, false>(q[i].x, f), word_bf16<kKind, true>(q[i].x, f),
+                         word_bf16<kKind, false>(q[i].y, f), word_bf16<kKind, true>(q[i].y, f));
+          b = make_uint4(word_bf16<kKind, false>(q[i].z, f), word_bf16<kKind, true>(q[i].z, f),
+                         word_bf16<kKind, false>(q[i].w, f), word_bf16<kKind, true>(q[i].w, f));
+        } else {
+          a = make_uint4(word_f16<kKind, false>(q[i].x), word_f16<kKind, true>(q[i].x),
+                         word_f16<kKind, false>(q[i].y), word_f16<kKind, true>(q[i].y));
+          b = make_uint4(word_f16<kKind, false>(q[i].z), word_f16<kKind, true>(q[i].z),
+                         word_f16<kKind, false>(q[i].w), word_f16<kKind, true>(q[i].w));
+          if constexpr (kKind == kCacheE4m3) {
+            const float g = fold ? scales[r] : 1.0f;
+            const uint32_t f = pack_f16(g, g);
+            a = make_uint4(mul2_f16(a.x, f), mul2_f16(a.y, f), mul2_f16(a.z, f), mul2_f16(a.w, f));
+            b = make_uint4(mul2_f16(b.x, f), mul2_f16(b.y, f), mul2_f16(b.z, f), mul2_f16(b.w, f));
+          }
         }
-        const uint4 a =
-            make_uint4(word_bf16<kKind, false>(q[i].x, f), word_bf16<kKind, true>(q[i].x, f),
-                       word_bf16<kKind, false>(q[i].y, f), word_bf16<kKind, true>(q[i].y, f));
-        const uint4 b =
-            make_uint4(word_bf16<kKind, false>(q[i].z, f), word_bf16<kKind, true>(q[i].z, f),
-                       word_bf16<kKind, false>(q[i].w, f), word_bf16<kKind, true>(q[i].w, f));
         *reinterpret_cast<uint4*>(tile + tile_at(r, swap ? c + 1 : c)) = swap ? b : a;
         *reinterpret_cast<uint4*>(tile + tile_at(r, swap ? c : c + 1)) = swap ? a : b;
       }
@@ -733,18 +754,21 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   unsigned char* s_v = s_k + PL::kK * PL::kTile;
   float* s_scale = reinterpret_cast<float*>(s_v + PL::kV * PL::kTile);
   int* s_rows = reinterpret_cast<int*>(reinterpret_cast<unsigned char*>(s_scale) + PL::kScales);
-  Shared* sh = reinterpret_cast<Shared*>(reinterpret_cast<unsigned char*>(s_rows) + PL::kPageRows);
+  float* s_row_scale =
+      reinterpret_cast<float*>(reinterpret_cast<unsigned char*>(s_rows) + PL::kPageRows);
+  Shared* sh = reinterpret_cast<Shared*>(reinterpret_cast<unsigned char*>(s_row_scale) +
+                                         PL::kRowScales);
   const bool two = w.nrows > kRows;      // both query tiles in use
 
   if (tid == 0) {
     mbar_init(&sh->q_full, two ? 256 : 128);
     for (int i = 0; i < PL::kK; ++i) {
-      mbar_init(&sh->k_full[i], k8 ? 128 : 1);
+      mbar_init(&sh->k_full[i], k8 ? 96 : 1);
       mbar_init(&sh->k_empty[i], 1);
     }
     for (int i = 0; i < PL::kV; ++i) {
       mbar_init(&sh->v_raw[i], 1);
-      mbar_init(&sh->v_full[i], k8 ? 96 : 1);
+      mbar_init(&sh->v_full[i], k8 ? 128 : 1);
       mbar_init(&sh->v_empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -812,9 +836,23 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           }
         }
 #pragma unroll
-        for (int i = 0; i < kVec; ++i)
+        for (int i = 0; i < kVec; ++i) {
+          if constexpr (k8) {      // f16 (K is), the row brought to its range: kVec lanes a row
+            uint32_t m = __vmaxu2(__vmaxu2(val[i].x & 0x7FFF7FFFu, val[i].y & 0x7FFF7FFFu),
+                                  __vmaxu2(val[i].z & 0x7FFF7FFFu, val[i].w & 0x7FFF7FFFu));
+#pragma unroll
+            for (int o = kVec / 2; o > 0; o >>= 1)
+              m = __vmaxu2(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+            float inverse, f[8];
+            const float mul = f16_scale(max(m & 0xFFFFu, m >> 16), &inverse);
+            unpack8(val[i], f);
+            val[i] = make_uint4(pack_f16(f[0] * mul, f[1] * mul), pack_f16(f[2] * mul, f[3] * mul),
+                                pack_f16(f[4] * mul, f[5] * mul), pack_f16(f[6] * mul, f[7] * mul));
+            if (c == 0) s_row_scale[wg * kRows + t / kVec + i * kStep] = inverse;
+          }
           *reinterpret_cast<uint4*>(dst + tile_at(t / kVec + i * kStep, c)) =
               make_uint4(val[i].x ^ flip, val[i].y ^ flip, val[i].z ^ flip, val[i].w ^ flip);
+        }
         fence_async_smem();
         mbar_arrive(&sh->q_full);
       }
@@ -828,12 +866,17 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + PL::kColO + wg * D;
       const uint32_t t_p = PL::kOwnP ? tmem + lanes + PL::kColP + wg * (kKv / 2) : t_s;
       uint64_t* s_empty = &sh->s_empty[wg];
-      // (never 0, which would turn the -infinity of a masked score into a NaN)
-      const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f);
+      // (never 0 below, which would turn the -infinity of a masked score into a NaN)
+      float scale = fabsf(A.scale_log2);
+      bool ok = true;
+      if constexpr (k8) {          // (the factors are the other threads')
+        ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->q_full, 0, sh, A.err));
+        scale *= s_row_scale[rr];
+      }
+      scale = fmaxf(scale, 1e-37f);
       float m_ref = -INFINITY;
       float2 sum = make_float2(0.0f, 0.0f);
-      bool ok = true;
-      for (int j = 0; j < w.n; ++j) {
+      for (int j = 0; ok && j < w.n; ++j) {
         // (the tensor memory's loads and stores are the whole warp's: it goes on or not as one)
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->s_full[wg], j & 1, sh, A.err));
         if (!ok) break;
@@ -928,7 +971,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     }
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- the products
-    constexpr uint32_t id_s = tc_idesc(kKv, false), id_o = tc_idesc(D, true);
+    constexpr uint32_t id_s = tc_idesc(kKv, false, k8), id_o = tc_idesc(D, true, false);
     const uint64_t q_desc = tc_desc(smem_u32(s_q), 16), k_desc = tc_desc(smem_u32(s_k), 16);
     const uint64_t v_desc = tc_desc(smem_u32(s_v), 128 * 128);
     // (a descriptor counts addresses in 16 bytes)
@@ -1121,11 +1164,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       }
     }
   } else {
-    // ------------------------- K and V from 8-bit codes: warps 12-15 make K, 9-11 V
+    // ------------------------- K and V from 8-bit codes: warps 12-15 make V, 9-11 K
     if (warp < kConvertWarp)
-      convert_tiles<D, kKind, true>(A, list, w, tid - kLoadWarp * 32, s_v, s_scale, s_rows, sh);
+      convert_tiles<D, kKind, false>(A, list, w, tid - kLoadWarp * 32, s_k, s_scale, s_rows, sh);
     else
-      convert_tiles<D, kKind, false>(A, list, w, tid - kConvertWarp * 32, s_k, s_scale, s_rows, sh);
+      convert_tiles<D, kKind, true>(A, list, w, tid - kConvertWarp * 32, s_v, s_scale, s_rows, sh);
   }
 
   __syncthreads();
