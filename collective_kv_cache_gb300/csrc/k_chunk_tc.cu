@@ -528,10 +528,11 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
   constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
   constexpr int kThreads = kV ? 128 : 96;
   constexpr int kAll = kKv * kVec;
-  // vectors are taken four a thread at a time, the next four on their way meanwhile; the loop
-  // over the groups stays a loop (unrolled, the two converters and the softmax together ran
-  // out of the instruction cache)
-  constexpr int kGroups = (kAll + 4 * kThreads - 1) / (4 * kThreads);
+  // vectors are taken several a thread at a time, the next ones on their way meanwhile (K's
+  // conversion is shorter, so more of it covers a load); the loop over the groups stays a loop
+  // (unrolled, the two converters and the softmax together ran out of the instruction cache)
+  constexpr int kMany = kV || D == 64 ? 4 : 6;
+  constexpr int kGroups = (kAll + kMany * kThreads - 1) / (kMany * kThreads);
   constexpr int kSlots = kV ? PL::kV : PL::kK;
   const int lane = t & 31;
   const PoolDev& P = A.pool;
@@ -545,16 +546,16 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
     const int pos = w.tile(min(j, w.n - 1)) * kKv + t;
     return page_ref(P, list.agent[w.x], pos, j < w.n && w.needed(pos, pos));
   };
-  uint4 code[4];
+  uint4 code[kMany];
   auto load = [&](int j, int group) {
-    int row[4];
+    int row[kMany];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int v = t + (group * 4 + i) * kThreads;
+    for (int i = 0; i < kMany; ++i) {
+      const int v = t + (group * kMany + i) * kThreads;
       row[i] = v < kAll ? s_rows[(j & 3) * kKv + v / kVec] : -1;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kMany; ++i) {
       code[i] = make_uint4(0u, 0u, 0u, 0u);
       if (row[i] >= 0)
         code[i] = __ldg(reinterpret_cast<const uint4*>(
@@ -618,14 +619,14 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
     const bool swap = D == 128 && (c & 8);
 #pragma unroll 1
     for (int group = 0; group < kGroups; ++group) {
-      uint4 q[4];
+      uint4 q[kMany];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) q[i] = code[i];
+      for (int i = 0; i < kMany; ++i) q[i] = code[i];
       if (group + 1 < kGroups) load(j, group + 1);
       else load(j + 1, 0);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int v = t + (group * 4 + i) * kThreads;
+      for (int i = 0; i < kMany; ++i) {
+        const int v = t + (group * kMany + i) * kThreads;
         if (!ok || v >= kAll) break;
         const int r = v / kVec;
         uint4 a, b;

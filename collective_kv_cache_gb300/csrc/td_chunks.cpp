@@ -315,7 +315,8 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
                               int32_t window, int32_t n_sink, void* out, float* lse,
                               cudaStream_t st) {
   const int H = c->g.H, D = c->g.D;
-  if ((D != 64 && D != 128) || n_q_heads < H || n_q_heads % H != 0 || !std::isfinite(scale) ||
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if ((D != 64 && D != 128) || n_q_heads < H || n_q_heads % H != 0 || !std::isfinite(scale_log2) ||
       window < 0 || n_sink < 0 || !layers_ok(c, layer_begin, layer_end))
     return TD_ERR_INVALID_ARG;
   int64_t tokens = 0;
@@ -338,9 +339,10 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   a.G = n_q_heads / H;
   a.nl = layer_end - layer_begin;
   a.layer_begin = layer_begin;
-  a.window = window;
-  a.n_sink = n_sink;
-  a.scale_log2 = scale * 1.4426950408889634f;
+  // (a window past every position is none; the kernels subtract it from positions)
+  a.window = window > kMaxPosition ? 0 : window;
+  a.n_sink = static_cast<int>(std::min<int64_t>(n_sink, kMaxPosition));
+  a.scale_log2 = scale_log2;
   a.err = c->d_err;
   // Sequences of at most kFewRows query rows per kv head go to the streaming kernel, the
   // others to the tensor-core kernel, each in lists of kMaxChunkSeqs. Plans first, so that

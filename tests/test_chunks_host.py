@@ -139,6 +139,7 @@ BAD = {
     "negative sinks": (("attend", "attend8"), dict(window=5, sinks=-1)),
     "a scale that is infinite": (("attend",), dict(scale=float("inf"))),
     "a scale that is NaN": (("attend",), dict(scale=float("nan"))),
+    "a scale past float32 in base 2": (("attend",), dict(scale=3e38)),
     "more rows than 31 bits": (("attend", "attend8"), dict(chunks=[(0, 0, 10**8)] * 2, nq=28)),
 }
 

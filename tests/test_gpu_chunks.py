@@ -362,6 +362,17 @@ def test_other_scales(td, lens, scale):
     _close(got, (out, lse, mag, dot.abs()), _weight_step(b, 3))
 
 
+@pytest.mark.parametrize("lens", [[1, 3], [100, 40]])
+def test_windows_and_sinks_of_any_size(td, lens):
+    """A window past every position is none, whatever the sinks; sinks past it keep all."""
+    b = ck.Batch([300, 7], lens, 2, 64, 16, seed=35)
+    pool, q = b.rows(*b.pool_shape()), b.rows(1, b.T, 4, 64)
+    pages, ctx = td.make_paged(pool, b.bt_t), _ctx(td, b)
+    want = ck.attend(b, pool[:, 0].double(), pool[:, 1].double(), q)
+    for window, sinks in ((2**31 - 1, 0), (2**31 - 1, 2**31 - 1), (2**30, 5), (1, 2**31 - 1)):
+        _close(_run_attention(td, b, pages, q, window, sinks, ctx=ctx), want, _weight_step(b, 2))
+
+
 def test_three_hundred_sequences_span_two_launches(td):
     rng = np.random.RandomState(1)
     for lens in ([1] * 300, list(rng.randint(0, 40, 300))):
