@@ -68,22 +68,30 @@ bool layers_ok(const td_ctx* c, int32_t begin, int32_t end) {
   return begin >= 0 && end <= c->shape.n_layers && begin < end;
 }
 
-// Fills the list with up to kMaxChunkSeqs of the call's sequences from *x on that `take`
-// accepts, and advances *x and *tok (the dense row of sequence *x's first token).
-template <typename Take>
-void fill_list(const td_chunks* ch, int* x, int64_t* tok, Take take, ChunkList* list) {
+// The list of the sequences order[*at], order[*at + 1], ... (at most kMaxChunkSeqs; *at moves
+// past them). tok: the dense row of each sequence's first token.
+void fill_list(const td_chunks* ch, const std::vector<int32_t>& order,
+               const std::vector<int32_t>& tok, size_t* at, ChunkList* list) {
   list->n = 0;
   list->row[0] = 0;
-  for (; *x < ch->n && list->n < kMaxChunkSeqs; ++*x) {
-    const int len = ch->len[*x];
-    if (take(len)) {
-      const int i = list->n++;
-      list->tok[i] = static_cast<int32_t>(*tok);
-      list->agent[i] = ch->agent[*x];
-      list->start[i] = ch->start[*x];
-      list->row[i + 1] = list->row[i] + len;
-    }
-    *tok += len;
+  for (; *at < order.size() && list->n < kMaxChunkSeqs; ++*at) {
+    const int x = order[*at], i = list->n++;
+    list->tok[i] = tok[x];
+    list->agent[i] = ch->agent[x];
+    list->start[i] = ch->start[x];
+    list->row[i + 1] = list->row[i] + ch->len[x];
+  }
+}
+
+// The sequences that have tokens, in the batch's order, and every sequence's first dense row.
+void sequences(const td_chunks* ch, std::vector<int32_t>* order, std::vector<int32_t>* tok) {
+  order->reserve(ch->n);
+  tok->reserve(ch->n);
+  int32_t sum = 0;
+  for (int x = 0; x < ch->n; ++x) {
+    tok->push_back(sum);
+    sum += ch->len[x];
+    if (ch->len[x] > 0) order->push_back(x);
   }
 }
 
@@ -134,11 +142,12 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   while (a.per_cta > 4 &&
          (tokens + a.per_cta - 1) / a.per_cta * a.nl * 2 < 4 * static_cast<int64_t>(c->sm_count))
     a.per_cta >>= 1;
-  int64_t tok = 0;
-  for (int x = 0; x < ch->n;) {
+  std::vector<int32_t> order, tok;
+  sequences(ch, &order, &tok);
+  for (size_t at = 0; at < order.size();) {
     ChunkList list;
-    a.tok0 = tok;
-    fill_list(ch, &x, &tok, [](int) { return true; }, &list);
+    a.tok0 = tok[order[at]];
+    fill_list(ch, order, tok, &at, &list);
     const cudaError_t e = write ? launch_quantise(a, list, kind, st)
                                 : launch_dequantise(a, list, kind, st);
     if (e != cudaSuccess) return TD_ERR_CUDA;
@@ -347,21 +356,31 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   // Sequences of at most kFewRows query rows per kv head go to the streaming kernel, the
   // others to the tensor-core kernel, each in lists of kMaxChunkSeqs. Plans first, so that
   // the scratch is there (or the call refused) before anything is launched.
-  const bool tc_pages = kind != kCacheBf16 || bf16_map(c, a, pool, &a.box_rows, &map);
+  std::vector<int32_t> all, tok, order[2];
+  sequences(ch, &all, &tok);
+  bool many = false;
+  for (const int32_t x : all) many |= static_cast<int64_t>(ch->len[x]) * a.G > kFewRows;
+  if (many && kind == kCacheBf16) many = bf16_map(c, a, pool, &a.box_rows, &map);
+  if (many) {
+    for (const int32_t x : all)
+      order[static_cast<int64_t>(ch->len[x]) * a.G > kFewRows].push_back(x);
+  } else {
+    order[0].swap(all);
+  }
+  // the longest contexts first: a unit of the tensor-core kernel takes an SM for as long as its
+  // context is long, and the last ones to start should be short
+  std::stable_sort(order[1].begin(), order[1].end(), [&](int32_t x, int32_t y) {
+    return ch->start[x] + ch->len[x] > ch->start[y] + ch->len[y];
+  });
   a.tx_pad = c->attn_tx_pad;
   size_t need = 0;
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1 && (s = chunk_scratch(c, need, st)) != TD_OK) return s;
     for (int tc = 0; tc < 2; ++tc) {
-      int64_t tok = 0;
-      for (int x = 0; x < ch->n;) {
+      for (size_t at = 0; at < order[tc].size();) {
         ChunkList list;
         ChunkUnits units;
-        fill_list(ch, &x, &tok, [&](int len) {
-          const bool few = !tc_pages || static_cast<int64_t>(len) * a.G <= kFewRows;
-          return len > 0 && few == (tc == 0);
-        }, &list);
-        if (list.n == 0) continue;
+        fill_list(ch, order[tc], tok, &at, &list);
         int rows = 0;
         const int64_t n = tc ? plan_tc(c, list, &a, &units, &rows)
                              : plan_rows(c, list, &a, &units, &rows);
