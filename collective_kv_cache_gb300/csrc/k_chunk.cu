@@ -762,7 +762,7 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 
 template <int D, int kKind>
 static cudaError_t run_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            int rows_per_tile, cudaStream_t st) {
+                            int rows_per_tile, bool fresh, cudaStream_t st) {
   const int64_t n = static_cast<int64_t>(a.nl) * a.g.H * units.base[list.n];
   if (n == 0) return cudaSuccess;
   const unsigned grid = static_cast<unsigned>(n);
@@ -770,26 +770,28 @@ static cudaError_t run_rows(const ChunkArgs& a, const ChunkList& list, const Chu
   constexpr int kSmem = kWarps * Y::depth * Y::stage;
   static_assert(kSmem >= kWarps * 16 * (D + 4) * 4, "the rings' space takes the warps' results");
   auto* kernel = rows_per_tile == 8 ? chunk_rows_kernel<D, kKind, 1> : chunk_rows_kernel<D, kKind, 2>;
-  const cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-  if (e != cudaSuccess) return e;
+  if (fresh) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_after(kernel, grid, kWarps * 32, kSmem, st, a, list, units);
 }
 
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                              CacheKind kind, int rows_per_tile, cudaStream_t st) {
+                              CacheKind kind, int rows_per_tile, bool fresh, cudaStream_t st) {
   if (a.g.D != 64 && a.g.D != 128) return cudaErrorInvalidValue;
   const bool wide = a.g.D == 128;
   switch (kind) {
     case kCacheBf16:
-      return wide ? run_rows<128, kCacheBf16>(a, list, units, rows_per_tile, st)
-                  : run_rows<64, kCacheBf16>(a, list, units, rows_per_tile, st);
+      return wide ? run_rows<128, kCacheBf16>(a, list, units, rows_per_tile, fresh, st)
+                  : run_rows<64, kCacheBf16>(a, list, units, rows_per_tile, fresh, st);
     case kCacheInt8:
-      return wide ? run_rows<128, kCacheInt8>(a, list, units, rows_per_tile, st)
-                  : run_rows<64, kCacheInt8>(a, list, units, rows_per_tile, st);
+      return wide ? run_rows<128, kCacheInt8>(a, list, units, rows_per_tile, fresh, st)
+                  : run_rows<64, kCacheInt8>(a, list, units, rows_per_tile, fresh, st);
     case kCacheE4m3:
-      return wide ? run_rows<128, kCacheE4m3>(a, list, units, rows_per_tile, st)
-                  : run_rows<64, kCacheE4m3>(a, list, units, rows_per_tile, st);
+      return wide ? run_rows<128, kCacheE4m3>(a, list, units, rows_per_tile, fresh, st)
+                  : run_rows<64, kCacheE4m3>(a, list, units, rows_per_tile, fresh, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -1184,30 +1184,32 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
 
 template <int D, int kKind>
 static cudaError_t run_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                          const CUtensorMap& map, cudaStream_t st) {
+                          const CUtensorMap& map, bool fresh, cudaStream_t st) {
   using PL = Plan<D, kKind != kCacheBf16>;
   const unsigned grid = static_cast<unsigned>(units.base[list.n]) * a.g.H * a.nl;
-  cudaError_t e = cudaFuncSetAttribute(chunk_tc_kernel<D, kKind>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kSmem);
-  if (e != cudaSuccess) return e;
+  if (fresh) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        chunk_tc_kernel<D, kKind>, cudaFuncAttributeMaxDynamicSharedMemorySize, PL::kSmem);
+    if (e != cudaSuccess) return e;
+  }
   return launch_after(chunk_tc_kernel<D, kKind>, grid, PL::kThreads, PL::kSmem, st, a, list, units,
                       map);
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap& map, CacheKind kind, cudaStream_t st) {
+                            const CUtensorMap& map, CacheKind kind, bool fresh, cudaStream_t st) {
   if (a.g.D != 64 && a.g.D != 128) return cudaErrorInvalidValue;
   const bool wide = a.g.D == 128;
   switch (kind) {
     case kCacheBf16:
-      return wide ? run_tc<128, kCacheBf16>(a, list, units, map, st)
-                  : run_tc<64, kCacheBf16>(a, list, units, map, st);
+      return wide ? run_tc<128, kCacheBf16>(a, list, units, map, fresh, st)
+                  : run_tc<64, kCacheBf16>(a, list, units, map, fresh, st);
     case kCacheInt8:
-      return wide ? run_tc<128, kCacheInt8>(a, list, units, map, st)
-                  : run_tc<64, kCacheInt8>(a, list, units, map, st);
+      return wide ? run_tc<128, kCacheInt8>(a, list, units, map, fresh, st)
+                  : run_tc<64, kCacheInt8>(a, list, units, map, fresh, st);
     case kCacheE4m3:
-      return wide ? run_tc<128, kCacheE4m3>(a, list, units, map, st)
-                  : run_tc<64, kCacheE4m3>(a, list, units, map, st);
+      return wide ? run_tc<128, kCacheE4m3>(a, list, units, map, fresh, st)
+                  : run_tc<64, kCacheE4m3>(a, list, units, map, fresh, st);
   }
   return cudaErrorInvalidValue;
 }

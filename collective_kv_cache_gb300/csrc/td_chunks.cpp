@@ -390,10 +390,13 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
         if (pass == 0) continue;
         a.part_o = c->d_chunk;
         a.part_ml = a.direct ? nullptr : c->d_chunk + static_cast<size_t>(n) * rows * D;
-        if ((tc ? launch_chunk_tc(a, list, units, map, kind, st)
-                : launch_chunk_rows(a, list, units, kind, rows, st)) != cudaSuccess ||
+        const uint32_t bit = 1u << (kind * 3 + (tc ? 2 : rows == 8));
+        const bool fresh = !(c->chunk_launched & bit);
+        if ((tc ? launch_chunk_tc(a, list, units, map, kind, fresh, st)
+                : launch_chunk_rows(a, list, units, kind, rows, fresh, st)) != cudaSuccess ||
             (!a.direct && launch_chunk_join(a, list, units, rows, st) != cudaSuccess))
           return TD_ERR_CUDA;
+        c->chunk_launched |= bit;
       }
     }
   }

@@ -264,13 +264,15 @@ struct ChunkArgs {
   uint32_t* err;
 };
 
-// Query rows (token, head of the group) per tile of the streaming kernel: 8 or 16.
+// Query rows (token, head of the group) per tile of the streaming kernel: 8 or 16. fresh (here
+// and below): the first launch of this kernel on the context's device, which allows it its
+// shared memory first.
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                              CacheKind kind, int rows_per_tile, cudaStream_t st);
+                              CacheKind kind, int rows_per_tile, bool fresh, cudaStream_t st);
 // The tensor-core kernel for many rows. map: the bf16 pool's rows of the call's layers, boxes
 // of box_rows x 64 (8-bit pages: not read).
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap& map, CacheKind kind, cudaStream_t st);
+                            const CUtensorMap& map, CacheKind kind, bool fresh, cudaStream_t st);
 // Joins the units of every query row.
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st);

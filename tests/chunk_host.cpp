@@ -44,7 +44,7 @@ cudaError_t launch_dequantise(const QuantArgs& a, const ChunkList& list, CacheKi
   return cudaSuccess;
 }
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                              CacheKind kind, int rows, cudaStream_t) {
+                              CacheKind kind, int rows, bool, cudaStream_t) {
   Launch& l = push(2, list);
   l.a = a;
   l.units = units;
@@ -53,7 +53,7 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
   return cudaSuccess;
 }
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap&, CacheKind kind, cudaStream_t) {
+                            const CUtensorMap&, CacheKind kind, bool, cudaStream_t) {
   Launch& l = push(4, list);
   l.a = a;
   l.units = units;
