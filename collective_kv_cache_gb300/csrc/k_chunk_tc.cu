@@ -9,21 +9,33 @@
 //   P_w = 2^(S_w - m)    (bf16, in TMEM: over S_w at D = 128, beside it at D = 64)
 //   O_w += P_w V         (float32 in TMEM; A operand from TMEM, V as stored: dims-major)
 // Warps 0-3 and 4-7 run the softmax of the two tiles, a thread a row, so that no statistic
-// crosses threads; one thread issues all products; the two tiles alternate, so that the tensor
+// crosses threads; one warp issues all products; the two tiles alternate, so that the tensor
 // core works on one while the other is in its softmax. Per KV tile and both query tiles the
-// products take 4 D 2^14 / 8192 = 1024 cycles (D = 128) and the 2 x 2^14 exponentials as many
-// (32 a cycle): the kernel is bound by both, and by the issue of the softmax.
+// 4 x 2^14 D multiply-adds take 2048 cycles at D = 128 and 1024 at D = 64 (4096 a cycle), the
+// 2 x 2^14 exponentials 1024 (32 a cycle): the products bound D = 128, both D = 64.
+//
+// Measured on one GB300: two chunks of 2048 tokens after 8192, 28 query heads on 4, D = 128,
+// take 353 us = 1.53 PFLOP/s (79% of what a large library product reaches), the products busy
+// for four fifths of the time; ragged spans of 1 to 301 tokens over pages of 24, whose boxes
+// are 8 rows, reach 1.29. Under a window of 1024 at D = 64 a block has 11 KV tiles, the first
+// and last of them partly masked: 322 us = 584 TFLOP/s of visible work (64 heads on 8, four
+// chunks of 1500 to 4097), a quarter of it the block's start and end and the rest bound by the
+// softmax's issue. e4m3 pages, four chunks of 500 to 700 after 4096 to 8192, 40 heads on 8,
+// D = 128: 395 us = 831 TFLOP/s, bound by the conversion of the codes, which every block does
+// for itself. Blocks that stay and take unit after unit lost 5 to 22% to this grid; a single
+// query tile a block, two blocks an SM, lost 13 to 23% at D = 64 (it loads K and V twice).
 //
 // The running maximum is lazy: m is raised, and O rescaled (in TMEM, by the softmax warps),
 // only when a row's maximum grew by more than 2^8; until then weights may reach 2^8, which
-// float32 sums and bf16's relative precision do not mind. The weights are rounded to bf16 (2^-9
-// relative, random) for the tensor cores, like the output; their sum is taken before, in
-// float32.
+// float32 sums and bf16's relative precision do not mind. The weights are rounded to bf16 (at
+// most 2^-8 relative) for the tensor cores, as the output is; their sum is taken before, in
+// float32. (Split in two parts as in the streaming kernel they would cost half the products'
+// time again.)
 //
 // bf16 pages: a tile arrives as boxes of 8 to 128 rows x 64 dims, each inside one page
 // (tensor map, 128-byte swizzle), K on a ring of its own, V on another. Every V tile passes
-// two patch warps before the products read it: where a tile holds positions that some row
-// does not see, they clear the rows that none sees (their bytes may be anything) and watch for
+// a patch warp before the products read it: where a tile holds positions that some row does
+// not see, it clears the rows that none sees (their bytes may be anything) and watches for
 // infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
 // value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
 // 8-bit pages: three warps load K's codes and four V's, turn them into f16 and bf16 (exact) and
@@ -381,8 +393,8 @@ __device__ __forceinline__ int64_t out_row(const ChunkArgs& A, const ChunkList& 
          w.h * A.G + (r - tok * A.G);
 }
 
-// Columns of a chunk of 32 that a row sees: c <= hi and (c > lo or c < sk), chunk-relative.
-__device__ __forceinline__ uint32_t first_bits(int n) {   // the lowest n bits
+// The lowest n bits of a word (none for n <= 0, all from 32 on).
+__device__ __forceinline__ uint32_t first_bits(int n) {
   return n <= 0 ? 0u : (n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1u);
 }
 
@@ -594,7 +606,9 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
     float* scales = s_scale + (j % kInfo) * 2 * kKv;
     if constexpr (kV) {
       const uint32_t hole = __ballot_sync(0xFFFFFFFFu, row == -2);
-      const bool fold = kKind == kCacheE4m3 && __all_sync(0xFFFFFFFFu, folds(ks) && (ks == 0.0f || ks >= 0x1p-15f) && folds(vs));
+      const bool fold =
+          kKind == kCacheE4m3 &&
+          __all_sync(0xFFFFFFFFu, folds(ks) && (ks == 0.0f || ks >= 0x1p-15f) && folds(vs));
       if (hole && lane == 0) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
       if (lane == 0) {
         info.valid[t >> 5] = ~hole;
@@ -896,19 +910,21 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             if (w.window) b &= ~first_bits(hi - w.window + 1 - c * 32) | first_bits(sk - c * 32);
             seen[c] = b & in[c];
           }
-          ok = scaled ? softmax_tile<D, k8, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv, j == 0,
-                                                  &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
-                                                  m_ref, sum, sh, A.err)
-                      : softmax_tile<D, false, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv, j == 0,
-                                                     &sh->o_done[wg], (j - 1) & 1,
-                                                     sh->p_ready[wg], m_ref, sum, sh, A.err);
+          ok = scaled
+                   ? softmax_tile<D, k8, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv,
+                                               j == 0, &sh->o_done[wg], (j - 1) & 1,
+                                               sh->p_ready[wg], m_ref, sum, sh, A.err)
+                   : softmax_tile<D, false, true>(t_s, t_o, t_p, s_empty, seen, scale, ks,
+                                                  ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
+                                                  sh->p_ready[wg], m_ref, sum, sh, A.err);
         } else {
-          ok = scaled ? softmax_tile<D, k8, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks, ks + kKv, j == 0,
-                                                   &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg],
-                                                   m_ref, sum, sh, A.err)
-                      : softmax_tile<D, false, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks, ks + kKv,
-                                                      j == 0, &sh->o_done[wg], (j - 1) & 1,
-                                                      sh->p_ready[wg], m_ref, sum, sh, A.err);
+          ok = scaled
+                   ? softmax_tile<D, k8, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
+                                                ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
+                                                sh->p_ready[wg], m_ref, sum, sh, A.err)
+                   : softmax_tile<D, false, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
+                                                   ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
+                                                   sh->p_ready[wg], m_ref, sum, sh, A.err);
         }
         if (!ok) break;
       }

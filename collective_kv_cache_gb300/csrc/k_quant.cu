@@ -8,8 +8,11 @@
 // steps are uniform, so its scale uses the whole range and the nearest code is decided by the
 // exact residual x - n s (below). Reading back: bf16(fl32(code * s)).
 //
-// Both kernels move 2 + 1 + 4/D bytes an element once and are bound by HBM. A group of lanes
-// holds one head row, so the row's maximum is a few shuffles and no row is read twice. The
+// Both kernels move 2 + 1 + 4/D bytes an element once and are bound by HBM: ten
+// chunks of 300 to 1100 tokens, 28 layers of 4 heads, D = 128, are written as e4m3 in 89.5 us,
+// and ten of 5120 tokens, 8 layers of 8 heads, read back in 374 us, both at 6.7 to 6.8 TB/s, a
+// copy's rate. A call of a few tokens takes 8 us, which are the launch. A group of lanes holds
+// one head row, so the row's maximum is a few shuffles and no row is read twice. The
 // write takes 16 elements a lane: with 8 the shuffles, scales and addresses cost twice as much
 // an element and it ran at 80% of the copy rate, bound by their issue. The read takes 8 (one
 // 16-byte store a lane, whole lines a warp): with 16 it ran at 92%. A CTA takes up to
@@ -238,8 +241,10 @@ template <int kKind, bool kWrite>
 static cudaError_t run_kind(const QuantArgs& a, const ChunkList& list, dim3 grid,
                             cudaStream_t st) {
   constexpr int k64 = kWrite ? 2 : 3;
-  if (a.g.D == 128) return launch_after(quant_kernel<kKind, kWrite, k64 + 1>, grid, kThreads, 0, st, a, list);
-  if (a.g.D == 64) return launch_after(quant_kernel<kKind, kWrite, k64>, grid, kThreads, 0, st, a, list);
+  if (a.g.D == 128)
+    return launch_after(quant_kernel<kKind, kWrite, k64 + 1>, grid, kThreads, 0, st, a, list);
+  if (a.g.D == 64)
+    return launch_after(quant_kernel<kKind, kWrite, k64>, grid, kThreads, 0, st, a, list);
   return launch_after(quant_kernel<kKind, kWrite, -1>, grid, kThreads, 0, st, a, list);
 }
 

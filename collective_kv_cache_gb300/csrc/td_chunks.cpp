@@ -173,6 +173,12 @@ td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
   return TD_OK;
 }
 
+// Query rows of a sequence (per kv head) up to which the streaming kernel takes it. One more and
+// it would read the pages twice over: 28 rows on 4000 to 6000 positions of 32 agents take 66 us
+// on the tensor-core kernel and 146 on the streaming one (D = 128; 44 and 83 at D = 64, int8
+// pages 114 and 116), 56 rows 67 and 257. Short contexts lean the other way by a little (30
+// rows on 1000 positions: 15.1 and 13.1 us), and up to 16 rows the tensor-core kernel's tile of
+// 128 is mostly empty.
 constexpr int kFewRows = 16;
 
 // The bf16 pages of the call's layers as a tensor map of boxes that lie inside a page; false
@@ -312,7 +318,8 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
       // a window's positions may straddle one tile more, the first ones' another
       [&](int x) {
-        const int64_t all = (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
+        const int64_t all =
+            (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
         return a->window ? std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2) : all;
       },
       1, a, units);
@@ -333,7 +340,8 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   if (s != TD_OK) return s;
   if (tokens == 0) return TD_OK;
   if (!q || !out || !aligned16(q) || !aligned16(out) ||
-      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 || tokens > INT32_MAX / n_q_heads / (layer_end - layer_begin))
+      (reinterpret_cast<uintptr_t>(lse) & 3u) != 0 ||
+      tokens > INT32_MAX / n_q_heads / (layer_end - layer_begin))
     return TD_ERR_INVALID_ARG;
   ChunkArgs a{};
   CUtensorMap map{};

@@ -429,8 +429,8 @@ td_status td_dequantise_read(td_ctx* ctx, const td_chunks* chunks, const td_page
  *   q     DEVICE bf16 [layer_end-layer_begin][T][n_q_heads][D], rotated, 16-byte aligned
  *   out   DEVICE bf16, as q
  *   lse   DEVICE float [layer_end-layer_begin][T][n_q_heads], or NULL
- * n_q_heads a multiple of H, (layer_end-layer_begin) * T * n_q_heads < 2^31; head dims 64 and 128 (else
- * TD_ERR_INVALID_ARG).
+ * n_q_heads a multiple of H, (layer_end-layer_begin) * T * n_q_heads < 2^31; head dims 64
+ * and 128; scale finite, also in base 2 (else TD_ERR_INVALID_ARG).
  * The context owns the partial results' scratch, which grows with the calls: a call made in a
  * stream capture must find it large enough (make the call once before capturing it; else
  * TD_ERR_INVALID_ARG). */
