@@ -28,7 +28,7 @@ CXX_FLAGS = ["-O2", "-std=c++17", "-fPIC", "-ffp-contract=off", "-fno-fast-math"
 
 CU_SOURCES = ["k_rerotate.cu", "k_select.cu", "k_master.cu", "k_encode.cu", "k_restore.cu",
               "k_variants.cu", "td_noalloc.cu", "k_attention.cu", "k_quant.cu",
-              "k_chunk.cu", "k_chunk_tc.cu"]
+              "k_chunk.cu", "k_chunk_tc.cu", "k_expand.cu"]
 CXX_SOURCES = ["td_host.cpp", "td_chunks.cpp", "td_rounds.cpp"]
 HEADERS = ["td_internal.h", "td_ctx.h", "td_device.cuh",
            "td_cache8.cuh"]

@@ -21,8 +21,8 @@
 // and last of them partly masked: 322 us = 584 TFLOP/s of visible work (64 heads on 8, four
 // chunks of 1500 to 4097), a quarter of it the block's start and end and the rest bound by the
 // softmax's issue. e4m3 pages, four chunks of 500 to 700 after 4096 to 8192, 40 heads on 8,
-// D = 128: 395 us = 831 TFLOP/s, bound by the conversion of the codes, which every block does
-// for itself. Blocks that stay and take unit after unit lost 5 to 22% to this grid; a single
+// D = 128: 274 us = 1.20 PFLOP/s with the pages unfolded first; converted by every block for
+// itself they took 395. Blocks that stay and take unit after unit lost 5 to 22% to this grid; a single
 // query tile a block, two blocks an SM, lost 13 to 23% at D = 64 (it loads K and V twice).
 //
 // The running maximum is lazy: m is raised, and O rescaled (in TMEM, by the softmax warps),
@@ -38,7 +38,9 @@
 // not see, it clears the rows that none sees (their bytes may be anything) and watches for
 // infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
 // value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
-// 8-bit pages: three warps load K's codes and four V's, turn them into f16 and bf16 (exact) and
+// 8-bit pages of long chunks are unfolded before (k_expand.cu): their tiles lie together, whole,
+// with zeros where nothing is seen, and come by TMA without a table or a patch; one warp
+// brings the positions' scales. For chunks of few rows three warps load K's codes and four V's, turn them into f16 and bf16 (exact) and
 // store them as the same tiles; the queries become f16 too, each row with a power of two that
 // brings it to f16's range. The scale of K's row goes on the score's column, that of V's on the
 // weight's; powers of two (e4m3 as td_quantise_append writes it) go into the conversion
@@ -61,22 +63,30 @@ constexpr int kPatchWarp = 11;
 constexpr int kConvertWarp = 12;      // 8-bit: the first of four that convert V (9-11: K)
 constexpr int kInfo = 8;              // KV tiles whose facts are kept
 
-template <int D, bool k8>
+// Kinds of the kernel: CacheKind, or 8-bit pages' unfolded copy.
+constexpr int kUnfolded = 3;
+__host__ __device__ constexpr bool converts(int kind) {
+  return kind == kCacheInt8 || kind == kCacheE4m3;
+}
+
+template <int D, int kKind>
 struct Plan {
+  static constexpr bool k8 = converts(kKind);
   static constexpr int kTile = kKv * D * 2;              // bytes of a K or V tile
   static constexpr int kQ = 2 * kRows * D * 2;
   // K and V tiles in flight. One CTA an SM either way (TMEM is taken whole): D = 64 leaves
   // room for more, and must take more than half of the shared memory
-  static constexpr int kK = D == 64 ? 4 : (k8 ? 2 : 3);
+  // (at D = 128 the scales take the third K tile's place)
+  static constexpr int kK = D == 64 ? 4 : (kKind == kCacheBf16 ? 3 : 2);
   static constexpr int kV = D == 64 ? 4 : 2;
   // TMEM columns: two S, two O, and at D = 64 two P of their own: the next scores may then be
   // computed while the softmax still works on the last ones (at D = 128 P lies over S)
   static constexpr bool kOwnP = D == 64;
   static constexpr uint32_t kColO = 2 * kKv, kColP = 2 * kKv + 2 * D;
   static constexpr int kThreads = k8 ? 512 : 384;
-  // 8-bit pages: the last KV tiles' scales, four tiles' page rows (a thread may write those of
-  // tile j + 2 while another still reads tile j's)
-  static constexpr int kScales = k8 ? kInfo * 2 * kKv * 4 : 0;
+  // 8-bit pages: the last KV tiles' scales; where they are converted here, four tiles' page rows
+  // (a thread may write those of tile j + 2 while another still reads tile j's)
+  static constexpr int kScales = kKind != kCacheBf16 ? kInfo * 2 * kKv * 4 : 0;
   static constexpr int kPageRows = k8 ? 4 * kKv * 4 : 0;
   static constexpr int kRowScales = k8 ? 2 * kRows * 4 : 0;     // and the query rows' factors
   static constexpr int kSmem = 1024 + kQ + (kK + kV) * kTile + kScales + kPageRows + kRowScales + 1024;
@@ -421,7 +431,7 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_
   tc_wait_ld(x[0]);
 #pragma unroll
   for (int c = 1; c < 4; ++c) tc_loaded(x[c]);
-  constexpr bool kOwnP = Plan<D, false>::kOwnP;
+  constexpr bool kOwnP = Plan<D, kCacheBf16>::kOwnP;
   if constexpr (kOwnP) {
     tc_fence_before();
     __syncwarp();
@@ -536,7 +546,7 @@ template <int D, int kKind, bool kV>
 __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkList& list,
                                               const Work& w, int t, unsigned char* ring,
                                               float* s_scale, int* s_rows, Shared* sh) {
-  using PL = Plan<D, true>;
+  using PL = Plan<D, kKind>;
   constexpr int kVec = D / 16;                          // 16-byte vectors of codes per row
   constexpr int kThreads = kV ? 128 : 96;
   constexpr int kAll = kKv * kVec;
@@ -746,11 +756,12 @@ __device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list
 }  // namespace
 
 template <int D, int kKind>
-__global__ void __launch_bounds__(Plan<D, kKind != kCacheBf16>::kThreads, 1)
+__global__ void __launch_bounds__(Plan<D, kKind>::kThreads, 1)
 chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ ChunkList list,
-                const __grid_constant__ ChunkUnits units, const __grid_constant__ CUtensorMap map) {
-  constexpr bool k8 = kKind != kCacheBf16;
-  using PL = Plan<D, k8>;
+                const __grid_constant__ ChunkUnits units, const __grid_constant__ DenseTiles dense,
+                const __grid_constant__ CUtensorMap map) {
+  using PL = Plan<D, kKind>;
+  constexpr bool k8 = PL::k8, kScaled = kKind != kCacheBf16;
   extern __shared__ unsigned char s_dyn[];
   const Work w = work_of(A, list, units);
   const int tid = threadIdx.x, lane = tid & 31;
@@ -899,7 +910,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         const int kt = w.tile(j);
         const uint4 valid = sh->info[j % kInfo].load();
         const float* ks = s_scale + (j % kInfo) * 2 * kKv;
-        const bool scaled = k8 && !sh->info[j % kInfo].all_folded();
+        const bool scaled = kScaled && !sh->info[j % kInfo].all_folded();
         if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
           const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
           uint32_t seen[4];
@@ -911,7 +922,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             seen[c] = b & in[c];
           }
           ok = scaled
-                   ? softmax_tile<D, k8, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv,
+                   ? softmax_tile<D, kScaled, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv,
                                                j == 0, &sh->o_done[wg], (j - 1) & 1,
                                                sh->p_ready[wg], m_ref, sum, sh, A.err)
                    : softmax_tile<D, false, true>(t_s, t_o, t_p, s_empty, seen, scale, ks,
@@ -919,7 +930,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
                                                   sh->p_ready[wg], m_ref, sum, sh, A.err);
         } else {
           ok = scaled
-                   ? softmax_tile<D, k8, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
+                   ? softmax_tile<D, kScaled, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
                                                 ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
                                                 sh->p_ready[wg], m_ref, sum, sh, A.err)
                    : softmax_tile<D, false, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
@@ -1006,8 +1017,11 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       __syncwarp();
     };
     const int last = two ? 1 : 0;
-    bool ok = wait_or_abort(&sh->q_full, 0, sh, A.err) &&
-              wait_or_abort(&sh->k_full[0], 0, sh, A.err);
+    auto keys = [&](int slot, int parity) {       // a K tile, and its scales
+      return wait_or_abort(&sh->k_full[slot], parity, sh, A.err) &&
+             (kKind != kUnfolded || wait_or_abort(&sh->v_raw[slot], parity, sh, A.err));
+    };
+    bool ok = wait_or_abort(&sh->q_full, 0, sh, A.err) && keys(0, 0);
     ok = __all_sync(0xFFFFFFFFu, ok);
     if (ok) {
       tc_fence_after();
@@ -1022,7 +1036,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       }
       // the next scores of a query tile: once its S is free
       auto next_scores = [&](int wg) {
-        if (wg == 0) ok = wait_or_abort(&sh->k_full[ks], k_par, sh, A.err);
+        if (wg == 0) ok = keys(ks, k_par);
         if constexpr (PL::kOwnP) ok = ok && wait_or_abort(&sh->s_empty[wg], j & 1, sh, A.err);
         ok = __all_sync(0xFFFFFFFFu, ok);
         if (!ok) return;
@@ -1067,7 +1081,85 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     if (elected()) tc_commit(&sh->drain);
     __syncwarp();
     mbar_wait_bounded(&sh->drain, 0);
-  } else if constexpr (!k8) {
+  } else if constexpr (kKind == kUnfolded) {
+    const DenseSpan span = dense_span(w.start, w.len, w.window, w.n_sink);
+    const int first = dense.base[w.x];
+    if (warp < kPatchWarp) {
+      // --------------------------- K (first warp) or V (second) by TMA, tiles lie together
+      const bool is_v = warp != kLoadWarp;
+      const int plane = (2 * w.li + is_v) * A.dense_rows;
+      const int slots = is_v ? PL::kV : PL::kK;
+      const uint32_t ring = smem_u32(is_v ? s_v : s_k);
+      uint64_t* full = is_v ? sh->v_full : sh->k_full;
+      uint64_t* empty = is_v ? sh->v_empty : sh->k_empty;
+      int slot = 0, parity = 1, n = 0;                    // n: tiles started
+      for (; n < w.n; ++n) {
+        if (n >= slots &&
+            !__all_sync(0xFFFFFFFFu, wait_or_abort(&empty[slot], parity, sh, A.err)))
+          break;
+        const int row = plane + (first + span.index(w.tile(n))) * kKv;
+        if (elected()) {
+          mbar_arrive_expect_tx(&full[slot], PL::kTile + A.tx_pad);
+#pragma unroll
+          for (int half = 0; half < D / 64; ++half)
+            tma_box(ring + slot * PL::kTile + half * (128 * 128), &map, w.h * D + half * 64, row,
+                    &full[slot]);
+        }
+        __syncwarp();
+        if (++slot == slots) {
+          slot = 0;
+          parity ^= 1;
+        }
+      }
+      // the copies that were started land before the block goes, time-out or not
+      for (int i = max(0, n - slots); i < n; ++i)
+        mbar_wait_bounded(&full[i % slots], (i / slots) & 1);
+    } else {
+      // ---------- the tiles' scales and what they tell, beside K's tiles (in V's first barrier,
+      // which this kind has no other use for)
+      static_assert(PL::kK <= PL::kV, "a barrier for every K tile");
+      const float* src = A.dense_scale +
+                         (static_cast<int64_t>(w.li) * 2 * A.g.H + w.h) * A.dense_rows;
+      const int64_t v_off = static_cast<int64_t>(A.g.H) * A.dense_rows;
+      auto load = [&](int j, uint4* k, uint4* v) {
+        const float* at = src + (first + span.index(w.tile(min(j, w.n - 1)))) * kKv + lane * 4;
+        *k = __ldg(reinterpret_cast<const uint4*>(at));
+        *v = __ldg(reinterpret_cast<const uint4*>(at + v_off));
+      };
+      uint4 nk, nv;
+      load(0, &nk, &nv);
+      int slot = 0, parity = 1;
+      for (int j = 0; j < w.n; ++j) {
+        const uint4 k = nk, v = nv;
+        load(j + 1, &nk, &nv);
+        if (j >= PL::kK &&
+            !__all_sync(0xFFFFFFFFu, wait_or_abort(&sh->k_empty[slot], parity, sh, A.err)))
+          break;
+        float* to = s_scale + (j % kInfo) * 2 * kKv + lane * 4;
+        *reinterpret_cast<uint4*>(to) = k;
+        *reinterpret_cast<uint4*>(to + kKv) = v;
+        constexpr uint32_t kOne = 0x3F800000u;
+        const uint32_t holes = (k.x == kHole) | (k.y == kHole) << 1 | (k.z == kHole) << 2 |
+                               (k.w == kHole) << 3;
+        const bool ones = k.x == kOne && k.y == kOne && k.z == kOne && k.w == kOne &&
+                          v.x == kOne && v.y == kOne && v.z == kOne && v.w == kOne;
+        uint32_t word = holes << (4 * (lane & 7));        // eight lanes make a word
+#pragma unroll
+        for (int o = 1; o < 8; o *= 2) word |= __shfl_xor_sync(0xFFFFFFFFu, word, o);
+        const bool all = __all_sync(0xFFFFFFFFu, ones);
+        if ((lane & 7) == 0) {
+          sh->info[j % kInfo].valid[lane >> 3] = ~word;
+          sh->info[j % kInfo].folded[lane >> 3] = all;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->v_raw[slot]);
+        if (++slot == PL::kK) {
+          slot = 0;
+          parity ^= 1;
+        }
+      }
+    }
+  } else if constexpr (kKind == kCacheBf16) {
     if (warp < kPatchWarp) {
       // ------------------------------------- K (first warp) or V (second) by TMA
       const bool is_v = warp != kLoadWarp;
@@ -1189,7 +1281,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   }
 
   __syncthreads();
-  if constexpr (!k8) {
+  if constexpr (kKind == kCacheBf16) {
     if (sh->bad && !sh->abort && warp < kSoftmaxWarps) slow_rows<D>(A, list, units, warp);
   }
   if (warp == kMmaWarp) {
@@ -1200,8 +1292,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
 
 template <int D, int kKind>
 static cudaError_t run_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                          const CUtensorMap& map, bool fresh, cudaStream_t st) {
-  using PL = Plan<D, kKind != kCacheBf16>;
+                          const DenseTiles& dense, const CUtensorMap& map, bool fresh,
+                          cudaStream_t st) {
+  using PL = Plan<D, kKind>;
   const unsigned grid = static_cast<unsigned>(units.base[list.n]) * a.g.H * a.nl;
   if (fresh) {
     const cudaError_t e = cudaFuncSetAttribute(
@@ -1209,23 +1302,27 @@ static cudaError_t run_tc(const ChunkArgs& a, const ChunkList& list, const Chunk
     if (e != cudaSuccess) return e;
   }
   return launch_after(chunk_tc_kernel<D, kKind>, grid, PL::kThreads, PL::kSmem, st, a, list, units,
-                      map);
+                      dense, map);
 }
 
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap& map, CacheKind kind, bool fresh, cudaStream_t st) {
+                            const DenseTiles& dense, const CUtensorMap& map, CacheKind kind,
+                            bool fresh, cudaStream_t st) {
   if (a.g.D != 64 && a.g.D != 128) return cudaErrorInvalidValue;
   const bool wide = a.g.D == 128;
-  switch (kind) {
+  switch (a.dense ? kUnfolded : kind) {
     case kCacheBf16:
-      return wide ? run_tc<128, kCacheBf16>(a, list, units, map, fresh, st)
-                  : run_tc<64, kCacheBf16>(a, list, units, map, fresh, st);
+      return wide ? run_tc<128, kCacheBf16>(a, list, units, dense, map, fresh, st)
+                  : run_tc<64, kCacheBf16>(a, list, units, dense, map, fresh, st);
     case kCacheInt8:
-      return wide ? run_tc<128, kCacheInt8>(a, list, units, map, fresh, st)
-                  : run_tc<64, kCacheInt8>(a, list, units, map, fresh, st);
+      return wide ? run_tc<128, kCacheInt8>(a, list, units, dense, map, fresh, st)
+                  : run_tc<64, kCacheInt8>(a, list, units, dense, map, fresh, st);
     case kCacheE4m3:
-      return wide ? run_tc<128, kCacheE4m3>(a, list, units, map, fresh, st)
-                  : run_tc<64, kCacheE4m3>(a, list, units, map, fresh, st);
+      return wide ? run_tc<128, kCacheE4m3>(a, list, units, dense, map, fresh, st)
+                  : run_tc<64, kCacheE4m3>(a, list, units, dense, map, fresh, st);
+    case kUnfolded:
+      return wide ? run_tc<128, kUnfolded>(a, list, units, dense, map, fresh, st)
+                  : run_tc<64, kUnfolded>(a, list, units, dense, map, fresh, st);
   }
   return cudaErrorInvalidValue;
 }

@@ -181,9 +181,45 @@ td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
 // 128 is mostly empty.
 constexpr int kFewRows = 16;
 
+// Over 8-bit pages the tensor-core kernel converts the codes itself for up to two tiles of query
+// rows (of 256); from three on they are unfolded once, before it. Two tiles of 480 rows on 12000
+// positions of 16 agents take 254 us converted in the kernel and 266 unfolded (int8, 4 kv heads,
+// D = 128; 2000 positions of 8: 43 and 47), 960 rows 559 and 419 (54 and 51), 2560 rows 1240
+// and 888 (157 and 120). At D = 64 the crossing is the same.
+constexpr int kOwnRows = 512;
+// The unfolded copy of one launch, at most: sequences that would pass it go to the next one, a
+// sequence that is longer by itself is converted in the kernel.
+constexpr int64_t kDenseBytes = int64_t{1} << 30;
+
+// KV tiles of sequence x's unfolded copy, and a tile's bytes over the call's layers.
+int64_t dense_tiles(const td_chunks* ch, int x, const ChunkArgs& a) {
+  return dense_span(ch->start[x], ch->len[x], a.window, a.n_sink).n;
+}
+int64_t dense_tile_bytes(const ChunkArgs& a) {
+  return static_cast<int64_t>(a.nl) * 2 * 128 * (a.g.E * 2 + a.g.H * 4);
+}
+
+// The first tiles of the list's sequences; those that do not fit go back to the order.
+void fill_dense(const td_chunks* ch, const std::vector<int32_t>& order, const ChunkArgs& a,
+                size_t* at, ChunkList* list, DenseTiles* dense) {
+  const int64_t most = kDenseBytes / dense_tile_bytes(a);
+  const size_t first = *at - list->n;
+  int64_t sum = 0;
+  int n = 0;
+  dense->base[0] = 0;
+  for (; n < list->n; ++n) {
+    sum += dense_tiles(ch, order[first + n], a);
+    if (sum > most) break;
+    dense->base[n + 1] = static_cast<int32_t>(sum);
+  }
+  *at -= list->n - n;
+  list->n = n;
+}
+
 // The bf16 pages of the call's layers as a tensor map of boxes that lie inside a page; false
 // where the tensor-core kernel cannot read them: pages that are no multiple of 8 tokens (a
 // box is at least 8 rows, the period of the swizzle), or more rows than a coordinate counts.
+bool row_map(int E, uint16_t* base, int64_t rows, int b, CUtensorMap* m);
 bool bf16_map(const td_ctx* c, const ChunkArgs& a, const PoolDev& pool, int* box, CUtensorMap* m) {
   if (pool.P % 8 != 0) return false;
   const int64_t plane = pool.num_pages * pool.P;
@@ -192,10 +228,14 @@ bool bf16_map(const td_ctx* c, const ChunkArgs& a, const PoolDev& pool, int* box
   int b = 8;
   while (b < 128 && pool.P % (2 * b) == 0) b *= 2;
   *box = b;
+  const int E = c->g.E;
+  return row_map(E, pool.base + static_cast<int64_t>(a.layer_begin) * 2 * plane * E, rows, b, m);
+}
+
+// Rows of E bf16 as a tensor map of boxes of b rows x 64.
+bool row_map(int E, uint16_t* base, int64_t rows, int b, CUtensorMap* m) {
   EncodeTiledFn fn = encode_tiled();
   if (!fn) return false;
-  const int E = c->g.E;
-  uint16_t* base = pool.base + static_cast<int64_t>(a.layer_begin) * 2 * plane * E;
   const cuuint64_t dims[2] = {static_cast<cuuint64_t>(E), static_cast<cuuint64_t>(rows)};
   const cuuint64_t strides[1] = {static_cast<cuuint64_t>(E) * 2};
   const cuuint32_t bx[2] = {64, static_cast<cuuint32_t>(b)};
@@ -310,9 +350,10 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
   const int R = *rows = a->rows_cta = most <= 128 ? 128 : 256;
   // one CTA an SM; a KV tile's products and softmax
-  const double step = a->scale ? 2.4 : (a->g.D == 128 ? 1.4 : 0.8);
+  const bool codes = a->scale && !a->dense_rows;
+  const double step = codes ? 2.4 : (a->g.D == 128 ? 1.4 : 0.8);
   const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, step, 4.0,
-                  2.0 * 128 * a->g.D * (a->scale ? 1 : 2) / 8, 2, partial_bytes(list, *a)};
+                  2.0 * 128 * a->g.D * (codes ? 1 : 2) / 8, 2, partial_bytes(list, *a)};
   return cut(
       list, cost,
       [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
@@ -362,46 +403,67 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
   a.scale_log2 = scale_log2;
   a.err = c->d_err;
   // Sequences of at most kFewRows query rows per kv head go to the streaming kernel, the
-  // others to the tensor-core kernel, each in lists of kMaxChunkSeqs. Plans first, so that
-  // the scratch is there (or the call refused) before anything is launched.
-  std::vector<int32_t> all, tok, order[2];
+  // others to the tensor-core kernel, those of many rows over 8-bit pages by way of the
+  // unfolded copy; each in lists of kMaxChunkSeqs. Plans first, so that the scratch is there
+  // (or the call refused) before anything is launched.
+  std::vector<int32_t> all, tok, order[3];
   sequences(ch, &all, &tok);
   bool many = false;
   for (const int32_t x : all) many |= static_cast<int64_t>(ch->len[x]) * a.G > kFewRows;
   if (many && kind == kCacheBf16) many = bf16_map(c, a, pool, &a.box_rows, &map);
-  if (many) {
-    for (const int32_t x : all)
-      order[static_cast<int64_t>(ch->len[x]) * a.G > kFewRows].push_back(x);
-  } else {
-    order[0].swap(all);
+  const int64_t most_tiles =
+      kind != kCacheBf16 && encode_tiled() ? kDenseBytes / dense_tile_bytes(a) : 0;
+  for (const int32_t x : all) {
+    const int64_t rows = static_cast<int64_t>(ch->len[x]) * a.G;
+    order[!many || rows <= kFewRows                                        ? 0
+          : rows <= kOwnRows || dense_tiles(ch, x, a) > most_tiles ? 1
+                                                                           : 2].push_back(x);
   }
   // the longest contexts first: a unit of the tensor-core kernel takes an SM for as long as its
   // context is long, and the last ones to start should be short
-  std::stable_sort(order[1].begin(), order[1].end(), [&](int32_t x, int32_t y) {
-    return ch->start[x] + ch->len[x] > ch->start[y] + ch->len[y];
-  });
+  for (int i = 1; i < 3; ++i)
+    std::stable_sort(order[i].begin(), order[i].end(), [&](int32_t x, int32_t y) {
+      return ch->start[x] + ch->len[x] > ch->start[y] + ch->len[y];
+    });
   a.tx_pad = c->attn_tx_pad;
   size_t need = 0;
   for (int pass = 0; pass < 2; ++pass) {
     if (pass == 1 && (s = chunk_scratch(c, need, st)) != TD_OK) return s;
-    for (int tc = 0; tc < 2; ++tc) {
-      for (size_t at = 0; at < order[tc].size();) {
+    for (int group = 0; group < 3; ++group) {
+      for (size_t at = 0; at < order[group].size();) {
         ChunkList list;
         ChunkUnits units;
-        fill_list(ch, order[tc], tok, &at, &list);
+        DenseTiles dense;
+        fill_list(ch, order[group], tok, &at, &list);
+        a.dense_rows = 0;
+        if (group == 2) {
+          fill_dense(ch, order[group], a, &at, &list, &dense);
+          a.dense_rows = dense.base[list.n] * 128;
+        }
         int rows = 0;
-        const int64_t n = tc ? plan_tc(c, list, &a, &units, &rows)
-                             : plan_rows(c, list, &a, &units, &rows);
+        const int64_t n = group ? plan_tc(c, list, &a, &units, &rows)
+                                : plan_rows(c, list, &a, &units, &rows);
         if (n < 0) return TD_ERR_INVALID_ARG;
+        // the unfolded rows, their scales, then the partial results
+        const size_t planes = static_cast<size_t>(a.nl) * 2 * a.dense_rows;
+        const size_t scales = planes * a.g.E / 2, parts = scales + planes * H;
         const size_t floats = a.direct ? 0 : static_cast<size_t>(n) * rows * (D + 2);
-        need = std::max(need, floats);
+        need = std::max(need, parts + floats);
         if (pass == 0) continue;
-        a.part_o = c->d_chunk;
-        a.part_ml = a.direct ? nullptr : c->d_chunk + static_cast<size_t>(n) * rows * D;
-        const uint32_t bit = 1u << (kind * 3 + (tc ? 2 : rows == 8));
+        a.part_o = c->d_chunk + parts;
+        a.part_ml = a.direct ? nullptr : a.part_o + static_cast<size_t>(n) * rows * D;
+        a.dense = nullptr;
+        if (group == 2) {
+          a.dense = reinterpret_cast<uint16_t*>(c->d_chunk);
+          a.dense_scale = c->d_chunk + scales;
+          if (!row_map(a.g.E, a.dense, static_cast<int64_t>(planes), 128, &map) ||
+              launch_expand(a, list, dense, kind, st) != cudaSuccess)
+            return TD_ERR_CUDA;
+        }
+        const uint32_t bit = 1u << (group == 2 ? 9 : kind * 3 + (group ? 2 : rows == 8));
         const bool fresh = !(c->chunk_launched & bit);
-        if ((tc ? launch_chunk_tc(a, list, units, map, kind, fresh, st)
-                : launch_chunk_rows(a, list, units, kind, rows, fresh, st)) != cudaSuccess ||
+        if ((group ? launch_chunk_tc(a, list, units, dense, map, kind, fresh, st)
+                   : launch_chunk_rows(a, list, units, kind, rows, fresh, st)) != cudaSuccess ||
             (!a.direct && launch_chunk_join(a, list, units, rows, st) != cudaSuccess))
           return TD_ERR_CUDA;
         c->chunk_launched |= bit;

@@ -210,6 +210,31 @@ struct ChunkUnits {
   int32_t nsplit[kMaxChunkSeqs];
 };
 
+// The KV tiles (of 128 positions) that the tokens of a chunk see: the first s ones, where the
+// kept first tokens lie before the window, then n - s from tile t0 on.
+struct DenseSpan {
+  int s, t0, n;
+  __host__ __device__ int tile(int i) const { return i < s ? i : t0 + i - s; }
+  __host__ __device__ int index(int kt) const { return kt < s ? kt : s + kt - t0; }
+};
+__host__ __device__ inline DenseSpan dense_span(int start, int len, int window, int n_sink) {
+  const int lo = window > 0 && start >= window ? start - window + 1 : 0;
+  const int kept = window > 0 ? (n_sink < lo ? n_sink : lo) : 0;
+  DenseSpan d;
+  d.s = (kept + 127) / 128;
+  d.t0 = lo / 128 > d.s ? lo / 128 : d.s;
+  const int last = (start + len - 1) / 128;
+  d.n = d.s + (last >= d.t0 ? last - d.t0 + 1 : 0);
+  return d;
+}
+
+// Where the sequences' tiles lie in the unfolded copy: sequence x's are base[x] .. base[x + 1] - 1.
+struct DenseTiles {
+  int32_t base[kMaxChunkSeqs + 1];
+};
+// The scale of a position whose page is unmapped (a NaN that no other scale is stored as).
+constexpr uint32_t kHole = 0x7FC0A5A5u;
+
 // What the cache's pages hold: bf16 rows, or 8-bit codes with a float scale per head row.
 enum CacheKind { kCacheBf16 = 0, kCacheInt8 = 1, kCacheE4m3 = 2 };
 
@@ -245,6 +270,9 @@ struct ChunkArgs {
   Geom g;
   PoolDev pool;              // the pages (bf16 rows, or 8-bit codes)
   const float* scale;        // 8-bit pages: their scales
+  uint16_t* dense;           // 8-bit pages unfolded: [nl][2][dense_rows][E] bf16, or nullptr
+  float* dense_scale;        // ... and [nl][2][H][dense_rows] floats
+  int dense_rows;
   const uint16_t* q;         // [nl][tokens][nq][D] bf16
   uint16_t* out;             // [nl][tokens][nq][D] bf16
   float* lse;                // [nl][tokens][nq] or nullptr
@@ -270,9 +298,14 @@ struct ChunkArgs {
 cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               CacheKind kind, int rows_per_tile, bool fresh, cudaStream_t st);
 // The tensor-core kernel for many rows. map: the bf16 pool's rows of the call's layers, boxes
-// of box_rows x 64 (8-bit pages: not read).
+// of box_rows x 64, or the unfolded copy's, boxes of 128 x 64, where there is one (8-bit pages
+// without one: not read).
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap& map, CacheKind kind, bool fresh, cudaStream_t st);
+                            const DenseTiles& dense, const CUtensorMap& map, CacheKind kind,
+                            bool fresh, cudaStream_t st);
+// Unfolds the tiles that the launch's sequences see into a.dense and a.dense_scale.
+cudaError_t launch_expand(const ChunkArgs& a, const ChunkList& list, const DenseTiles& dense,
+                          CacheKind kind, cudaStream_t st);
 // Joins the units of every query row.
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st);

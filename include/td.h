@@ -439,7 +439,10 @@ td_status td_chunk_attention(td_ctx* ctx, const td_chunks* chunks, const td_page
                              int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
                              void* out, float* lse, void* stream);
 
-/* The same over 8-bit pages: K and V are code * scale. */
+/* The same over 8-bit pages: K and V are code * scale, with any scale. (The e4m3 codes that
+ * stand for a NaN, which td_quantise_append does not write, have no defined value in sight.)
+ * For long chunks the visible pages are first unfolded into the context's scratch, at most
+ * 2^30 bytes of it. */
 td_status td_chunk_attention_q8(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
                                 int32_t layer_begin, int32_t layer_end, const void* q,
                                 int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
@@ -497,12 +500,13 @@ td_status td_group_round(const td_prompt* prompts, int32_t n_prompts, int32_t se
                          int32_t* perm);
 
 /* Fault injection for tests; no counterpart in the paper. With bytes > 0 every later
- * td_fused_attention / td_paged_attention call on this context, and every
- * td_chunk_attention call of chunks that its tensor-core kernel takes, makes each stage's
- * barrier expect `bytes` more than its copies deliver, so every bounded wait runs out (0.2 s
- * of device time each): the units record TD_ERR_DEVICE_TIMEOUT in the error word, wait
- * (bounded) for their own copies and return, and the outputs are not valid. No copy is
- * lost and nothing faults: the context stays usable. bytes = 0 restores normal calls. */
+ * td_fused_attention / td_paged_attention call on this context, and every chunk attention
+ * call whose tensor-core kernel copies bf16 tiles (td_chunk_attention of chunks of more than
+ * a few query rows, td_chunk_attention_q8 of long ones), makes each stage's barrier expect
+ * `bytes` more than its copies deliver, so every bounded wait runs out (0.2 s of device time
+ * each): the units record TD_ERR_DEVICE_TIMEOUT in the error word, wait (bounded) for their
+ * own copies and return, and the outputs are not valid. No copy is lost and nothing faults:
+ * the context stays usable. bytes = 0 restores normal calls. */
 td_status td_inject_attention_wait_fault(td_ctx* ctx, uint32_t bytes);
 
 /* Synchronize the stream, read and clear the error word. Returns TD_OK when no device

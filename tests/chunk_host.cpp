@@ -16,8 +16,17 @@ struct Launch {
   QuantArgs qa;
   ChunkList list;
   ChunkUnits units;
+  DenseTiles dense;
 };
 std::vector<Launch> g_launches;
+struct Unfold {
+  int before;         // the launch that follows
+  int n;
+  const uint16_t* to;
+  int rows;
+  DenseTiles dense;
+};
+std::vector<Unfold> g_unfolds;
 int g_device = 0, g_capturing = 0, g_fail_malloc = 0;
 size_t g_floats = 0;
 
@@ -53,12 +62,19 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
   return cudaSuccess;
 }
 cudaError_t launch_chunk_tc(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
-                            const CUtensorMap&, CacheKind kind, bool, cudaStream_t) {
+                            const DenseTiles& dense, const CUtensorMap&, CacheKind kind, bool,
+                            cudaStream_t) {
   Launch& l = push(4, list);
   l.a = a;
   l.units = units;
+  l.dense = dense;
   l.kind = kind;
   l.rows = a.rows_cta;
+  return cudaSuccess;
+}
+cudaError_t launch_expand(const ChunkArgs& a, const ChunkList& list, const DenseTiles& dense,
+                          CacheKind, cudaStream_t) {
+  g_unfolds.push_back({static_cast<int>(g_launches.size()), list.n, a.dense, a.dense_rows, dense});
   return cudaSuccess;
 }
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
@@ -98,7 +114,7 @@ cudaError_t cudaGetDevice(int* d) {
 cudaError_t cudaMalloc(void** p, size_t bytes) {
   if (g_fail_malloc) return cudaErrorMemoryAllocation;
   g_floats = bytes / sizeof(float);
-  static char place[64];
+  alignas(256) static char place[64];
   *p = place;
   return cudaSuccess;
 }
@@ -125,7 +141,10 @@ void fake_state(int device, int capturing, int fail_malloc) {
   g_capturing = capturing;
   g_fail_malloc = fail_malloc;
 }
-void fake_reset(void) { g_launches.clear(); }
+void fake_reset(void) {
+  g_launches.clear();
+  g_unfolds.clear();
+}
 int64_t fake_floats(void) { return static_cast<int64_t>(g_floats); }
 int fake_launches(void) { return static_cast<int>(g_launches.size()); }
 // what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul, box_rows
@@ -136,6 +155,31 @@ void fake_launch(int i, int64_t* out) {
                        quant ? l.qa.tok0 : 0, quant ? l.qa.tokens : l.a.tokens,
                        l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul, l.a.box_rows};
   for (int k = 0; k < 12; ++k) out[k] = v[k];
+}
+int fake_unfolds(void) { return static_cast<int>(g_unfolds.size()); }
+// The tiles' places of unfolding i; out: the attention launch that follows, its sequences, the
+// copy's rows, whether that launch reads this copy with the same places, and where the scales
+// and the partial results begin, in floats from the copy's begin.
+void fake_unfold(int i, int32_t* base, int64_t* out) {
+  const Unfold& u = g_unfolds[i];
+  const Launch& l = g_launches[u.before];
+  bool same = l.what == 4 && l.list.n == u.n && l.a.dense == u.to && l.a.dense_rows == u.rows;
+  for (int x = 0; x <= u.n; ++x) {
+    base[x] = u.dense.base[x];
+    same = same && l.dense.base[x] == u.dense.base[x];
+  }
+  out[0] = u.before;
+  out[1] = u.n;
+  out[2] = u.rows;
+  out[3] = same;
+  out[4] = l.a.dense_scale - reinterpret_cast<const float*>(u.to);
+  out[5] = l.a.part_o - reinterpret_cast<const float*>(u.to);
+}
+void fake_span(int start, int len, int window, int n_sink, int32_t* out) {
+  const DenseSpan d = dense_span(start, len, window, n_sink);
+  out[0] = d.s;
+  out[1] = d.t0;
+  out[2] = d.n;
 }
 void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* base, int32_t* ns,
                int32_t* tok) {

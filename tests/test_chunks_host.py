@@ -275,3 +275,59 @@ def test_plans_cover_every_visible_position(td, lib):
         assert call.run(op, chunks=chunks, nq=H * G, window=window, sinks=sinks,
                         layers=(1, 1 + nl)) == td.TD_OK
         _check_attention(lib, call, H, D, P, H * G, chunks, window, sinks, nl, op == "attend8")
+
+
+def test_long_chunks_over_8bit_pages_are_unfolded_once(td, lib):
+    """Every KV tile that a query tile takes has a place of its own in the copy that its launch
+    reads; the copy stays within its limit, and the scratch holds all of it."""
+    rng = random.Random(11)
+    unfolded = 0
+    for i in range(300):
+        H, D, G = rng.choice((1, 2, 8)), rng.choice((64, 128)), rng.choice((1, 5, 8))
+        nl = rng.choice((1, 2, 28))
+        n = rng.choice((1, 3, 300))
+        chunks = [(j % 8, rng.randint(0, rng.choice((1, 300, 30000))), rng.randint(0, 900))
+                  for j in range(n)]
+        window, sinks = rng.choice((0, 0, 1, 130, 1000)), rng.choice((0, 4, 300, 2000))
+        call = Call(td, lib, H=H, D=D, L=29)
+        assert call.run("attend8", chunks=chunks, nq=H * G, window=window, sinks=sinks,
+                        layers=(1, 1 + nl)) == td.TD_OK
+        launches = call.launches()
+        seen = set()
+        for u in range(lib.fake_unfolds()):
+            base, out = np.zeros(257, np.int32), np.zeros(6, np.int64)
+            lib.fake_unfold(u, base.ctypes.data_as(C.c_void_p), out.ctypes.data_as(C.c_void_p))
+            at, m, rows, same, scales, parts = (int(v) for v in out)
+            l = launches[at]
+            assert same and rows == 128 * base[m] and at not in seen
+            seen.add(at)
+            floats = nl * 2 * rows * H * D // 2
+            assert scales == floats and parts == floats + nl * 2 * rows * H
+            assert 4 * parts <= 2**30 and parts % 4 == 0 and scales % 4 == 0
+            units = int(l["base"][m]) * H * nl
+            assert parts + (0 if l["direct"] else units * 256 * (D + 2)) <= lib.fake_floats()
+            for x in range(m):
+                s, t = int(l["start"][x]), int(l["row"][x + 1] - l["row"][x])
+                assert t * G > 512
+                span = np.zeros(3, np.int32)
+                lib.fake_span(s, t, window, sinks, span.ctypes.data_as(C.c_void_p))
+                first, t0, tiles = (int(v) for v in span)
+                assert base[x + 1] - base[x] == tiles
+                have = list(range(first)) + list(range(t0, t0 + tiles - first))
+                assert len(set(have)) == len(have) and have[-1] <= (s + t - 1) // 128
+                for tile in range(-(-t * G // 256)):
+                    p0, p1 = s + tile * 256 // G, s + min(tile * 256 + 255, t * G - 1) // G
+                    lo = max(0, p0 - window + 1) if window else 0
+                    kept = min(sinks, lo) if window else 0
+                    need = set(range(lo // 128, p1 // 128 + 1)) | set(range(-(-kept // 128)))
+                    assert need <= set(have)
+                    for kt in need:                      # the kernel's place of a tile
+                        assert have[kt if kt < first else first + kt - t0] == kt
+                unfolded += 1
+        for k, l in enumerate(launches):
+            if l["what"] == 4 and k not in seen:         # converted in the kernel: short, or long
+                for x in range(int(l["n"])):
+                    s, t = int(l["start"][x]), int(l["row"][x + 1] - l["row"][x])
+                    tiles = -(-(s + t) // 128)
+                    assert t * G <= 512 or nl * 2 * 128 * tiles * H * (2 * D + 4) > 2**30
+    assert unfolded > 1000

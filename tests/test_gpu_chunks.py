@@ -656,3 +656,111 @@ def test_batches_without_tokens_write_nothing(td):
                               None, _stream())
     assert _errors(td, ctx) == (0, 0)
     assert bool((codes == 3).all()) and bool((sc == 0.5).all()) and bool((pool == 2.0).all())
+
+
+# ------------------------------------------------- long chunks over 8-bit pages, unfolded first
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("D,window,sinks", [(64, 0, 0), (128, 0, 0), (128, 210, 150), (64, 33, 3)])
+def test_long_chunks_over_scales_of_any_kind(td, fmt, D, window, sinks):
+    """Powers of two (which the unfolded values take in) up to some position, then scales of
+    both signs, zeros and large ones; an unmapped page within sight of all tokens."""
+    b = ck.Batch([400, 37, 900, 3], [150, 300, 2, 40], 2, D, 16, seed=41)
+    val, s = ck.quantise(b.rows(*b.pool_shape()), fmt)
+    codes, scale = ck.code_bytes(val, fmt).contiguous(), s.float().contiguous()
+    if fmt == "e4m3":
+        scale[:, 1] *= 2.0 ** -90                      # (still a power of two)
+    pick = torch.randint(0, 6, scale.shape, generator=b.gen, device="cuda")
+    odd = torch.zeros_like(scale, dtype=torch.bool)
+    for x, first in ((0, 256), (1, 130)):
+        pg, sl = b.place(x, np.arange(first, b.starts[x] + b.lens[x]))
+        odd[:, :, pg, sl] = True
+    other = torch.where(pick == 0, -0.7 * scale, torch.where(pick == 1, scale * 0, scale * 1.3))
+    scale = torch.where(odd & (pick < 3), other, scale).contiguous()
+    scale[:, 1] = torch.where(odd[:, 1] & (pick[:, 1] == 5), 2.0 ** 9, scale[:, 1])
+    hole = int(b.bt[0, 24]), int(b.bt[1, 3])           # positions 384 and 48 on
+    b.bt_t[0, 24] = b.bt_t[1, 3] = -1
+    codes[:, :, list(hole)] = 0x7F
+    scale[:, :, list(hole)] = math.nan
+    q = b.rows(1, b.T, 8, D)
+    hit = (td.TD_ERR_UNMAPPED_PAGE, 1 << td.TD_ERR_UNMAPPED_PAGE)
+    got = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, fmt), q, window, sinks, q8=True,
+                         expect=hit)
+    kv = torch.nan_to_num(ck.code_values(codes, fmt) * scale.double()[..., None])
+    want = ck.attend(b, kv[:, 0], kv[:, 1], q, window, sinks)
+    _close(got, want, 2.0 ** -8)
+    again = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, fmt), q, window, sinks,
+                           q8=True, expect=hit)
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_a_scale_that_is_not_finite_stays_with_the_rows_that_see_it(td):
+    """K's or V's scale of a token in the middle of a long chunk is a NaN."""
+    b = ck.Batch([150], [300], 2, 128, 16, seed=42)
+    val, s = ck.quantise(b.rows(*b.pool_shape()), "e4m3")
+    codes, scale = ck.code_bytes(val, "e4m3").contiguous(), s.float().contiguous()
+    q = b.rows(1, b.T, 4, 128)
+    clean, zc = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, "e4m3"), q, q8=True)
+    pg, sl = b.place(0, np.array([290]))
+    for half in (0, 1):
+        dirty_scale = scale.clone()
+        dirty_scale[0, half, pg, sl, 1] = math.nan
+        out, z = _run_attention(td, b, td.make_paged8(codes, dirty_scale, b.bt_t, "e4m3"), q, q8=True)
+        # (a tile with such a scale applies its scales to the scores and weights instead: other
+        # roundings, so the bounds rather than the same bits)
+        kv = val * s[..., None]
+        want = ck.attend(b, kv[:, 0], kv[:, 1], q)
+        blind = torch.arange(300, device="cuda") < 140
+        _close((out[:, blind], z[:, blind]), [t[:, blind] for t in want], 2.0 ** -8)
+        _close((out[:, :, :2], z[:, :, :2]), [t[:, :, :2] for t in want], 2.0 ** -8)
+        assert bool(torch.isnan(out[0, ~blind, 2:]).all())
+
+
+def test_unfolded_copies_past_their_limit_take_several_launches(td):
+    """Three sequences over 28 layers, whose copies together pass 2^30 bytes."""
+    b = ck.Batch([4700, 3300, 4000], [300, 280, 290], 8, 128, 16, 28, seed=43)
+    codes = torch.randint(-127, 128, b.pool_shape(), generator=b.gen, device="cuda",
+                          dtype=torch.int8)
+    scale = torch.rand(b.pool_shape()[:-1], generator=b.gen, device="cuda") * 0.01 + 0.001
+    q = b.rows(28, b.T, 16, 128)
+    got = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, "int8"), q, q8=True)
+    kv = codes.double() * scale.double()[..., None]
+    _close(got, ck.attend(b, kv[:, 0], kv[:, 1], q), 2.0 ** -8)
+
+
+def test_long_chunks_over_8bit_pages_in_a_captured_graph(td):
+    """Unfolding, attention and join replayed over new pages and queries."""
+    b = ck.Batch([2000, 90], [200, 150], 2, 128, 16, seed=44)
+    q = b.rows(1, b.T, 6, 128)
+    ctx = _ctx(td, b)
+    val, s = ck.quantise(b.rows(*b.pool_shape()), "int8")
+    codes, scale = ck.code_bytes(val, "int8").contiguous(), s.float().contiguous()
+    pages = td.make_paged8(codes, scale, b.bt_t, "int8")
+    _run_attention(td, b, pages, q, q8=True, ctx=ctx)
+    out = torch.full(q.shape, math.nan, dtype=torch.bfloat16, device="cuda")
+    z = torch.full(q.shape[:3], math.nan, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        td.td_chunk_attention_q8(ctx.handle, _chunks(td, b), pages, 0, 1, q.data_ptr(), 6, 0.09, 0,
+                                 0, out.data_ptr(), z.data_ptr(), _stream())
+    for _ in range(2):
+        val, s = ck.quantise(b.rows(*b.pool_shape()), "int8")
+        codes.copy_(ck.code_bytes(val, "int8"))
+        scale.copy_(s.float())
+        q.copy_(b.rows(1, b.T, 6, 128))
+        graph.replay()
+        kv = val * s[..., None]
+        _close((out, z), ck.attend(b, kv[:, 0], kv[:, 1], q, scale=0.09), 2.0 ** -8)
+
+
+def test_a_wait_that_runs_out_over_unfolded_pages(td):
+    b = ck.Batch([300], [140], 1, 128, 16, seed=45)
+    val, s = ck.quantise(b.rows(*b.pool_shape()), "e4m3")
+    codes, scale = ck.code_bytes(val, "e4m3").contiguous(), s.float().contiguous()
+    pages, q, ctx = td.make_paged8(codes, scale, b.bt_t, "e4m3"), b.rows(1, b.T, 4, 128), _ctx(td, b)
+    td.td_inject_attention_wait_fault(ctx.handle, 64)
+    _run_attention(td, b, pages, q, q8=True, ctx=ctx,
+                   expect=(td.TD_ERR_DEVICE_TIMEOUT, 1 << td.TD_ERR_DEVICE_TIMEOUT))
+    td.td_inject_attention_wait_fault(ctx.handle, 0)
+    got = _run_attention(td, b, pages, q, q8=True, ctx=ctx)
+    kv = val * s[..., None]
+    _close(got, ck.attend(b, kv[:, 0], kv[:, 1], q), 2.0 ** -8)
