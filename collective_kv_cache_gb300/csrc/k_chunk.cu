@@ -688,12 +688,12 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   __shared__ float s_acc[kJoinWarps][D];
   __shared__ float s_l[kJoinWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int n_tok = list.row[list.n];
+  const int n_tok = list.row[list.n] - A.join_from;
   const unsigned n = kSplit ? blockIdx.x : blockIdx.x * kJoinWarps + warp;
   const int gq = static_cast<int>(n % A.nq);
   const int lt = static_cast<int>(n / A.nq);
   if (!kSplit && lt >= A.nl * n_tok) return;
-  const int t = lt % n_tok, li = lt / n_tok;
+  const int t = A.join_from + lt % n_tok, li = lt / n_tok;
   int x = 0;
   for (int hi = list.n - 1; x < hi;) {
     const int mid = (x + hi + 1) >> 1;
@@ -703,9 +703,13 @@ chunk_join_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
   const int h = gq / A.G;
   const int r = (t - list.row[x]) * A.G + gq - h * A.G;
   const int tile = r / R, rt = r - tile * R;
-  const int ns = units.nsplit[x];
-  const int64_t u0 = (static_cast<int64_t>(li) * A.g.H + h) * units.base[list.n] + units.base[x] +
-                     static_cast<int64_t>(tile) * ns;
+  const int ns = units.nsplit[x], whole = units.whole[x];
+  // (the tensor-core kernel, whose tiles are larger, numbers them from the last one down)
+  const int at = R < 128 ? tile : ((list.row[x + 1] - list.row[x]) * A.G - 1) / R - tile;
+  if (at < whole) return;         // written already
+  const int64_t u0 =
+      (static_cast<int64_t>(li) * A.g.H + h) * (units.base[list.n] - A.whole_units) +
+      (units.base[x] + whole - A.whole_units) + static_cast<int64_t>(at - whole) * ns;
   // every warp finds the row's maximum itself
   float mx = -INFINITY;
   bool nan = false;
@@ -806,7 +810,7 @@ cudaError_t launch_chunk_rows(const ChunkArgs& a, const ChunkList& list, const C
 
 cudaError_t launch_chunk_join(const ChunkArgs& a, const ChunkList& list, const ChunkUnits& units,
                               int rows_per_tile, cudaStream_t st) {
-  const unsigned rows = static_cast<unsigned>(a.nl) * list.row[list.n] * a.nq;
+  const unsigned rows = static_cast<unsigned>(a.nl) * (list.row[list.n] - a.join_from) * a.nq;
   // a warp a row from 8192 rows on (the machine holds 152 x 64 warps)
   const bool split = rows < 8192;
   const unsigned grid = split ? rows : (rows + kJoinWarps - 1) / kJoinWarps;

@@ -310,6 +310,7 @@ struct Work {
   int p_first, p_last;          // positions of the first and the last row's tokens
   int s_tiles, t_lo;            // KV tiles: 0 .. s_tiles - 1, then t_lo ..
   int i0, n;                    // the part: KV tiles i0 .. i0 + n - 1 of that list
+  bool direct;                  // all of them: the outputs are written here
   int window, n_sink;
 
   // the part's j-th tile: under a window from the middle on, then the first ones, since those
@@ -354,11 +355,13 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& lis
   w.len = list.row[x + 1] - list.row[x];
   const int rows = w.len * A.G;
   // a sequence's last tiles see most: they start first
-  const int turned = (c - units.base[x]) / ns;
-  const int split = c - units.base[x] - turned * ns;
+  const int at = c - units.base[x], whole = units.whole[x];
+  const int turned = at < whole ? at : whole + (at - whole) / ns;
+  const int split = at < whole ? 0 : (at - whole) % ns;
+  w.direct = A.direct || at < whole;
   const int tile = (rows + A.rows_cta - 1) / A.rows_cta - 1 - turned;
-  w.unit = (static_cast<int64_t>(w.li) * A.g.H + w.h) * total + units.base[x] +
-           static_cast<int64_t>(tile) * ns + split;
+  w.unit = (static_cast<int64_t>(w.li) * A.g.H + w.h) * (total - A.whole_units) +
+           (c - A.whole_units);
   w.r0 = tile * A.rows_cta;
   w.nrows = min(A.rows_cta, rows - w.r0);
   w.p_first = w.start + w.r0 / A.G;
@@ -371,7 +374,7 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& lis
   w.t_lo = max(lo / kKv, w.s_tiles);
   const int all = w.s_tiles + max(0, w.p_last / kKv - w.t_lo + 1);
   w.i0 = split * A.span;
-  w.n = min(A.span, all - w.i0);
+  w.n = w.direct ? all : min(A.span, all - w.i0);
   return w;
 }
 
@@ -735,7 +738,7 @@ __device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list
         }
       }
     }
-    if (A.direct) {
+    if (w.direct) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       for (int i = 0; i < N; i += 2)
         *reinterpret_cast<uint32_t*>(A.out + orow * D + lane * N + i) =
@@ -944,7 +947,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       if (ok && *reinterpret_cast<volatile int*>(&sh->bad) == 0) {
         tc_fence_after();
         const float l = sum.x + sum.y;
-        if (A.direct) {
+        if (w.direct) {
           const int64_t row = live ? out_row(A, list, w, w.r0 + rr) : -1;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;      // a row that sees nothing: zeros
           // through the query tile's place (its products have ended), so that a warp writes

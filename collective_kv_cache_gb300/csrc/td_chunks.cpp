@@ -300,6 +300,7 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
   }
   a->span = static_cast<int>(best * step);
   a->direct = 1;
+  a->whole_units = a->join_from = 0;
   units->base[0] = 0;
   int64_t sum = 0;
   for (int x = 0; x < list.n; ++x) {
@@ -308,9 +309,70 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
     sum += tiles(x) * ns;
     if (sum > INT32_MAX) return -1;
     units->nsplit[x] = static_cast<int32_t>(ns);
+    units->whole[x] = 0;
     units->base[x + 1] = static_cast<int32_t>(sum);
   }
   return sum * cost.heads > INT32_MAX ? -1 : sum * cost.heads;
+}
+
+// Where every tile is one unit and they are one to six waves of the machine: the tiles of the
+// last, partly filled wave are cut into parts that fill it, where that is estimated to gain
+// more than their join costs. The order is the launch's: sequences from first to last. 156
+// units of one sequence: 142 us whole, 103 with the last 4 in eight parts; 376 (chunks of 500 to
+// 700 tokens over e4m3 pages, the last 72 in halves) 276 and 261, but 278 in thirds, which are
+// more than one wave again. 984 units of unequal length (6.5 waves) fill the machine by
+// themselves: 724 us whole, 733 cut.
+template <typename Tiles, typename Seen>
+int64_t cut_tail(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int64_t n,
+                 double unit_bytes, ChunkArgs* a, ChunkUnits* units) {
+  const int64_t r = n % cost.slots;
+  if (!a->direct || n <= cost.slots || n > 6 * cost.slots || r == 0) return n;
+  const int64_t m = (r + cost.heads - 1) / cost.heads;      // the tail's tiles
+  double total = 0.0, tail = 0.0;
+  int64_t left = m, longest = 0;                            // steps of the tail's first unit
+  for (int x = list.n - 1; x >= 0; --x) {
+    const double us = (seen(x) * cost.step_us + cost.fixed_us) * cost.heads;
+    total += tiles(x) * us;
+    const int64_t take = std::min(left, tiles(x));
+    if (take > 0) longest = seen(x);
+    tail += take * us;
+    left -= take;
+  }
+  const double full = (total - tail) / cost.slots;
+  double best_us = 0.97 * (full + longest * cost.step_us + cost.fixed_us);
+  int64_t best = 0;
+  for (int64_t k = 2; k <= 8 && longest / k >= cost.least; ++k) {
+    const double part = (longest + k - 1) / k * cost.step_us + cost.fixed_us;
+    const int64_t waves = (m * cost.heads * k + cost.slots - 1) / cost.slots;
+    const double us =
+        full + waves * part + 4.0 + 2.0 * m * cost.heads * k * unit_bytes / 10e6;
+    if (us < best_us) {
+      best_us = us;
+      best = k;
+    }
+  }
+  if (best == 0) return n;
+  const int64_t span = (longest + best - 1) / best;
+  a->span = static_cast<int>(span);
+  a->direct = 0;
+  left = m;
+  for (int x = list.n - 1; x >= 0; --x) {
+    const int64_t take = std::min(left, tiles(x));
+    left -= take;
+    units->whole[x] = static_cast<int32_t>(tiles(x) - take);
+    units->nsplit[x] = take ? static_cast<int32_t>((seen(x) + span - 1) / span) : 1;
+    if (take) a->join_from = list.row[x];
+  }
+  int64_t sum = 0;
+  bool whole = true;
+  for (int x = 0; x < list.n; ++x) {
+    units->base[x] = static_cast<int32_t>(sum);
+    if (whole) a->whole_units = static_cast<int>(sum + units->whole[x]);
+    whole = whole && units->whole[x] == tiles(x);
+    sum += units->whole[x] + (tiles(x) - units->whole[x]) * units->nsplit[x];
+  }
+  units->base[list.n] = static_cast<int32_t>(sum);
+  return sum * cost.heads;
 }
 
 // Positions that a tile of `rows` query rows of sequence x sees, at most.
@@ -354,16 +416,17 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
   const double step = codes ? 2.4 : (a->g.D == 128 ? 1.4 : 0.8);
   const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, step, 4.0,
                   2.0 * 128 * a->g.D * (codes ? 1 : 2) / 8, 2, partial_bytes(list, *a)};
-  return cut(
-      list, cost,
-      [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
-      // a window's positions may straddle one tile more, the first ones' another
-      [&](int x) {
-        const int64_t all =
-            (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
-        return a->window ? std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2) : all;
-      },
-      1, a, units);
+  const auto tiles = [&](int x) {
+    return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R;
+  };
+  // a window's positions may straddle one tile more, the first ones' another
+  const auto seen = [&](int x) {
+    const int64_t all =
+        (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
+    return a->window ? std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2) : all;
+  };
+  const int64_t n = cut(list, cost, tiles, seen, 1, a, units);
+  return n < 0 ? n : cut_tail(list, cost, tiles, seen, n, 4.0 * R * (a->g.D + 2), a, units);
 }
 
 td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& pool,
@@ -447,11 +510,13 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
         // the unfolded rows, their scales, then the partial results
         const size_t planes = static_cast<size_t>(a.nl) * 2 * a.dense_rows;
         const size_t scales = planes * a.g.E / 2, parts = scales + planes * H;
-        const size_t floats = a.direct ? 0 : static_cast<size_t>(n) * rows * (D + 2);
+        const size_t part_rows =
+            static_cast<size_t>(n - static_cast<int64_t>(a.whole_units) * H * a.nl) * rows;
+        const size_t floats = a.direct ? 0 : part_rows * (D + 2);
         need = std::max(need, parts + floats);
         if (pass == 0) continue;
         a.part_o = c->d_chunk + parts;
-        a.part_ml = a.direct ? nullptr : a.part_o + static_cast<size_t>(n) * rows * D;
+        a.part_ml = a.direct ? nullptr : a.part_o + part_rows * D;
         a.dense = nullptr;
         if (group == 2) {
           a.dense = reinterpret_cast<uint16_t*>(c->d_chunk);

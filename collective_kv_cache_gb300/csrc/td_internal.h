@@ -205,9 +205,12 @@ struct ChunkList {
 
 // How the attention's work is cut: sequence x has units base[x] .. base[x + 1] - 1 for each
 // (layer, kv head), nsplit[x] of them (parts of its visible positions) per tile of query rows.
+// The tensor-core kernel takes a sequence's tiles from the last one down; the first whole[x] of
+// them are one unit each, which writes its outputs itself.
 struct ChunkUnits {
   int32_t base[kMaxChunkSeqs + 1];
   int32_t nsplit[kMaxChunkSeqs];
+  int32_t whole[kMaxChunkSeqs];
 };
 
 // The KV tiles (of 128 positions) that the tokens of a chunk see: the first s ones, where the
@@ -288,6 +291,8 @@ struct ChunkArgs {
   int box_rows;              // ... and rows per box of its tensor map
   uint32_t tx_pad;           // ... extra bytes every tile expects (fault injection; 0 normally)
   int direct;                // 1: one unit per tile everywhere, outputs written at once
+  int whole_units;           // 0: units that precede the first tile in parts, per (layer, kv
+  int join_from;             // head), and the first token of the launch that has such tiles
   float scale_log2;          // softmax scale * log2(e)
   uint32_t* err;
 };

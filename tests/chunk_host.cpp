@@ -147,14 +147,16 @@ void fake_reset(void) {
 }
 int64_t fake_floats(void) { return static_cast<int64_t>(g_floats); }
 int fake_launches(void) { return static_cast<int>(g_launches.size()); }
-// what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul, box_rows
+// what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul, box_rows,
+// whole_units, join_from
 void fake_launch(int i, int64_t* out) {
   const Launch& l = g_launches[i];
   const bool quant = l.what < 2;
   const int64_t v[] = {l.what, l.kind, l.rows, l.list.n, l.a.direct, l.a.span,
                        quant ? l.qa.tok0 : 0, quant ? l.qa.tokens : l.a.tokens,
-                       l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul, l.a.box_rows};
-  for (int k = 0; k < 12; ++k) out[k] = v[k];
+                       l.qa.per_cta, l.qa.lane_shift, l.qa.head_mul, l.a.box_rows, l.a.whole_units,
+                       l.a.join_from};
+  for (int k = 0; k < 14; ++k) out[k] = v[k];
 }
 int fake_unfolds(void) { return static_cast<int>(g_unfolds.size()); }
 // The tiles' places of unfolding i; out: the attention launch that follows, its sequences, the
@@ -182,7 +184,7 @@ void fake_span(int start, int len, int window, int n_sink, int32_t* out) {
   out[2] = d.n;
 }
 void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* base, int32_t* ns,
-               int32_t* tok) {
+               int32_t* tok, int32_t* whole) {
   const Launch& l = g_launches[i];
   for (int x = 0; x <= l.list.n; ++x) {
     row[x] = l.list.row[x];
@@ -192,6 +194,7 @@ void fake_list(int i, int32_t* agent, int32_t* start, int32_t* row, int32_t* bas
       start[x] = l.list.start[x];
       ns[x] = l.units.nsplit[x];
       tok[x] = l.list.tok[x];
+      whole[x] = l.units.whole[x];
     }
   }
 }

@@ -85,14 +85,14 @@ class Call:
     def launches(self):
         res = []
         for i in range(self.lib.fake_launches()):
-            v = (C.c_int64 * 12)()
+            v = (C.c_int64 * 14)()
             self.lib.fake_launch(i, v)
             keys = ("what kind rows n direct span tok0 tokens per_cta lane_shift head_mul "
-                    "box").split()
+                    "box whole_units join_from").split()
             d = dict(zip(keys, v))
-            arr = [np.zeros(300, np.int32) for _ in range(6)]
+            arr = [np.zeros(300, np.int32) for _ in range(7)]
             self.lib.fake_list(i, *(a.ctypes.data_as(C.c_void_p) for a in arr))
-            d.update(zip(("agent", "start", "row", "base", "nsplit", "tok"), arr))
+            d.update(zip(("agent", "start", "row", "base", "nsplit", "tok", "whole"), arr))
             res.append(d)
         return res
 
@@ -229,8 +229,7 @@ def _steps(what, s, t, G, R, tile, window, sinks):
 
 def _check_attention(lib, call, H, D, P, nq, chunks, window, sinks, nl, q8):
     G = nq // H
-    at, rows_of = {}, {}
-    tok = 0
+    at, tok, tails = {}, 0, 0
     for i, (a, s, t) in enumerate(chunks):
         if t:
             at[tok] = (a, s, t)
@@ -241,6 +240,7 @@ def _check_attention(lib, call, H, D, P, nq, chunks, window, sinks, nl, q8):
         n, R, tc = int(l["n"]), int(l["rows"]), l["what"] == 4
         assert R in ((128, 256) if tc else (8, 16)) and 0 < n <= 256
         assert tc or l["span"] % 16 == 0
+        split = l["direct"] == 0 and l["whole_units"] == 0
         assert not tc or q8 or (P % 8 == 0 and P % l["box"] == 0 and 8 <= l["box"] <= 128)
         for x in range(n):
             a, s, t = at.pop(int(l["tok"][x]))
@@ -249,19 +249,31 @@ def _check_attention(lib, call, H, D, P, nq, chunks, window, sinks, nl, q8):
             assert tc or t * G <= 16 or (not q8 and P % 8)
             tiles = -(-t * G // R)
             ns = int(l["nsplit"][x])
-            assert l["base"][x + 1] - l["base"][x] == tiles * ns
+            whole = int(l["whole"][x])             # tiles from the last one down, a unit each
+            assert 0 <= whole <= tiles and (tc or whole == 0)
+            assert l["base"][x + 1] - l["base"][x] == whole + (tiles - whole) * ns
             assert ns == 1 or not l["direct"]
-            for tile in range(tiles):
+            split |= whole < tiles
+            if not split:                          # whole ones come first, and are not joined
+                assert l["direct"] or l["join_from"] >= l["row"][x + 1]
+            elif whole:
+                assert l["whole_units"] == l["base"][x] + whole and l["join_from"] == l["row"][x]
+            tails += whole > 0
+            for tile in range(tiles - whole):
                 assert ns * int(l["span"]) >= _steps(l["what"], s, t, G, R, tile, window, sinks)
         units = int(l["base"][n]) * H * nl
+        assert not l["direct"] or l["whole_units"] == l["join_from"] == 0
         if not l["direct"]:
-            assert units * R * (D + 2) <= lib.fake_floats()
+            parts = units - l["whole_units"] * H * nl
+            assert parts > 0 and parts * R * (D + 2) <= lib.fake_floats()
         assert units < 2**31
     assert not at                                   # every sequence in one launch
+    return tails
 
 
 def test_plans_cover_every_visible_position(td, lib):
     rng = random.Random(7)
+    tails = 0
     for i in range(400):
         H, D, G = rng.choice((1, 2, 3, 8)), rng.choice((64, 128)), rng.choice((1, 2, 5, 7, 8, 16, 40))
         P, nl = rng.choice((1, 5, 8, 16, 24, 32, 256)), rng.choice((1, 2))
@@ -274,7 +286,9 @@ def test_plans_cover_every_visible_position(td, lib):
         op = rng.choice(("attend", "attend8"))
         assert call.run(op, chunks=chunks, nq=H * G, window=window, sinks=sinks,
                         layers=(1, 1 + nl)) == td.TD_OK
-        _check_attention(lib, call, H, D, P, H * G, chunks, window, sinks, nl, op == "attend8")
+        tails += _check_attention(lib, call, H, D, P, H * G, chunks, window, sinks, nl,
+                                  op == "attend8")
+    assert tails > 3
 
 
 def test_long_chunks_over_8bit_pages_are_unfolded_once(td, lib):
@@ -304,7 +318,7 @@ def test_long_chunks_over_8bit_pages_are_unfolded_once(td, lib):
             floats = nl * 2 * rows * H * D // 2
             assert scales == floats and parts == floats + nl * 2 * rows * H
             assert 4 * parts <= 2**30 and parts % 4 == 0 and scales % 4 == 0
-            units = int(l["base"][m]) * H * nl
+            units = (int(l["base"][m]) - int(l["whole_units"])) * H * nl
             assert parts + (0 if l["direct"] else units * 256 * (D + 2)) <= lib.fake_floats()
             for x in range(m):
                 s, t = int(l["start"][x]), int(l["row"][x + 1] - l["row"][x])
@@ -331,3 +345,16 @@ def test_long_chunks_over_8bit_pages_are_unfolded_once(td, lib):
                     tiles = -(-(s + t) // 128)
                     assert t * G <= 512 or nl * 2 * 128 * tiles * H * (2 * D + 4) > 2**30
     assert unfolded > 1000
+
+
+def test_the_last_wave_is_cut_where_it_pays(td, lib):
+    """372 units on 152 SMs: the last 68 in parts; 128, 152 and 304 stay as they are."""
+    call = Call(td, lib, H=4, D=128)
+    for chunks, cut in (([(0, 4200, 1500), (1, 3900, 1300), (2, 3700, 160)], 17),
+                        ([(0, 4000, 1216)], 0), ([(0, 4000, 2432)], 0), ([(0, 4000, 1000)], 0)):
+        assert call.run("attend", chunks=chunks, nq=32) == td.TD_OK
+        l = [x for x in call.launches() if x["what"] == 4][0]
+        n = int(l["n"])
+        tiles = sum(-(-8 * t // 256) for _, _, t in chunks)
+        assert cut == (0 if l["direct"] else tiles - int(l["whole"][:n].sum()))
+        _check_attention(lib, call, 4, 128, 16, 32, chunks, 0, 0, 1, False)

@@ -764,3 +764,43 @@ def test_a_wait_that_runs_out_over_unfolded_pages(td):
     got = _run_attention(td, b, pages, q, q8=True, ctx=ctx)
     kv = val * s[..., None]
     _close(got, ck.attend(b, kv[:, 0], kv[:, 1], q), 2.0 ** -8)
+
+
+# ------------------------------------------- more tiles than SMs: the last wave's tiles in parts
+TAIL = ([4200, 3900, 3700], [1500, 1300, 160], 4, 8)     # (47 + 41 + 5) x 4 units
+
+
+@pytest.mark.parametrize("D,fmt,window,sinks", [(128, "", 0, 0), (64, "", 0, 0),
+                                                (128, "e4m3", 0, 0), (64, "int8", 2500, 4)])
+def test_a_last_wave_in_parts(td, D, fmt, window, sinks):
+    starts, lens, H, G = TAIL
+    b = ck.Batch(starts, lens, H, D, 16, seed=51)
+    pool, q = b.rows(*b.pool_shape()), b.rows(1, b.T, H * G, D)
+    if fmt:
+        val, s = ck.quantise(pool, fmt)
+        kv = val * s[..., None]
+        pages = td.make_paged8(ck.code_bytes(val, fmt).contiguous(), s.float().contiguous(), b.bt_t,
+                               fmt)
+    else:
+        kv, pages = pool.double(), td.make_paged(pool, b.bt_t)
+    got = _run_attention(td, b, pages, q, window, sinks, q8=bool(fmt))
+    _close(got, ck.attend(b, kv[:, 0], kv[:, 1], q, window, sinks), 2.0 ** -8)
+    again = _run_attention(td, b, pages, q, window, sinks, q8=bool(fmt))
+    assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+def test_a_last_wave_in_parts_with_a_nan_in_v(td):
+    """In the part of a tile that some of its rows see and others do not."""
+    starts, lens, H, G = TAIL
+    b = ck.Batch(starts, lens, H, 128, 16, seed=52)
+    pool, q = b.rows(*b.pool_shape()), b.rows(1, b.T, H * G, 128)
+    want = ck.attend(b, pool[:, 0].double(), pool[:, 1].double(), q)
+    at = starts[2] + 11
+    pg, sl = b.place(2, np.array([at]))
+    pool[0, 1, pg, sl, 1, 5] = math.nan
+    out, z = _run_attention(td, b, td.make_paged(pool, b.bt_t), q)
+    keep = torch.ones(out.shape, dtype=torch.bool, device="cuda")
+    keep[0, b.T - lens[2] + 11:, G:2 * G, 5] = False
+    assert bool(torch.isnan(out[~keep]).all())
+    o = torch.where(keep, out, want[0].to(torch.bfloat16))
+    _close((o, z), want, 2.0 ** -8)
