@@ -113,6 +113,7 @@ struct Shared {
   uint64_t s_full[2], s_empty[2], p_ready[2][2], o_done[2], drain;   // p_ready: the weights' halves
   uint32_t tmem;
   int abort, bad;
+  int place[4];                      // x, h, li and unit of the CTA's work
   alignas(16) int box_row[2][16];    // K's and V's loader: rows of the tile's boxes
   Info info[kInfo];
 };
@@ -215,6 +216,16 @@ __device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
       : "memory");
 }
 
+// 16 bytes of shared memory, read where it is written.
+__device__ __forceinline__ int4 lds_int4(const int* p) {
+  int4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(smem_u32(p))
+               : "memory");
+  return v;
+}
+
 // One lane of the warp, always the same. The products' warp runs as one and only issues under
 // this: its addresses and descriptors stay warp-uniform, in uniform registers (issued from a
 // branch of lane 0 alone, each product cost about 100 cycles of moves, against 64 of tensor
@@ -304,13 +315,13 @@ __device__ __forceinline__ uint32_t tile_at(int r, int c) {
 // What a CTA works on.
 struct Work {
   int x, h, li;                 // sequence, kv head, layer of the launch
-  int64_t unit;                 // number of its partial results
+  int unit;                     // number of its partial results; -1: none, it has all KV tiles
+                                // of its rows and writes their outputs
   int r0, nrows;                // query rows r0 .. r0 + nrows - 1 of the sequence
   int start, len;
   int p_first, p_last;          // positions of the first and the last row's tokens
   int s_tiles, t_lo;            // KV tiles: 0 .. s_tiles - 1, then t_lo ..
   int i0, n;                    // the part: KV tiles i0 .. i0 + n - 1 of that list
-  bool direct;                  // all of them: the outputs are written here
   int window, n_sink;
 
   // the part's j-th tile: under a window from the middle on, then the first ones, since those
@@ -358,10 +369,9 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& lis
   const int at = c - units.base[x], whole = units.whole[x];
   const int turned = at < whole ? at : whole + (at - whole) / ns;
   const int split = at < whole ? 0 : (at - whole) % ns;
-  w.direct = A.direct || at < whole;
+  const bool direct = A.direct || at < whole;
   const int tile = (rows + A.rows_cta - 1) / A.rows_cta - 1 - turned;
-  w.unit = (static_cast<int64_t>(w.li) * A.g.H + w.h) * (total - A.whole_units) +
-           (c - A.whole_units);
+  w.unit = direct ? -1 : lh * (total - A.whole_units) + (c - A.whole_units);
   w.r0 = tile * A.rows_cta;
   w.nrows = min(A.rows_cta, rows - w.r0);
   w.p_first = w.start + w.r0 / A.G;
@@ -374,7 +384,7 @@ __device__ __forceinline__ Work work_of(const ChunkArgs& A, const ChunkList& lis
   w.t_lo = max(lo / kKv, w.s_tiles);
   const int all = w.s_tiles + max(0, w.p_last / kKv - w.t_lo + 1);
   w.i0 = split * A.span;
-  w.n = w.direct ? all : min(A.span, all - w.i0);
+  w.n = direct ? all : min(A.span, all - w.i0);
   return w;
 }
 
@@ -738,7 +748,7 @@ __device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list
         }
       }
     }
-    if (w.direct) {
+    if (w.unit < 0) {
       const float inv = l == 0.0f ? 0.0f : 1.0f / l;
       for (int i = 0; i < N; i += 2)
         *reinterpret_cast<uint32_t*>(A.out + orow * D + lane * N + i) =
@@ -746,7 +756,7 @@ __device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list
       if (lane == 0 && A.lse)
         A.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
     } else {
-      const int64_t pr = w.unit * A.rows_cta + rr;
+      const int64_t pr = static_cast<int64_t>(w.unit) * A.rows_cta + rr;
       for (int i = 0; i < N; ++i) A.part_o[pr * D + lane * N + i] = acc[i];
       if (lane == 0) {
         A.part_ml[pr * 2] = m;
@@ -771,9 +781,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
   const int warp = __shfl_sync(0xFFFFFFFFu, tid >> 5, 0);    // known to be the warp's
   if (w.n <= 0) {           // a part past the visible positions of its rows: empty
     pdl_wait();
+    float* ml = A.part_ml + static_cast<int64_t>(w.unit) * A.rows_cta * 2;
     for (int rr = tid; rr < w.nrows; rr += PL::kThreads) {
-      A.part_ml[(w.unit * A.rows_cta + rr) * 2] = -INFINITY;
-      A.part_ml[(w.unit * A.rows_cta + rr) * 2 + 1] = 0.0f;
+      ml[rr * 2] = -INFINITY;
+      ml[rr * 2 + 1] = 0.0f;
     }
     return;
   }
@@ -810,6 +821,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     mbar_init(&sh->drain, 1);
     sh->abort = 0;
     sh->bad = 0;
+    sh->place[0] = w.x;
+    sh->place[1] = w.h;
+    sh->place[2] = w.li;
+    sh->place[3] = w.unit;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kMmaWarp) {
@@ -947,8 +962,15 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       if (ok && *reinterpret_cast<volatile int*>(&sh->bad) == 0) {
         tc_fence_after();
         const float l = sum.x + sum.y;
-        if (w.direct) {
-          const int64_t row = live ? out_row(A, list, w, w.r0 + rr) : -1;
+        // (read again here: kept in registers over the loop they were spilled inside it)
+        Work e = w;
+        const volatile int* place = sh->place;
+        e.x = place[0];
+        e.h = place[1];
+        e.li = place[2];
+        e.unit = place[3];
+        if (e.unit < 0) {
+          const int64_t row = live ? out_row(A, list, e, e.r0 + rr) : -1;
           const float inv = l == 0.0f ? 0.0f : 1.0f / l;      // a row that sees nothing: zeros
           // through the query tile's place (its products have ended), so that a warp writes
           // whole rows: lane by lane a row's 16-byte pieces took 3.8 us at D = 128
@@ -979,7 +1001,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
           if (live && A.lse)
             A.lse[row] = l == 0.0f ? -INFINITY : (m_ref + log2f(l)) * 0.69314718055994530942f;
         } else {
-          const int64_t pr = w.unit * A.rows_cta + rr;
+          const int64_t pr = static_cast<int64_t>(e.unit) * A.rows_cta + rr;
 #pragma unroll
           for (int c = 0; c < D / 32; ++c) {
             uint32_t x[32];
@@ -1205,16 +1227,17 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         if (elected()) {
           mbar_arrive_expect_tx(&full[slot], bytes + A.tx_pad);
           const uint32_t dst = ring + slot * PL::kTile;
-          int r[16];
-#pragma unroll
-          for (int b = 0; b < 16; b += 4)
-            *reinterpret_cast<int4*>(r + b) = *reinterpret_cast<const int4*>(rows + b);
+          // (rows by fours: one by one their latency held back pages of 8 and 24 tokens, spans
+          // 736 -> 810 us; all 16 in registers made the kernel spill)
+          int4 four;
 #pragma unroll
           for (int b = 0; b < 16; ++b) {
-            if (b >= per || r[b] < 0) continue;
+            if (b % 4 == 0) four = lds_int4(rows + b);
+            const int r = b % 4 == 0 ? four.x : b % 4 == 1 ? four.y : b % 4 == 2 ? four.z : four.w;
+            if (b >= per || r < 0) continue;
 #pragma unroll
             for (int half = 0; half < D / 64; ++half)
-              tma_box(dst + half * (128 * 128) + b * box * 128, &map, w.h * D + half * 64, r[b],
+              tma_box(dst + half * (128 * 128) + b * box * 128, &map, w.h * D + half * 64, r,
                       &full[slot]);
           }
         }
