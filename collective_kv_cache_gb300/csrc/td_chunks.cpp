@@ -160,12 +160,18 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
 td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
   if (need <= c->chunk_cap) return TD_OK;
   if (capturing(st)) return TD_ERR_INVALID_ARG;
-  const size_t cap = std::max(need, 2 * c->chunk_cap);
+  // twice the last one, so that growing calls do not leave many behind; where that is not to be
+  // had, what is needed
+  size_t cap = std::max(need, 2 * c->chunk_cap);
   float* p = nullptr;
   if (c->d_chunk) c->old_chunk.reserve(c->old_chunk.size() + 1);
   if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
     cudaGetLastError();
-    return TD_ERR_CUDA;
+    cap = need;
+    if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
+      cudaGetLastError();
+      return TD_ERR_CUDA;
+    }
   }
   if (c->d_chunk) c->old_chunk.push_back(c->d_chunk);
   c->d_chunk = p;

@@ -28,7 +28,7 @@ struct Unfold {
 };
 std::vector<Unfold> g_unfolds;
 int g_device = 0, g_capturing = 0, g_fail_malloc = 0;
-size_t g_floats = 0;
+size_t g_floats = 0, g_room = SIZE_MAX;
 
 Launch& push(int what, const ChunkList& list) {
   g_launches.emplace_back();
@@ -112,7 +112,7 @@ cudaError_t cudaGetDevice(int* d) {
   return cudaSuccess;
 }
 cudaError_t cudaMalloc(void** p, size_t bytes) {
-  if (g_fail_malloc) return cudaErrorMemoryAllocation;
+  if (g_fail_malloc || bytes > g_room) return cudaErrorMemoryAllocation;
   g_floats = bytes / sizeof(float);
   alignas(256) static char place[64];
   *p = place;
@@ -141,6 +141,7 @@ void fake_state(int device, int capturing, int fail_malloc) {
   g_capturing = capturing;
   g_fail_malloc = fail_malloc;
 }
+void fake_room(int64_t bytes) { g_room = static_cast<size_t>(bytes); }
 void fake_reset(void) {
   g_launches.clear();
   g_unfolds.clear();

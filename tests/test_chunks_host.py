@@ -358,3 +358,25 @@ def test_the_last_wave_is_cut_where_it_pays(td, lib):
         tiles = sum(-(-8 * t // 256) for _, _, t in chunks)
         assert cut == (0 if l["direct"] else tiles - int(l["whole"][:n].sum()))
         _check_attention(lib, call, 4, 128, 16, 32, chunks, 0, 0, 1, False)
+
+
+def test_scratch_that_cannot_double_takes_what_is_needed(td, lib):
+    call = Call(td, lib, H=2, D=128)
+    lib.fake_room.argtypes = [C.c_int64]
+    try:
+        assert call.run("attend", chunks=[(0, 9000, 1)], nq=14) == td.TD_OK
+        first = lib.fake_floats()
+        assert call.run("attend", chunks=[(i, 9000, 1) for i in range(4)], nq=14) == td.TD_OK
+        assert lib.fake_floats() >= 2 * first
+        second = lib.fake_floats()
+        # long chunks over 8-bit pages: 7 tiles of 128 positions unfolded, K and V, over 2 layers
+        need = 2 * 2 * 7 * 128 * (2 * 128 // 2 + 2)
+        assert second < need < 2 * second
+        lib.fake_room(need * 4)
+        assert call.run("attend8", chunks=[(0, 0, 800)], nq=14, layers=(0, 2)) == td.TD_OK
+        assert need == lib.fake_floats()
+        lib.fake_room(need * 4 - 4)
+        call = Call(td, lib, H=2, D=128)
+        assert call.run("attend8", chunks=[(0, 0, 800)], nq=14, layers=(0, 2)) == td.TD_ERR_CUDA
+    finally:
+        lib.fake_room(2**62)
