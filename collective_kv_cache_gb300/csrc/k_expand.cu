@@ -8,9 +8,10 @@
 // stored multiplied, with the scale 1. Positions that no token of the chunk sees become zeros
 // with the scale 1, so that 0 * V is 0; a position of an unmapped page zeros with kHole.
 //
-// It reads a byte and writes two an element, once: bound by memory. A CTA takes 32 positions
-// of one layer's K or V, all heads; a thread's vectors of 16 codes are kThreads apart, four in
-// flight.
+// It reads a byte and writes two an element, once: bound by memory (four chunks' 26,000
+// positions of 8 heads, D = 128: some 30 us of a 261 us call, 24 at a copy's rate). A CTA takes
+// 16 positions of one layer's K or V, all heads (32: 264 us, 64: 268); a thread's vectors of 16
+// codes are kThreads apart, four in flight (two as fast, eight 266).
 #include "td_cache8.cuh"
 
 namespace td {
@@ -18,7 +19,7 @@ namespace td {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kPositions = 32;
+constexpr int kPositions = 16;
 
 }  // namespace
 
@@ -32,7 +33,8 @@ expand_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chunk
   __shared__ int s_row[kPositions];
   pdl_wait();
   const int tid = threadIdx.x;
-  const int tile = blockIdx.x >> 2, first = (blockIdx.x & 3) * kPositions;
+  constexpr int kPer = 128 / kPositions;
+  const int tile = blockIdx.x / kPer, first = (blockIdx.x % kPer) * kPositions;
   const int li = blockIdx.y >> 1, kv = blockIdx.y & 1;
   const PoolDev& P = A.pool;
   if (tid < kPositions) {
