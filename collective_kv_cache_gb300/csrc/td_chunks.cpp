@@ -5,6 +5,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <memory>
 #include <new>
 #include <vector>
 
@@ -252,10 +253,14 @@ bool row_map(int E, uint16_t* base, int64_t rows, int b, CUtensorMap* m) {
          CUDA_SUCCESS;
 }
 
+// Sequences' tiles of query rows, and the steps of positions that one of them sees at most.
+struct Loads {
+  uint32_t tiles[kMaxChunkSeqs], seen[kMaxChunkSeqs];
+};
+
 // Cuts every tile's visible positions (in steps of `step` positions) into parts of one length
-// and fills base, nsplit, span and direct; the number of units, or -1. tiles(x), seen(x): a
-// sequence's tiles of query rows and the steps that one of them sees at most. The length is
-// the one with the least estimated time among the divisions of the longest tile.
+// and fills base, nsplit, span and direct; the number of units, or -1. The length is the one
+// with the least estimated time among the divisions of the longest tile.
 struct Cost {
   int64_t slots;      // units that run at once
   int64_t heads;      // kv heads x layers
@@ -266,13 +271,13 @@ struct Cost {
   double row_bytes;   // of partial results per part, over all rows of the launch
 };
 
-template <typename Tiles, typename Seen>
-int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int step,
-            ChunkArgs* a, ChunkUnits* units) {
+int64_t cut(const ChunkList& list, const Cost& cost, const Loads& loads, int step, ChunkArgs* a,
+            ChunkUnits* units) {
+  const uint32_t* const seen = loads.seen;
   int64_t longest = 1, total = 0;
   for (int x = 0; x < list.n; ++x) {
-    longest = std::max<int64_t>(longest, seen(x));
-    total += tiles(x) * seen(x);
+    longest = std::max<int64_t>(longest, seen[x]);
+    total += static_cast<int64_t>(loads.tiles[x]) * seen[x];
   }
   int64_t best = longest, last = 0;
   double best_us = 0.0;
@@ -281,12 +286,11 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
                                            std::min<int64_t>(cost.least, longest));
     if (span == last) continue;
     last = span;
-    int64_t n = 0, most = 1;
-    for (int x = 0; x < list.n; ++x) {
-      const int64_t ns = (seen(x) + span - 1) / span;
-      n += tiles(x) * ns;
-      most = std::max(most, ns);
-    }
+    int64_t n = 0;
+    const uint32_t s32 = static_cast<uint32_t>(span);
+    for (int x = 0; x < list.n; ++x)
+      n += static_cast<int64_t>(loads.tiles[x]) * ((seen[x] + s32 - 1) / s32);
+    const int64_t most = (longest + span - 1) / span;
     n *= cost.heads;
     // one wave: its longest unit; more: the slots' share of the work and half a unit of tail;
     // or the bytes
@@ -310,9 +314,9 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
   units->base[0] = 0;
   int64_t sum = 0;
   for (int x = 0; x < list.n; ++x) {
-    const int64_t ns = (seen(x) + best - 1) / best;
+    const int64_t ns = (seen[x] + best - 1) / best;
     if (ns > 1) a->direct = 0;
-    sum += tiles(x) * ns;
+    sum += loads.tiles[x] * ns;
     if (sum > INT32_MAX) return -1;
     units->nsplit[x] = static_cast<int32_t>(ns);
     units->whole[x] = 0;
@@ -328,8 +332,7 @@ int64_t cut(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int
 // 700 tokens over e4m3 pages, the last 72 in halves) 276 and 261, but 278 in thirds, which are
 // more than one wave again. 984 units of unequal length (6.5 waves) fill the machine by
 // themselves: 724 us whole, 733 cut.
-template <typename Tiles, typename Seen>
-int64_t cut_tail(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen, int64_t n,
+int64_t cut_tail(const ChunkList& list, const Cost& cost, const Loads& loads, int64_t n,
                  double unit_bytes, ChunkArgs* a, ChunkUnits* units) {
   const int64_t r = n % cost.slots;
   if (!a->direct || n <= cost.slots || n > 6 * cost.slots || r == 0) return n;
@@ -337,10 +340,10 @@ int64_t cut_tail(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen
   double total = 0.0, tail = 0.0;
   int64_t left = m, longest = 0;                            // steps of the tail's first unit
   for (int x = list.n - 1; x >= 0; --x) {
-    const double us = (seen(x) * cost.step_us + cost.fixed_us) * cost.heads;
-    total += tiles(x) * us;
-    const int64_t take = std::min(left, tiles(x));
-    if (take > 0) longest = seen(x);
+    const double us = (loads.seen[x] * cost.step_us + cost.fixed_us) * cost.heads;
+    total += loads.tiles[x] * us;
+    const int64_t take = std::min<int64_t>(left, loads.tiles[x]);
+    if (take > 0) longest = loads.seen[x];
     tail += take * us;
     left -= take;
   }
@@ -363,10 +366,10 @@ int64_t cut_tail(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen
   a->direct = 0;
   left = m;
   for (int x = list.n - 1; x >= 0; --x) {
-    const int64_t take = std::min(left, tiles(x));
+    const int64_t take = std::min<int64_t>(left, loads.tiles[x]);
     left -= take;
-    units->whole[x] = static_cast<int32_t>(tiles(x) - take);
-    units->nsplit[x] = take ? static_cast<int32_t>((seen(x) + span - 1) / span) : 1;
+    units->whole[x] = static_cast<int32_t>(loads.tiles[x] - take);
+    units->nsplit[x] = take ? static_cast<int32_t>((loads.seen[x] + span - 1) / span) : 1;
     if (take) a->join_from = list.row[x];
   }
   int64_t sum = 0;
@@ -374,8 +377,9 @@ int64_t cut_tail(const ChunkList& list, const Cost& cost, Tiles tiles, Seen seen
   for (int x = 0; x < list.n; ++x) {
     units->base[x] = static_cast<int32_t>(sum);
     if (whole) a->whole_units = static_cast<int>(sum + units->whole[x]);
-    whole = whole && units->whole[x] == tiles(x);
-    sum += units->whole[x] + (tiles(x) - units->whole[x]) * units->nsplit[x];
+    const int64_t cut = static_cast<int64_t>(loads.tiles[x]) - units->whole[x];
+    whole = whole && cut == 0;
+    sum += units->whole[x] + cut * units->nsplit[x];
   }
   units->base[list.n] = static_cast<int32_t>(sum);
   return sum * cost.heads;
@@ -386,6 +390,11 @@ int64_t seen_positions(const ChunkList& list, const ChunkArgs& a, int x, int row
   const int64_t all = static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x];
   if (a.window == 0) return all;
   return std::min<int64_t>(all, static_cast<int64_t>(a.window) + a.n_sink + (rows - 1) / a.G + 1);
+}
+
+uint32_t tiles_of(const ChunkList& list, const ChunkArgs& a, int x, int rows) {
+  const int64_t all = static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a.G;
+  return static_cast<uint32_t>((all + rows - 1) / rows);
 }
 
 // Bytes of one part of every query row's partial result.
@@ -405,10 +414,12 @@ int64_t plan_rows(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUni
   const double bytes = 2.0 * 128 * a->g.D * (a->scale ? 1 : 2);
   const Cost cost{slots, static_cast<int64_t>(a->g.H) * a->nl,
                   !a->scale && a->g.D == 128 ? 3.1 : 2.0, 4.0, bytes, 2, partial_bytes(list, *a)};
-  return cut(
-      list, cost,
-      [&](int x) { return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R; },
-      [&](int x) { return (seen_positions(list, *a, x, R) + 127) / 128; }, 128, a, units);
+  Loads loads;
+  for (int x = 0; x < list.n; ++x) {
+    loads.tiles[x] = tiles_of(list, *a, x, R);
+    loads.seen[x] = static_cast<uint32_t>((seen_positions(list, *a, x, R) + 127) / 128);
+  }
+  return cut(list, cost, loads, 128, a, units);
 }
 
 int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits* units,
@@ -422,17 +433,17 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
   const double step = codes ? 2.4 : (a->g.D == 128 ? 1.4 : 0.8);
   const Cost cost{c->sm_count, static_cast<int64_t>(a->g.H) * a->nl, step, 4.0,
                   2.0 * 128 * a->g.D * (codes ? 1 : 2) / 8, 2, partial_bytes(list, *a)};
-  const auto tiles = [&](int x) {
-    return (static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G + R - 1) / R;
-  };
-  // a window's positions may straddle one tile more, the first ones' another
-  const auto seen = [&](int x) {
-    const int64_t all =
+  Loads loads;
+  for (int x = 0; x < list.n; ++x) {
+    loads.tiles[x] = tiles_of(list, *a, x, R);
+    int64_t all =
         (static_cast<int64_t>(list.start[x]) + list.row[x + 1] - list.row[x] + 127) / 128;
-    return a->window ? std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2) : all;
-  };
-  const int64_t n = cut(list, cost, tiles, seen, 1, a, units);
-  return n < 0 ? n : cut_tail(list, cost, tiles, seen, n, 4.0 * R * (a->g.D + 2), a, units);
+    // a window's positions may straddle one tile more, the first ones' another
+    if (a->window) all = std::min(all, (seen_positions(list, *a, x, R) + 127) / 128 + 2);
+    loads.seen[x] = static_cast<uint32_t>(all);
+  }
+  const int64_t n = cut(list, cost, loads, 1, a, units);
+  return n < 0 ? n : cut_tail(list, cost, loads, n, 4.0 * R * (a->g.D + 2), a, units);
 }
 
 td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& pool,
@@ -495,51 +506,59 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
       return ch->start[x] + ch->len[x] > ch->start[y] + ch->len[y];
     });
   a.tx_pad = c->attn_tx_pad;
+  struct Launch {
+    ChunkList list;
+    ChunkUnits units;
+    DenseTiles dense;
+    ChunkArgs a;
+    int group, rows;
+    size_t planes, scales, parts, part_rows;
+  };
+  std::vector<std::unique_ptr<Launch>> launches;
   size_t need = 0;
-  for (int pass = 0; pass < 2; ++pass) {
-    if (pass == 1 && (s = chunk_scratch(c, need, st)) != TD_OK) return s;
-    for (int group = 0; group < 3; ++group) {
-      for (size_t at = 0; at < order[group].size();) {
-        ChunkList list;
-        ChunkUnits units;
-        DenseTiles dense;
-        fill_list(ch, order[group], tok, &at, &list);
-        a.dense_rows = 0;
-        if (group == 2) {
-          fill_dense(ch, order[group], a, &at, &list, &dense);
-          a.dense_rows = dense.base[list.n] * 128;
-        }
-        int rows = 0;
-        const int64_t n = group ? plan_tc(c, list, &a, &units, &rows)
-                                : plan_rows(c, list, &a, &units, &rows);
-        if (n < 0) return TD_ERR_INVALID_ARG;
-        // the unfolded rows, their scales, then the partial results
-        const size_t planes = static_cast<size_t>(a.nl) * 2 * a.dense_rows;
-        const size_t scales = planes * a.g.E / 2, parts = scales + planes * H;
-        const size_t part_rows =
-            static_cast<size_t>(n - static_cast<int64_t>(a.whole_units) * H * a.nl) * rows;
-        const size_t floats = a.direct ? 0 : part_rows * (D + 2);
-        need = std::max(need, parts + floats);
-        if (pass == 0) continue;
-        a.part_o = c->d_chunk + parts;
-        a.part_ml = a.direct ? nullptr : a.part_o + part_rows * D;
-        a.dense = nullptr;
-        if (group == 2) {
-          a.dense = reinterpret_cast<uint16_t*>(c->d_chunk);
-          a.dense_scale = c->d_chunk + scales;
-          if (!row_map(a.g.E, a.dense, static_cast<int64_t>(planes), 128, &map) ||
-              launch_expand(a, list, dense, kind, st) != cudaSuccess)
-            return TD_ERR_CUDA;
-        }
-        const uint32_t bit = 1u << (group == 2 ? 9 : kind * 3 + (group ? 2 : rows == 8));
-        const bool fresh = !(c->chunk_launched & bit);
-        if ((group ? launch_chunk_tc(a, list, units, dense, map, kind, fresh, st)
-                   : launch_chunk_rows(a, list, units, kind, rows, fresh, st)) != cudaSuccess ||
-            (!a.direct && launch_chunk_join(a, list, units, rows, st) != cudaSuccess))
-          return TD_ERR_CUDA;
-        c->chunk_launched |= bit;
+  for (int group = 0; group < 3; ++group) {
+    for (size_t at = 0; at < order[group].size();) {
+      launches.emplace_back(new Launch);
+      Launch& l = *launches.back();
+      l.a = a;
+      l.group = group;
+      fill_list(ch, order[group], tok, &at, &l.list);
+      if (group == 2) {
+        fill_dense(ch, order[group], a, &at, &l.list, &l.dense);
+        l.a.dense_rows = l.dense.base[l.list.n] * 128;
       }
+      const int64_t n = group ? plan_tc(c, l.list, &l.a, &l.units, &l.rows)
+                              : plan_rows(c, l.list, &l.a, &l.units, &l.rows);
+      if (n < 0) return TD_ERR_INVALID_ARG;
+      // the unfolded rows, their scales, then the partial results
+      l.planes = static_cast<size_t>(a.nl) * 2 * l.a.dense_rows;
+      l.scales = l.planes * a.g.E / 2;
+      l.parts = l.scales + l.planes * H;
+      l.part_rows =
+          static_cast<size_t>(n - static_cast<int64_t>(l.a.whole_units) * H * a.nl) * l.rows;
+      need = std::max(need, l.parts + (l.a.direct ? 0 : l.part_rows * (D + 2)));
     }
+  }
+  if ((s = chunk_scratch(c, need, st)) != TD_OK) return s;
+  for (const auto& next : launches) {
+    Launch& l = *next;
+    l.a.part_o = c->d_chunk + l.parts;
+    l.a.part_ml = l.a.direct ? nullptr : l.a.part_o + l.part_rows * D;
+    if (l.group == 2) {
+      l.a.dense = reinterpret_cast<uint16_t*>(c->d_chunk);
+      l.a.dense_scale = c->d_chunk + l.scales;
+      if (!row_map(a.g.E, l.a.dense, static_cast<int64_t>(l.planes), 128, &map) ||
+          launch_expand(l.a, l.list, l.dense, kind, st) != cudaSuccess)
+        return TD_ERR_CUDA;
+    }
+    const uint32_t bit = 1u << (l.group == 2 ? 9 : kind * 3 + (l.group ? 2 : l.rows == 8));
+    const bool fresh = !(c->chunk_launched & bit);
+    if ((l.group ? launch_chunk_tc(l.a, l.list, l.units, l.dense, map, kind, fresh, st)
+                 : launch_chunk_rows(l.a, l.list, l.units, kind, l.rows, fresh, st)) !=
+            cudaSuccess ||
+        (!l.a.direct && launch_chunk_join(l.a, l.list, l.units, l.rows, st) != cudaSuccess))
+      return TD_ERR_CUDA;
+    c->chunk_launched |= bit;
   }
   return TD_OK;
 }
