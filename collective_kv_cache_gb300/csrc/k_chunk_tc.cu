@@ -15,15 +15,16 @@
 // 2 x 2^14 exponentials 1024 (32 a cycle): the products bound D = 128, both D = 64.
 //
 // Measured on one GB300: two chunks of 2048 tokens after 8192, 28 query heads on 4, D = 128,
-// take 353 us = 1.53 PFLOP/s (79% of what a large library product reaches), the products busy
-// for four fifths of the time; ragged spans of 1 to 301 tokens over pages of 24, whose boxes
-// are 8 rows, reach 1.29. Under a window of 1024 at D = 64 a block has 11 KV tiles, the first
-// and last of them partly masked: 322 us = 584 TFLOP/s of visible work (64 heads on 8, four
-// chunks of 1500 to 4097), a quarter of it the block's start and end and the rest bound by the
-// softmax's issue. e4m3 pages, four chunks of 500 to 700 after 4096 to 8192, 40 heads on 8,
-// D = 128: 274 us = 1.20 PFLOP/s with the pages unfolded first; converted by every block for
-// itself they took 395. Blocks that stay and take unit after unit lost 5 to 22% to this grid; a single
-// query tile a block, two blocks an SM, lost 13 to 23% at D = 64 (it loads K and V twice).
+// take 349 us = 1.55 PFLOP/s (81% of what a large library product reaches), the tensor pipe
+// busy for 73% of the cycles; ragged spans of 1 to 301 tokens after 6000 to 13000, 40 heads on
+// 8, reach 1.33 (whatever the page size from 8 on). Under a window of 1024 at D = 64 a block has
+// 11 KV tiles, the first and last of them partly masked: 315 us = 597 TFLOP/s of visible work
+// (64 heads on 8, four chunks of 1500 to 4097), a quarter of it the block's start and end and
+// the rest bound by the softmax's issue. e4m3 pages, four chunks of 500 to 700 after 4096 to
+// 8192, 40 heads on 8, D = 128: 262 us = 1.25 PFLOP/s with the pages unfolded first; converted
+// by every block for itself they took 395. Blocks that stay and take unit after unit lost 5 to
+// 22% to this grid; a single query tile a block, two blocks an SM, lost 13 to 23% at D = 64 (it
+// loads K and V twice).
 //
 // The running maximum is lazy: m is raised, and O rescaled (in TMEM, by the softmax warps),
 // only when a row's maximum grew by more than 2^8; until then weights may reach 2^8, which
@@ -40,11 +41,12 @@
 // value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
 // 8-bit pages of long chunks are unfolded before (k_expand.cu): their tiles lie together, whole,
 // with zeros where nothing is seen, and come by TMA without a table or a patch; one warp
-// brings the positions' scales. For chunks of few rows three warps load K's codes and four V's, turn them into f16 and bf16 (exact) and
-// store them as the same tiles; the queries become f16 too, each row with a power of two that
-// brings it to f16's range. The scale of K's row goes on the score's column, that of V's on the
-// weight's; powers of two (e4m3 as td_quantise_append writes it) go into the conversion
-// itself, exactly, and cost the softmax nothing.
+// brings the positions' scales. For shorter chunks three warps load K's codes and four V's, turn
+// them into f16 and bf16 (exact) and store them as the same tiles; the queries become f16 too,
+// each row with a power of two that brings it to f16's range. Either way the scale of K's row
+// goes on the score's column, that of V's on the weight's; powers of two (e4m3 as
+// td_quantise_append writes it) go into the conversion itself, exactly, and cost the softmax
+// nothing.
 //
 // Every wait is bounded by the global timer; when one runs out TD_ERR_DEVICE_TIMEOUT is set
 // and all roles leave their loops, wait (bounded) for what they started and free the TMEM.
@@ -76,8 +78,8 @@ struct Plan {
   static constexpr int kQ = 2 * kRows * D * 2;
   // K and V tiles in flight. One CTA an SM either way (TMEM is taken whole): D = 64 leaves
   // room for more, and must take more than half of the shared memory
-  // (at D = 128 the scales take the third K tile's place)
-  static constexpr int kK = D == 64 ? 4 : (kKind == kCacheBf16 ? 3 : 2);
+  // (at D = 128 a third K tile changed nothing)
+  static constexpr int kK = D == 64 ? 4 : 2;
   static constexpr int kV = D == 64 ? 4 : 2;
   // TMEM columns: two S, two O, and at D = 64 two P of their own: the next scores may then be
   // computed while the softmax still works on the last ones (at D = 128 P lies over S)
