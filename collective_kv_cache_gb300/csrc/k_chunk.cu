@@ -139,10 +139,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       reinterpret_cast<unsigned char (*)[Y::stage]>(s_dyn + warp * (Y::depth * Y::stage));
   const int gid = lane >> 2, tig = lane & 3;
   const int total = units.base[list.n];
-  const int64_t unit = blockIdx.x;
-  const int c = static_cast<int>(unit % total);
-  const int64_t lh = unit / total;
-  const int h = static_cast<int>(lh % A.g.H), li = static_cast<int>(lh / A.g.H);
+  // the heads of one part side by side: their rows lie together, and their scales share sectors
+  const int c = blockIdx.x / (A.g.H * A.nl), lh = blockIdx.x - c * (A.g.H * A.nl);
+  const int h = lh % A.g.H, li = lh / A.g.H;
+  const int64_t unit = static_cast<int64_t>(lh) * total + c;
   int x = 0;
   for (int hi = list.n - 1; x < hi;) {
     const int mid = (x + hi + 1) >> 1;
