@@ -829,13 +829,16 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
     sh->place[3] = w.unit;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
+  pdl_wait();               // (above, the kernel's own arguments and the block's shared memory)
+  // The TMEM only after the wait: a block that held it while it waited for the previous kernel
+  // would keep that kernel's own blocks from theirs, if they allocate after they let this one
+  // start, and neither would end.
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;"
                  ::"r"(smem_u32(&sh->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
     tc_fence_before();
   }
-  pdl_wait();               // (above, the kernel's own arguments and the block's own memory)
   __syncthreads();
   pdl_trigger();
   tc_fence_after();
