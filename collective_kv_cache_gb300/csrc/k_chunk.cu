@@ -388,6 +388,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     const int pa = position(v), pb = position(v + kStep - 1);
     const bool whole = have == kAll && pb <= p_first &&
                        (A.window == 0 || pa > p_last - A.window || v + kStep <= sinks);
+    // what the lane's rows see, a bit a score ((sub * NB + nb) * 4 + i), in steps that mask. (A
+    // score of -infinity or a weight of 0 does not say that a position is out of sight.)
+    uint32_t seen = 0;
 #pragma unroll
     for (int sub = 0; sub < Y::subs; ++sub) {
       [[maybe_unused]] float ks[2];      // rows gid, gid + 8
@@ -410,7 +413,8 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
             const int pq = pos_q[nb][i & 1], pp = position(v + at);
             const bool ok = ((have >> at) & 1u) && pp <= pq &&
                             (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
-            if (!ok) s[sub][nb][i] = -INFINITY;
+            if (ok) seen |= 1u << ((sub * NB + nb) * 4 + i);
+            else s[sub][nb][i] = -INFINITY;
           }
       }
     }
@@ -468,8 +472,8 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             p[nb][i] = __fmul_rn(p[nb][i], vs[i >> 1]);
-            // (a row out of sight keeps the weight 0 whatever its scale)
-            if (!whole && s[sub][nb][i] == -INFINITY) p[nb][i] = 0.0f;
+            // (a position out of sight keeps the weight 0 whatever its scale)
+            if (!whole && !((seen >> ((sub * NB + nb) * 4 + i)) & 1u)) p[nb][i] = 0.0f;
           }
       }
       const unsigned char* sv = st + sub * (Y::kBytes + Y::vAll) + Y::kBytes;
@@ -491,8 +495,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           return const_cast<unsigned char*>(sv) + (i * Y::vChunks + (ch >> 3)) * 512 +
                  ((((ch & 7) * 4 + ((k & 7) >> 1)) * 16) ^ ((i & 1) << 6)) + (d & 7) * 2;
         };
-        // values that must not meet a zero weight (rare: a step that masks, with such a value):
-        // their terms are added to the rows that see them, and they leave the product
+        // values that must not meet the zero weight of a row out of whose sight they are (rare: a
+        // step that masks, with such a value): their terms are added to the rows that see them,
+        // under whatever weight (0 times a NaN or an infinity is a NaN, as in a step that masks
+        // nothing), and they leave the product
         if (!whole) {
           bool bad = false;
 #pragma unroll
@@ -504,6 +510,8 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll 1
             for (int k = 0; k < 16; ++k) {
               float pk[NB][2];
+              const uint32_t sk = __shfl_sync(0xFFFFFFFFu, seen, (k & 7) * 4 + tig) >>
+                                  (sub * NB * 4 + 2 * (k >> 3));
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -522,7 +530,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
                   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if (pk[nb][e] != 0.0f)
+                      if ((sk >> (nb * 4 + e)) & 1u)
                         acc[nb][mt][half * 2 + e] =
                             __fmaf_rn(pk[nb][e], __uint_as_float(b << 16), acc[nb][mt][half * 2 + e]);
                 }
