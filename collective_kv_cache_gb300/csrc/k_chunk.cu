@@ -95,10 +95,6 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-__device__ __forceinline__ bool nonfinite2(uint32_t w) {
-  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
-}
-
 // What a lane holds of one kind of page.
 template <int D, int kKind>
 struct Layout {

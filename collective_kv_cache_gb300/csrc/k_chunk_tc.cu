@@ -38,7 +38,8 @@
 // a patch warp before the products read it: where a tile holds positions that some row does
 // not see, it clears the rows that none sees (their bytes may be anything) and watches for
 // infinities and NaNs in the others: 0 * NaN would reach rows that do not see them. Such a
-// value (rare) is cleared, and the CTA's rows are computed again one by one (slow_rows).
+// value (rare) becomes a zero in the tile, and is added to its element of the rows that see it
+// after their outputs are written (add_values): no other element and no other row changes.
 // 8-bit pages of long chunks are unfolded before (k_expand.cu): their tiles lie together, whole,
 // with zeros where nothing is seen, and come by TMA without a table or a patch; one warp
 // brings the positions' scales. For shorter chunks three warps load K's codes and four V's, turn
@@ -706,63 +707,49 @@ __device__ __forceinline__ void convert_tiles(const ChunkArgs& A, const ChunkLis
   }
 }
 
-// The CTA's rows one by one, a warp a row, in float32 throughout: for tiles that hold
-// infinities or NaNs which some rows see and others do not.
+// V's infinities and NaNs that some of the CTA's rows see and others do not, which the patch
+// warp made zeros: added to their element of the rows that see them. A weight is positive, so
+// the sum with it is that infinity or a NaN whatever the weight, and an output that is written
+// or a part's sum takes the value as it is. A warp finds the positions of a tile, a lane a
+// position; it takes every eighth row.
 template <int D>
-__device__ __noinline__ void slow_rows(const ChunkArgs& A, const ChunkList& list,
-                                       const ChunkUnits& units, int warp) {
+__device__ __noinline__ void add_values(const ChunkArgs& A, const ChunkList& list,
+                                        const ChunkUnits& units, int warp) {
   constexpr int N = D / 32;
   const Work w = work_of(A, list, units);
   const int lane = threadIdx.x & 31;
   const PoolDev& P = A.pool;
-  const int64_t plane = (static_cast<int64_t>(A.layer_begin + w.li) * 2) * P.num_pages * P.P;
-  const int64_t vplane = plane + P.num_pages * P.P;
-  for (int rr = warp; rr < w.nrows; rr += kSoftmaxWarps) {
-    const int r = w.r0 + rr;
-    const int pos = w.start + r / A.G;
-    const int64_t orow = out_row(A, list, w, r);
-    float q[N], acc[N], m = -INFINITY, l = 0.0f;
-    for (int i = 0; i < N; ++i) {
-      q[i] = __uint_as_float(static_cast<uint32_t>(A.q[orow * D + lane * N + i]) << 16);
-      acc[i] = 0.0f;
-    }
-    for (int j = 0; j < w.n; ++j) {
-      const int t0 = w.tile(j) * kKv;
-      for (int p = t0; p < t0 + kKv && p <= pos; ++p) {
-        if (w.window && p <= pos - w.window && p >= w.n_sink) continue;
-        const int64_t row = page_ref(P, list.agent[w.x], p, true).row(P);
-        if (row < 0) continue;
-        const uint16_t* k = P.base + (plane + row) * A.g.E + w.h * D + lane * N;
-        const uint16_t* v = P.base + (vplane + row) * A.g.E + w.h * D + lane * N;
-        float s = 0.0f;
-        for (int i = 0; i < N; ++i)
-          s = __fmaf_rn(q[i], __uint_as_float(static_cast<uint32_t>(k[i]) << 16), s);
-        for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, o);
-        s *= A.scale_log2;
-        const float m_new = fmaxf(m, s);
-        const float f = m == -INFINITY ? 0.0f : exp2f(m - m_new);
-        const float e = s == -INFINITY ? 0.0f : exp2f(s - m_new);
-        l = __fmaf_rn(l, f, e);
-        m = m_new;
-        for (int i = 0; i < N; ++i) {
-          const float val = __uint_as_float(static_cast<uint32_t>(v[i]) << 16);
-          acc[i] = __fmaf_rn(e, val, acc[i] * f);
-        }
+  const int64_t vplane = (static_cast<int64_t>(A.layer_begin + w.li) * 2 + 1) * P.num_pages * P.P;
+  const uint16_t* v = P.base + vplane * A.g.E + w.h * D;
+  for (int j = 0; j < w.n; ++j) {
+    for (int first = 0; first < kKv; first += 32) {
+      const int mine = w.tile(j) * kKv + first + lane;
+      const bool all = mine <= w.p_first &&
+                       (w.window == 0 || mine > w.p_last - w.window || mine < w.n_sink);
+      const int row = page_ref(P, list.agent[w.x], mine, w.needed(mine, mine) && !all).row(P);
+      bool bad = false;
+      for (int c = 0; row >= 0 && c < D; c += 8) {
+        const uint4 q = ldg16(v + static_cast<int64_t>(row) * A.g.E + c);
+        bad = bad || nonfinite2(q.x) || nonfinite2(q.y) || nonfinite2(q.z) || nonfinite2(q.w);
       }
-    }
-    if (w.unit < 0) {
-      const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-      for (int i = 0; i < N; i += 2)
-        *reinterpret_cast<uint32_t*>(A.out + orow * D + lane * N + i) =
-            pack_bf2(acc[i] * inv, acc[i + 1] * inv);
-      if (lane == 0 && A.lse)
-        A.lse[orow] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.69314718055994530942f;
-    } else {
-      const int64_t pr = static_cast<int64_t>(w.unit) * A.rows_cta + rr;
-      for (int i = 0; i < N; ++i) A.part_o[pr * D + lane * N + i] = acc[i];
-      if (lane == 0) {
-        A.part_ml[pr * 2] = m;
-        A.part_ml[pr * 2 + 1] = l;
+      for (uint32_t left = __ballot_sync(0xFFFFFFFFu, bad); left; left &= left - 1) {
+        const int at = __ffs(left) - 1, p = w.tile(j) * kKv + first + at;
+        const uint16_t* x = v + static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, row, at)) * A.g.E;
+        for (int rr = warp; rr < w.nrows; rr += kSoftmaxWarps) {
+          const int pos = w.start + (w.r0 + rr) / A.G;
+          if (p > pos || (w.window && p <= pos - w.window && p >= w.n_sink)) continue;
+          for (int d = lane * N; d < lane * N + N; ++d) {
+            if ((x[d] & 0x7F80u) != 0x7F80u) continue;
+            const float val = __uint_as_float(static_cast<uint32_t>(x[d]) << 16);
+            if (w.unit < 0) {
+              uint16_t* o = A.out + out_row(A, list, w, w.r0 + rr) * D + d;
+              const float sum = __uint_as_float(static_cast<uint32_t>(*o) << 16) + val;
+              *o = static_cast<uint16_t>(pack_bf2(sum, 0.0f));
+            } else {
+              A.part_o[(static_cast<int64_t>(w.unit) * A.rows_cta + rr) * D + d] += val;
+            }
+          }
+        }
       }
     }
   }
@@ -964,7 +951,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       }
       if (ok)
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->o_done[wg], (w.n - 1) & 1, sh, A.err));
-      if (ok && *reinterpret_cast<volatile int*>(&sh->bad) == 0) {
+      if (ok) {
         tc_fence_after();
         const float l = sum.x + sum.y;
         // (read again here: kept in registers over the loop they were spilled inside it)
@@ -1287,10 +1274,13 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
               }
             }
             if ((top & 0xFFFFu) < 0x7F80u && (top >> 16) < 0x7F80u) continue;
-            bad = true;           // (the slow rows read the pages: the tile's row may go)
-#pragma unroll
-            for (int c = 0; c < D / 8; ++c)
-              *reinterpret_cast<uint4*>(tile + tile_at(r, c)) = make_uint4(0u, 0u, 0u, 0u);
+            bad = true;           // (add_values reads the pages: the tile's value may go)
+            uint16_t* at = reinterpret_cast<uint16_t*>(tile);
+#pragma unroll 1
+            for (int d = 0; d < D; ++d) {
+              uint16_t* e = at + tile_at(r, d >> 3) / 2 + (d & 7);
+              if ((*e & 0x7F80u) == 0x7F80u) *e = 0;
+            }
           }
           if (bad) *reinterpret_cast<volatile int*>(&sh->bad) = 1;
           fence_async_smem();
@@ -1313,7 +1303,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
 
   __syncthreads();
   if constexpr (kKind == kCacheBf16) {
-    if (sh->bad && !sh->abort && warp < kSoftmaxWarps) slow_rows<D>(A, list, units, warp);
+    if (sh->bad && !sh->abort && warp < kSoftmaxWarps) add_values<D>(A, list, units, warp);
   }
   if (warp == kMmaWarp) {
     tc_fence_after();

@@ -21,6 +21,11 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
   return r;
 }
 
+// Is either an infinity or a NaN?
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  return (w & 0x7F80u) == 0x7F80u || (w & 0x7F800000u) == 0x7F800000u;
+}
+
 __device__ __forceinline__ void unpack8(const uint4& v, float* x) {
   x[0] = bf_lo(v.x); x[1] = bf_hi(v.x); x[2] = bf_lo(v.y); x[3] = bf_hi(v.y);
   x[4] = bf_lo(v.z); x[5] = bf_hi(v.z); x[6] = bf_lo(v.w); x[7] = bf_hi(v.w);

@@ -62,3 +62,44 @@ def test_a_scale_in_sight_counts_at_a_score_of_minus_infinity(td, n):
     scale[0, 1, pg, sl, 0] = math.nan
     out, z = _run_attention(td, b, pages, q, q8=True)
     assert bool(torch.isnan(out).all())
+
+
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("case", [(2, 3, 128, 0), (40, 3, 128, 0), (170, 2, 64, 60), (300, 7, 128, 0),
+                                  (300, 7, 128, 90), (40, 8, 64, 0)])
+def test_a_value_of_v_changes_its_element_of_the_rows_that_see_it_alone(td, case, value):
+    """Bit for bit: every other element of those rows, and every other row, is as without it."""
+    n, G, D, W = case
+    b = ck.Batch([150, 40], [n, 20], 2, D, 16, seed=63)
+    pool, q = b.rows(*b.pool_shape()), b.rows(1, b.T, 2 * G, D)
+    clean, zc = _run_attention(td, b, td.make_paged(pool, b.bt_t), q, W, 3)
+    keep = torch.ones(clean.shape, dtype=torch.bool, device="cuda")
+    pos = 150 + torch.arange(n, device="cuda")
+    # in the chunk, before it, and among the kept first tokens; two of them in one page
+    for at, d in ((150 + n // 2, 5), (149, D - 1), (148, 5), (1, 17)):
+        pg, sl = b.place(0, np.array([at]))
+        pool[0, 1, pg, sl, 1, d] = value
+        sees = (pos >= at) & ((pos < at + W) | (at < 3) if W else pos >= 0)
+        keep[0, :n, G:, d] &= ~sees[:, None]
+    dirty, zd = _run_attention(td, b, td.make_paged(pool, b.bt_t), q, W, 3)
+    assert torch.equal(zc, zd)
+    assert bool((clean == dirty)[keep].all())
+    assert not bool(torch.isfinite(dirty[~keep]).any())
+    if math.isnan(value):
+        assert bool(torch.isnan(dirty[~keep]).all())
+
+
+def test_a_value_of_v_in_one_part_of_a_tile(td):
+    """The same where the tile's positions are several units, joined afterwards."""
+    b = ck.Batch([6000], [60], 1, 128, 16, seed=64)
+    pool, q = b.rows(*b.pool_shape()), b.rows(1, b.T, 3, 128)
+    clean, zc = _run_attention(td, b, td.make_paged(pool, b.bt_t), q)
+    pg, sl = b.place(0, np.array([6031, 6050]))
+    pool[0, 1, pg, sl, 0, 9] = torch.tensor([math.inf, -math.inf], device="cuda").to(torch.bfloat16)
+    dirty, zd = _run_attention(td, b, td.make_paged(pool, b.bt_t), q)
+    keep = torch.ones(clean.shape, dtype=torch.bool, device="cuda")
+    keep[0, 31:, :, 9] = False
+    assert torch.equal(zc, zd) and bool((clean == dirty)[keep].all())
+    assert not bool(torch.isfinite(dirty[~keep]).any())
+    assert bool((dirty[0, 31:50, :, 9] == math.inf).all())
+    assert bool(torch.isnan(dirty[0, 50:, :, 9]).all())
