@@ -433,11 +433,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // One tile's softmax for the thread's row: all 128 scores into registers, the maximum (and,
 // where it grew, O rescaled), the weights written over the scores and added to the sum. The
 // products may start on the first half of the weights while the second is computed: each half
-// has its barrier. `seen`: the columns in sight, 4 words.
-template <int D, bool kScaled, bool kMask>
+// has its barrier. `seen`: the columns in sight, 4 words. `row` (kRow): the query row's factor,
+// which goes on a score before K's scale does: the score of normalised queries may reach 2^31,
+// and with a large scale alone it would pass float32 where the true one does not.
+template <int D, bool kScaled, bool kMask, bool kRow>
 __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_t t_p,
                                              uint64_t* s_empty, const uint32_t* seen,
-                                             float scale, const float* ks, const float* vs,
+                                             float scale, float row, const float* ks, const float* vs,
                                              bool first, uint64_t* o_done, unsigned o_parity,
                                              uint64_t* p_ready, float& m_ref, float2& sum,
                                              Shared* sh, uint32_t* err) {
@@ -473,8 +475,9 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
         if (i % 4 == 0) k4 = *reinterpret_cast<const float4*>(ks + c * 32 + i);
-        const float2 v = mul2(make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1])),
-                              i % 4 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w));
+        float2 v = make_float2(__uint_as_float(x[c][i]), __uint_as_float(x[c][i + 1]));
+        if constexpr (kRow) v = mul2(v, make_float2(row, row));     // (a power of two: exact)
+        v = mul2(v, i % 4 == 0 ? make_float2(k4.x, k4.y) : make_float2(k4.z, k4.w));
         x[c][i] = __float_as_uint(v.x);
         x[c][i + 1] = __float_as_uint(v.y);
       }
@@ -903,13 +906,10 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const uint32_t t_p = PL::kOwnP ? tmem + lanes + PL::kColP + wg * (kKv / 2) : t_s;
       uint64_t* s_empty = &sh->s_empty[wg];
       // (never 0 below, which would turn the -infinity of a masked score into a NaN)
-      float scale = fabsf(A.scale_log2);
+      const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f);
       bool ok = true;
-      if constexpr (k8) {          // (the factors are the other threads')
+      if constexpr (k8)            // (the queries' factors are the other threads')
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->q_full, 0, sh, A.err));
-        scale *= s_row_scale[rr];
-      }
-      scale = fmaxf(scale, 1e-37f);
       float m_ref = -INFINITY;
       float2 sum = make_float2(0.0f, 0.0f);
       for (int j = 0; ok && j < w.n; ++j) {
@@ -921,6 +921,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         const uint4 valid = sh->info[j % kInfo].load();
         const float* ks = s_scale + (j % kInfo) * 2 * kKv;
         const bool scaled = kScaled && !sh->info[j % kInfo].all_folded();
+        // the query row's factor, by itself or (no scales on the scores) with the softmax's
+        const float row = k8 ? s_row_scale[rr] : 1.0f;
+        const float once = k8 ? fmaxf(scale * row, 1e-37f) : scale;
         if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
           const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
           uint32_t seen[4];
@@ -931,21 +934,19 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
             if (w.window) b &= ~first_bits(hi - w.window + 1 - c * 32) | first_bits(sk - c * 32);
             seen[c] = b & in[c];
           }
-          ok = scaled
-                   ? softmax_tile<D, kScaled, true>(t_s, t_o, t_p, s_empty, seen, scale, ks, ks + kKv,
-                                               j == 0, &sh->o_done[wg], (j - 1) & 1,
-                                               sh->p_ready[wg], m_ref, sum, sh, A.err)
-                   : softmax_tile<D, false, true>(t_s, t_o, t_p, s_empty, seen, scale, ks,
-                                                  ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
-                                                  sh->p_ready[wg], m_ref, sum, sh, A.err);
+          ok = scaled ? softmax_tile<D, kScaled, true, k8>(
+                            t_s, t_o, t_p, s_empty, seen, scale, row, ks, ks + kKv, j == 0,
+                            &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg], m_ref, sum, sh, A.err)
+                      : softmax_tile<D, false, true, false>(
+                            t_s, t_o, t_p, s_empty, seen, once, row, ks, ks + kKv, j == 0,
+                            &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg], m_ref, sum, sh, A.err);
         } else {
-          ok = scaled
-                   ? softmax_tile<D, kScaled, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
-                                                ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
-                                                sh->p_ready[wg], m_ref, sum, sh, A.err)
-                   : softmax_tile<D, false, false>(t_s, t_o, t_p, s_empty, nullptr, scale, ks,
-                                                   ks + kKv, j == 0, &sh->o_done[wg], (j - 1) & 1,
-                                                   sh->p_ready[wg], m_ref, sum, sh, A.err);
+          ok = scaled ? softmax_tile<D, kScaled, false, k8>(
+                            t_s, t_o, t_p, s_empty, nullptr, scale, row, ks, ks + kKv, j == 0,
+                            &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg], m_ref, sum, sh, A.err)
+                      : softmax_tile<D, false, false, false>(
+                            t_s, t_o, t_p, s_empty, nullptr, once, row, ks, ks + kKv, j == 0,
+                            &sh->o_done[wg], (j - 1) & 1, sh->p_ready[wg], m_ref, sum, sh, A.err);
         }
         if (!ok) break;
       }

@@ -103,3 +103,22 @@ def test_a_value_of_v_in_one_part_of_a_tile(td):
     assert not bool(torch.isfinite(dirty[~keep]).any())
     assert bool((dirty[0, 31:50, :, 9] == math.inf).all())
     assert bool(torch.isnan(dirty[0, 50:, :, 9]).all())
+
+
+# ---------------------------------------------- 8-bit pages: scales and queries far from one
+def _far(td, fmt, n, q_log2, k_log2, seed):
+    b = ck.Batch([150], [n], 2, 128, 16, seed=seed)
+    kv = b.rows(*b.pool_shape()).float()
+    kv[:, 0] *= 2.0 ** k_log2
+    pages, codes, scale, val = _pages8(td, b, kv.to(torch.bfloat16), fmt)
+    q = (b.rows(1, b.T, 6, 128).float() * 2.0 ** q_log2).to(torch.bfloat16)
+    got = _run_attention(td, b, pages, q, q8=True)
+    _close(got, ck.attend(b, val[:, 0], val[:, 1], q), _weight_step(b, 3))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [2, 100, 300])
+def test_large_scales_meet_small_queries(td, n, fmt):
+    """K's scales around 2^106 and queries around 2^-104: scores of some hundreds. A score before
+    its scales reaches 2^25 and more, which times K's scale alone is past float32."""
+    _far(td, fmt, n, -104, 112, 65)
