@@ -905,8 +905,9 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       const uint32_t t_s = tmem + lanes + wg * kKv, t_o = tmem + lanes + PL::kColO + wg * D;
       const uint32_t t_p = PL::kOwnP ? tmem + lanes + PL::kColP + wg * (kKv / 2) : t_s;
       uint64_t* s_empty = &sh->s_empty[wg];
-      // (never 0 below, which would turn the -infinity of a masked score into a NaN)
-      const float scale = fmaxf(fabsf(A.scale_log2), 1e-37f);
+      // (never 0 below, which would turn the -infinity of a masked score into a NaN: the least
+      // float32, under which no score is more than 2^-21)
+      const float scale = fmaxf(fabsf(A.scale_log2), 0x1p-149f);
       bool ok = true;
       if constexpr (k8)            // (the queries' factors are the other threads')
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->q_full, 0, sh, A.err));
@@ -923,7 +924,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         const bool scaled = kScaled && !sh->info[j % kInfo].all_folded();
         // the query row's factor, by itself or (no scales on the scores) with the softmax's
         const float row = k8 ? s_row_scale[rr] : 1.0f;
-        const float once = k8 ? fmaxf(scale * row, 1e-37f) : scale;
+        const float once = k8 ? fmaxf(scale * row, 0x1p-149f) : scale;
         if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
           const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
           uint32_t seen[4];

@@ -122,3 +122,29 @@ def test_large_scales_meet_small_queries(td, n, fmt):
     """K's scales around 2^106 and queries around 2^-104: scores of some hundreds. A score before
     its scales reaches 2^25 and more, which times K's scale alone is past float32."""
     _far(td, fmt, n, -104, 112, 65)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [2, 100, 300])
+def test_the_smallest_queries(td, n, fmt):
+    """Queries around 2^-115, next to the least normal numbers, and K's scales around 2^109. The
+    query row's power of two times the softmax scale is then a subnormal of 20 bits or more: 2^-21 of a
+    score, within the bound's 2^-16."""
+    _far(td, fmt, n, -115, 115, 66)
+
+
+@pytest.mark.parametrize("scale", [1e-38, -1e-38, 0.0])
+@pytest.mark.parametrize("n", [2, 100])
+def test_the_smallest_softmax_scales(td, n, scale):
+    """q . k around 2^126 times a softmax scale next to the least float32: scores around 1; and a
+    scale of 0, where every position counts alike."""
+    b = ck.Batch([150], [n], 2, 128, 16, seed=67)
+    pool, q = b.rows(*b.pool_shape()).float(), b.rows(1, b.T, 6, 128).float()
+    pool[:, 0] *= 2.0 ** 61
+    pool, q = pool.to(torch.bfloat16), (q * 2.0 ** 60).to(torch.bfloat16)
+    # what the calls take: the scale as a float32 in base 2, a subnormal of 2^-149 steps
+    s2 = float(np.float32(np.float32(scale) * np.float32(1.4426950408889634)))
+    got = _run_attention(td, b, td.make_paged(pool, b.bt_t), q, scale=scale)
+    out, lse, mag, dot = ck.attend(b, pool[:, 0].double(), pool[:, 1].double(), q,
+                                   scale=s2 * math.log(2.0))
+    _close(got, (out, lse, mag, dot.abs()), _weight_step(b, 3))
