@@ -398,8 +398,10 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
       for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          s[sub][nb][i] = __fmul_rn(s[sub][nb][i], Y::k8 ? __fmul_rn(ks[i >> 1], row_scale[nb][i & 1])
-                                                         : A.scale_log2);
+          // (the query row's factor, then K's scale: the two multiplied first could pass float32,
+          // and a score of 0 become infinity times 0)
+          s[sub][nb][i] = Y::k8 ? __fmul_rn(__fmul_rn(s[sub][nb][i], row_scale[nb][i & 1]), ks[i >> 1])
+                                : __fmul_rn(s[sub][nb][i], A.scale_log2);
       if (!whole) {
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb)

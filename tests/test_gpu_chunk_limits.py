@@ -148,3 +148,20 @@ def test_the_smallest_softmax_scales(td, n, scale):
     out, lse, mag, dot = ck.attend(b, pool[:, 0].double(), pool[:, 1].double(), q,
                                    scale=s2 * math.log(2.0))
     _close(got, (out, lse, mag, dot.abs()), _weight_step(b, 3))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [2, 100, 300])
+def test_a_large_scale_of_a_row_of_zero_codes(td, n, fmt):
+    """Codes of zero under a scale of 2^100, queries around 2^60, the other rows' scales around
+    2^-60: that position's score is 0, not infinity times 0."""
+    b = ck.Batch([150], [n], 2, 128, 16, seed=68)
+    kv = b.rows(*b.pool_shape()).float()
+    kv[:, 0] *= 2.0 ** -60
+    pg, sl = b.place(0, np.array([7, 131, 150]))
+    kv[0, 0, pg, sl] = 0
+    _, codes, scale, val = _pages8(td, b, kv.to(torch.bfloat16), fmt)
+    scale[0, 0, pg, sl] = 2.0 ** 100
+    q = (b.rows(1, b.T, 6, 128).float() * 2.0 ** 60).to(torch.bfloat16)
+    got = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, fmt), q, q8=True)
+    _close(got, ck.attend(b, val[:, 0], val[:, 1], q), _weight_step(b, 3))
