@@ -26,10 +26,11 @@
 // 22% to this grid; a single query tile a block, two blocks an SM, lost 13 to 23% at D = 64 (it
 // loads K and V twice).
 //
-// The running maximum is lazy: m is raised, and O rescaled (in TMEM, by the softmax warps),
-// only when a row's maximum grew by more than 2^8; until then weights may reach 2^8, which
-// float32 sums and bf16's relative precision do not mind. The weights are rounded to bf16 (at
-// most 2^-8 relative) for the tensor cores, as the output is; their sum is taken before, in
+// The running maximum is lazy: the reference m is set to a row's maximum and 8 more (in base 2),
+// and raised, and O rescaled (in TMEM, by the softmax warps), only when the maximum passes it.
+// So no weight is over 1 (V may be next to the largest float32), and a row's largest is 2^-8 or
+// more, which float32 sums and bf16's relative precision do not mind. The weights are rounded to
+// bf16 (at most 2^-8 relative) for the tensor cores, as the output is; their sum is taken before, in
 // float32. (Split in two parts as in the streaming kernel they would cost half the products'
 // time again.)
 //
@@ -65,6 +66,7 @@ constexpr int kLoadWarp = 9;          // bf16: K by TMA; V: the next warp
 constexpr int kPatchWarp = 11;
 constexpr int kConvertWarp = 12;      // 8-bit: the first of four that convert V (9-11: K)
 constexpr int kInfo = 8;              // KV tiles whose facts are kept
+constexpr float kLazy = 8.0f;         // the reference is set by this much over the maximum (base 2)
 
 // Kinds of the kernel: CacheKind, or 8-bit pages' unfolded copy.
 constexpr int kUnfolded = 3;
@@ -492,12 +494,12 @@ __device__ __forceinline__ bool softmax_tile(uint32_t t_s, uint32_t t_o, uint32_
   }
   const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
   const float m_tile = top == -INFINITY ? top : __fmul_rn(top, scale);
-  const float m_new = fmaxf(m_ref, m_tile);
   if (first) {
-    m_ref = m_new;
-  } else if (__any_sync(0xFFFFFFFFu, m_new > m_ref + 8.0f)) {
+    m_ref = m_tile + kLazy;
+  } else if (__any_sync(0xFFFFFFFFu, m_tile > m_ref)) {
     // rows that did not grow keep theirs: a row's result does not depend on the others
-    const bool grow = m_new > m_ref + 8.0f;
+    const bool grow = m_tile > m_ref;
+    const float m_new = m_tile + kLazy;
     const float f = grow ? ex2(m_ref - m_new) : 1.0f;
     if (grow) m_ref = m_new;
     sum.x *= f;

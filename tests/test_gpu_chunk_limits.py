@@ -165,3 +165,27 @@ def test_a_large_scale_of_a_row_of_zero_codes(td, n, fmt):
     q = (b.rows(1, b.T, 6, 128).float() * 2.0 ** 60).to(torch.bfloat16)
     got = _run_attention(td, b, td.make_paged8(codes, scale, b.bt_t, fmt), q, q8=True)
     _close(got, ck.attend(b, val[:, 0], val[:, 1], q), _weight_step(b, 3))
+
+
+# ----------------------------------------------------------------- large values under the sums
+@pytest.mark.parametrize("fmt", ["", "int8", "e4m3"])
+@pytest.mark.parametrize("n", [2, 40, 300])
+def test_weights_stay_at_one_or_less(td, n, fmt):
+    """A later tile's score is 7.5 (in base 2) over all before it, and its V next to the largest
+    float32 in half of its dims: weights over 1 would make its term infinite, where the row's
+    value is 181 / (200 + 181) of it or less."""
+    b = ck.Batch([200], [n], 1, 128, 16, seed=69)
+    kv = b.rows(*b.pool_shape())
+    q = torch.zeros((1, n, 3, 128), dtype=torch.bfloat16, device="cuda")
+    kv[:, 0] = 0
+    q[..., 0] = 1.0
+    pg, sl = b.place(0, np.array([140]))
+    kv[0, 0, pg, sl, 0, 0] = 7.5
+    kv[0, 1, pg, sl, 0] = 0
+    kv[0, 1, pg, sl, 0, :64] = 2e38
+    if fmt:
+        pages, _, _, val = _pages8(td, b, kv, fmt)
+    else:
+        pages, val = td.make_paged(kv, b.bt_t), kv.double()
+    got = _run_attention(td, b, pages, q, scale=math.log(2.0), q8=bool(fmt))
+    _close(got, ck.attend(b, val[:, 0], val[:, 1], q, scale=math.log(2.0)), _weight_step(b, 3))
