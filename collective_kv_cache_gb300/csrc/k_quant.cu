@@ -17,7 +17,7 @@
 // an element and it ran at 80% of the copy rate, bound by their issue. The read takes 8 (one
 // 16-byte store a lane, whole lines a warp): with 16 it ran at 92%. A CTA takes up to
 // 32 tokens of one layer and K or V; their page rows are looked up once, by one thread each.
-#include "td_device.cuh"
+#include "td_cache8.cuh"
 
 namespace td {
 
@@ -114,13 +114,13 @@ __device__ __forceinline__ void values4(uint32_t w, float* y) {
     for (int i = 0; i < 4; ++i)
       y[i] = static_cast<float>(static_cast<int8_t>((w >> (8 * i)) & 0xFFu));
   } else {
+    // by way of f16, which holds every code exactly, the two NaNs included
+    const uint32_t h[2] = {word_f16<kKind, false>(w), word_f16<kKind, true>(w)};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      // sign, exponent and fraction moved to a float's places, 2^120 too small (bias 7
-      // against 127); the product is exact, subnormal codes included
-      const uint32_t b = (w >> (8 * i)) & 0xFFu;
-      y[i] = __fmul_rn(__uint_as_float(((b & 0x80u) << 24) | ((b & 0x7Fu) << 20)), 0x1p120f);
-    }
+    for (int i = 0; i < 2; ++i)
+      asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\tcvt.f32.f16 %0, lo;\n\t"
+          "cvt.f32.f16 %1, hi;\n\t}"
+          : "=f"(y[2 * i]), "=f"(y[2 * i + 1]) : "r"(h[i]));
   }
 }
 

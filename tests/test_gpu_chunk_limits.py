@@ -189,3 +189,24 @@ def test_weights_stay_at_one_or_less(td, n, fmt):
         pages, val = td.make_paged(kv, b.bt_t), kv.double()
     got = _run_attention(td, b, pages, q, scale=math.log(2.0), q8=bool(fmt))
     _close(got, ck.attend(b, val[:, 0], val[:, 1], q, scale=math.log(2.0)), _weight_step(b, 3))
+
+
+# ------------------------------------------------------------------------------ 8-bit codes
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_every_code_is_read_as_the_value_it_stands_for(td, fmt):
+    """All 256 bytes, the two that e4m3 reads as NaN and int8's -128 among them."""
+    b = ck.Batch([5], [9], 2, 128, 16, seed=70)
+    codes = torch.arange(int(np.prod(b.pool_shape())), device="cuda").to(torch.int8)
+    codes = codes.view(b.pool_shape()).contiguous()
+    scale = torch.rand(b.pool_shape()[:-1], generator=b.gen, device="cuda") * 3 + 0.01
+    ctx = _ctx(td, b)
+    k, v = (torch.zeros((1, b.T, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    td.td_dequantise_read(ctx.handle, _chunks(td, b), td.make_paged8(codes, scale, b.bt_t, fmt), 0, 1,
+                          k.data_ptr(), v.data_ptr(), _stream())
+    assert _errors(td, ctx) == (0, 0)
+    pg, sl = b.place(0, np.arange(5, 14))
+    want = (ck.code_values(codes, fmt).float() * scale[..., None]).to(torch.bfloat16)
+    for kv, got in enumerate((k, v)):
+        w = want[:, kv, pg, sl]
+        assert torch.equal(torch.isnan(got), torch.isnan(w))
+        assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(w))
