@@ -156,16 +156,33 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   return TD_OK;
 }
 
-// Scratch of at least `need` floats. An outgrown buffer stays until the context goes: a
-// captured graph may hold its address. Inside a capture nothing can be allocated.
+// Scratch of at least `need` floats. A buffer that a captured call has used stays until the
+// context goes, since the graph holds its address; any other is freed when it is outgrown, after
+// the stream's work (the context's earlier calls are ordered before this one). Inside a capture
+// nothing can be allocated.
+constexpr size_t kScratchSpare = size_t{64} << 20;      // floats beyond the need, at most
 td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
-  if (need <= c->chunk_cap) return TD_OK;
-  if (capturing(st)) return TD_ERR_INVALID_ARG;
-  // twice the last one, so that growing calls do not leave many behind; where that is not to be
-  // had, what is needed
-  size_t cap = std::max(need, 2 * c->chunk_cap);
+  if (need == 0) return TD_OK;
+  const bool captured = capturing(st);
+  if (need <= c->chunk_cap) {
+    c->chunk_kept |= captured;
+    return TD_OK;
+  }
+  if (captured) return TD_ERR_INVALID_ARG;
+  // twice the last one, so that growing calls grow it seldom; where that is not to be had, what
+  // is needed
+  size_t cap = std::max(need, std::min(2 * c->chunk_cap, need + kScratchSpare));
+  if (c->d_chunk && c->chunk_kept) {
+    c->old_chunk.reserve(c->old_chunk.size() + 1);
+  } else if (c->d_chunk) {
+    if (cudaStreamSynchronize(st) != cudaSuccess || cudaFree(c->d_chunk) != cudaSuccess) {
+      cudaGetLastError();
+      return TD_ERR_CUDA;
+    }
+    c->d_chunk = nullptr;
+    c->chunk_cap = 0;
+  }
   float* p = nullptr;
-  if (c->d_chunk) c->old_chunk.reserve(c->old_chunk.size() + 1);
   if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
     cudaGetLastError();
     cap = need;
@@ -177,6 +194,7 @@ td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
   if (c->d_chunk) c->old_chunk.push_back(c->d_chunk);
   c->d_chunk = p;
   c->chunk_cap = cap;
+  c->chunk_kept = false;
   return TD_OK;
 }
 

@@ -69,8 +69,9 @@ struct td_ctx {
   uint32_t attn_tx_pad = 0;         // fault injection: bytes the attention never receives
   float* d_chunk = nullptr;         // chunk attention's partial results, grown on demand
   size_t chunk_cap = 0;             // its size in floats
+  bool chunk_kept = false;          // a captured call has used it
   uint32_t chunk_launched = 0;      // its kernels that this context has launched, a bit each
-  std::vector<float*> old_chunk;    // outgrown ones: captured graphs may still name them
+  std::vector<float*> old_chunk;    // outgrown ones that captured calls have used
   // pinned host words for results
   int64_t* h_words = nullptr;       // [4]
 };

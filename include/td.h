@@ -431,8 +431,11 @@ td_status td_dequantise_read(td_ctx* ctx, const td_chunks* chunks, const td_page
  *   lse   DEVICE float [layer_end-layer_begin][T][n_q_heads], or NULL
  * n_q_heads a multiple of H, (layer_end-layer_begin) * T * n_q_heads < 2^31; head dims 64
  * and 128; scale finite, also in base 2 (else TD_ERR_INVALID_ARG).
- * The context owns the partial results' scratch, which grows with the calls: a call made in a
- * stream capture must find it large enough (make the call once before capturing it; else
+ * The context owns the scratch for partial results, which grows with the calls: it holds what
+ * the largest call so far needed and at most 2^28 bytes more, and beside that the outgrown
+ * buffers that captured calls have used, until the context goes (a graph holds their address).
+ * The others are freed: a call that grows the scratch waits for `stream` first. A call made in
+ * a stream capture must find it large enough (make the call once before capturing it; else
  * TD_ERR_INVALID_ARG). */
 td_status td_chunk_attention(td_ctx* ctx, const td_chunks* chunks, const td_paged* pool,
                              int32_t layer_begin, int32_t layer_end, const void* q,
@@ -442,7 +445,7 @@ td_status td_chunk_attention(td_ctx* ctx, const td_chunks* chunks, const td_page
 /* The same over 8-bit pages: K and V are code * scale, with any scale. (The e4m3 codes that
  * stand for a NaN, which td_quantise_append does not write, have no defined value in sight.)
  * For long chunks the visible pages are first unfolded into the context's scratch, at most
- * 2^30 bytes of it. */
+ * 2^30 bytes of it at a time, beside the partial results. */
 td_status td_chunk_attention_q8(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
                                 int32_t layer_begin, int32_t layer_end, const void* q,
                                 int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,

@@ -2,6 +2,7 @@
 // runtime calls and the kernel launches are stand-ins that record what they were given, so
 // that refusals and launch plans can be tested by tests/test_chunks_host.py.
 #include <cstdlib>
+#include <map>
 #include <vector>
 
 #include "td_ctx.h"
@@ -29,6 +30,8 @@ struct Unfold {
 std::vector<Unfold> g_unfolds;
 int g_device = 0, g_capturing = 0, g_fail_malloc = 0;
 size_t g_floats = 0, g_room = SIZE_MAX;
+std::map<void*, size_t> g_held;      // what cudaMalloc gave and cudaFree has not had
+bool g_synchronised = false, g_fail_wait = false;
 
 Launch& push(int what, const ChunkList& list) {
   g_launches.emplace_back();
@@ -114,9 +117,21 @@ cudaError_t cudaGetDevice(int* d) {
 cudaError_t cudaMalloc(void** p, size_t bytes) {
   if (g_fail_malloc || bytes > g_room) return cudaErrorMemoryAllocation;
   g_floats = bytes / sizeof(float);
-  alignas(256) static char place[64];
-  *p = place;
+  // (an address of its own, 256-byte aligned, that nothing reads)
+  static uintptr_t next = 0x100000000;
+  *p = reinterpret_cast<void*>(next);
+  next += (bytes + 255) / 256 * 256 + 256;
+  g_held[*p] = bytes;
   return cudaSuccess;
+}
+cudaError_t cudaFree(void* p) {
+  if (!g_synchronised || g_held.erase(p) != 1) return cudaErrorInvalidValue;
+  g_synchronised = false;
+  return cudaSuccess;
+}
+cudaError_t cudaStreamSynchronize(cudaStream_t) {
+  g_synchronised = true;
+  return g_fail_wait ? cudaErrorLaunchFailure : cudaSuccess;
 }
 cudaError_t cudaGetLastError(void) { return cudaSuccess; }
 cudaError_t cudaStreamIsCapturing(cudaStream_t, cudaStreamCaptureStatus* s) {
@@ -146,6 +161,14 @@ void fake_reset(void) {
   g_launches.clear();
   g_unfolds.clear();
 }
+// Bytes that are held, of any context; buffers; whether waiting for a stream fails.
+int64_t fake_held(void) {
+  size_t sum = 0;
+  for (const auto& h : g_held) sum += h.second;
+  return static_cast<int64_t>(sum);
+}
+int fake_buffers(void) { return static_cast<int>(g_held.size()); }
+void fake_wait(int fails) { g_fail_wait = fails != 0; }
 int64_t fake_floats(void) { return static_cast<int64_t>(g_floats); }
 int fake_launches(void) { return static_cast<int>(g_launches.size()); }
 // what, kind, rows, n, direct, span, tok0, tokens, per_cta, lane_shift, head_mul, box_rows,
