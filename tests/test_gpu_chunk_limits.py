@@ -210,3 +210,61 @@ def test_every_code_is_read_as_the_value_it_stands_for(td, fmt):
         w = want[:, kv, pg, sl]
         assert torch.equal(torch.isnan(got), torch.isnan(w))
         assert torch.equal(torch.nan_to_num(got), torch.nan_to_num(w))
+
+
+# --------------------------------------------- 8-bit pages: layer ranges, far offsets, holes
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("lens", [[2, 1], [100, 31], [300, 2]])
+def test_layers_of_a_range_over_8bit_pages(td, lens, fmt):
+    """Layers 2 and 3 of 4, on each way through the attention."""
+    b = ck.Batch([200, 31], lens, 2, 64, 16, 4, seed=71)
+    pages, _, _, val = _pages8(td, b, b.rows(*b.pool_shape()), fmt)
+    q = b.rows(2, b.T, 6, 64)
+    ctx = _ctx(td, b)
+    out, z = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+    td.td_chunk_attention_q8(ctx.handle, _chunks(td, b), pages, 2, 4, q.data_ptr(), 6, 0.125, 0, 0,
+                             out.data_ptr(), z.data_ptr(), _stream())
+    assert _errors(td, ctx) == (0, 0)
+    b.L = 2
+    _close((out, z), ck.attend(b, val[2:, 0], val[2:, 1], q), _weight_step(b, 3))
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_8bit_pages_beyond_32_bit_offsets(td, fmt):
+    """A pool of more than 2^32 bytes of codes: the same bits as from a small one."""
+    H, D, P, L = 8, 128, 16, 2
+    pages = 70000                                # 2 layers: 4.6e9 codes
+    codes = torch.zeros((L, 2, pages, P, H, D), dtype=torch.int8, device="cuda")
+    scale = torch.zeros((L, 2, pages, P, H), device="cuda")
+    for lens in ([1, 1], [130, 40], [300, 40]):
+        b = ck.Batch([400, 90], lens, H, D, P, L, seed=72)
+        near, c, s, _ = _pages8(td, b, b.rows(*b.pool_shape()), fmt)
+        far = torch.where(b.bt_t >= 0, pages - 1 - b.bt_t, -1).to(torch.int32).contiguous()
+        codes[:, :, pages - b.pages:] = c.flip(2)
+        scale[:, :, pages - b.pages:] = s.flip(2)
+        q = b.rows(L, b.T, H * 2, D)
+        one = _run_attention(td, b, near, q, q8=True)
+        two = _run_attention(td, b, td.make_paged8(codes, scale, far, fmt), q, q8=True)
+        assert torch.equal(one[0], two[0]) and torch.equal(one[1], two[1])
+        assert bool(torch.isfinite(one[0]).all())
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("n", [2, 100])
+def test_a_scale_that_is_not_finite_in_the_middle_of_a_chunk(td, n, fmt):
+    """K's or V's scale of a token within the chunk is a NaN: the rows that see it are NaN, the
+    tokens before it and the other kv head keep to float64."""
+    b = ck.Batch([150], [n], 2, 128, 16, seed=73)
+    pages, codes, scale, val = _pages8(td, b, b.rows(*b.pool_shape()), fmt)
+    q = b.rows(1, b.T, 4, 128)
+    want = ck.attend(b, val[:, 0], val[:, 1], q)
+    at = n // 2
+    pg, sl = b.place(0, np.array([150 + at]))
+    for half in (0, 1):
+        dirty = scale.clone()
+        dirty[0, half, pg, sl, 1] = math.nan
+        out, z = _run_attention(td, b, td.make_paged8(codes, dirty, b.bt_t, fmt), q, q8=True)
+        step = _weight_step(b, 2)
+        _close((out[:, :at], z[:, :at]), [t[:, :at] for t in want], step)
+        _close((out[:, :, :2], z[:, :, :2]), [t[:, :, :2] for t in want], step)
+        assert bool(torch.isnan(out[0, at:, 2:]).all())
