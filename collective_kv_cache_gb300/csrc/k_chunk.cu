@@ -95,6 +95,13 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
+// The larger one, a NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // What a lane holds of one kind of page.
 template <int D, int kKind>
 struct Layout {
@@ -384,9 +391,6 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
     const int pa = position(v), pb = position(v + kStep - 1);
     const bool whole = have == kAll && pb <= p_first &&
                        (A.window == 0 || pa > p_last - A.window || v + kStep <= sinks);
-    // what the lane's rows see, a bit a score ((sub * NB + nb) * 4 + i), in steps that mask. (A
-    // score of -infinity or a weight of 0 does not say that a position is out of sight.)
-    uint32_t seen = 0;
 #pragma unroll
     for (int sub = 0; sub < Y::subs; ++sub) {
       [[maybe_unused]] float ks[2];      // rows gid, gid + 8
@@ -411,8 +415,9 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
             const int pq = pos_q[nb][i & 1], pp = position(v + at);
             const bool ok = ((have >> at) & 1u) && pp <= pq &&
                             (A.window == 0 || pp > pq - A.window || pp < A.n_sink);
-            if (ok) seen |= 1u << ((sub * NB + nb) * 4 + i);
-            else s[sub][nb][i] = -INFINITY;
+            // (-infinity says out of sight below, so a score that is -infinity by itself becomes
+            // the least number; a bit a score in a register cost 1.7% of an int8 token's time)
+            s[sub][nb][i] = ok ? max_nan(s[sub][nb][i], -3.402823466e38f) : -INFINITY;
           }
       }
     }
@@ -471,7 +476,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
           for (int i = 0; i < 4; ++i) {
             p[nb][i] = __fmul_rn(p[nb][i], vs[i >> 1]);
             // (a position out of sight keeps the weight 0 whatever its scale)
-            if (!whole && !((seen >> ((sub * NB + nb) * 4 + i)) & 1u)) p[nb][i] = 0.0f;
+            if (!whole && s[sub][nb][i] == -INFINITY) p[nb][i] = 0.0f;
           }
       }
       const unsigned char* sv = st + sub * (Y::kBytes + Y::vAll) + Y::kBytes;
@@ -508,14 +513,15 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
 #pragma unroll 1
             for (int k = 0; k < 16; ++k) {
               float pk[NB][2];
-              const uint32_t sk = __shfl_sync(0xFFFFFFFFu, seen, (k & 7) * 4 + tig) >>
-                                  (sub * NB * 4 + 2 * (k >> 3));
+              bool sees[NB][2];
 #pragma unroll
               for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                   const float mine = k < 8 ? p[nb][e] : p[nb][e + 2];
                   pk[nb][e] = __shfl_sync(0xFFFFFFFFu, mine, (k & 7) * 4 + tig);
+                  const float score = k < 8 ? s[sub][nb][e] : s[sub][nb][e + 2];
+                  sees[nb][e] = __shfl_sync(0xFFFFFFFFu, score, (k & 7) * 4 + tig) != -INFINITY;
                 }
 #pragma unroll
               for (int mt = 0; mt < KCH; ++mt)
@@ -528,7 +534,7 @@ chunk_rows_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ C
                   for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                      if ((sk >> (nb * 4 + e)) & 1u)
+                      if (sees[nb][e])
                         acc[nb][mt][half * 2 + e] =
                             __fmaf_rn(pk[nb][e], __uint_as_float(b << 16), acc[nb][mt][half * 2 + e]);
                 }
