@@ -913,6 +913,7 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
       bool ok = true;
       if constexpr (k8)            // (the queries' factors are the other threads')
         ok = __all_sync(0xFFFFFFFFu, wait_or_abort(&sh->q_full, 0, sh, A.err));
+      const float row = k8 ? s_row_scale[rr] : 1.0f;
       float m_ref = -INFINITY;
       float2 sum = make_float2(0.0f, 0.0f);
       for (int j = 0; ok && j < w.n; ++j) {
@@ -925,7 +926,6 @@ chunk_tc_kernel(const __grid_constant__ ChunkArgs A, const __grid_constant__ Chu
         const float* ks = s_scale + (j % kInfo) * 2 * kKv;
         const bool scaled = kScaled && !sh->info[j % kInfo].all_folded();
         // the query row's factor, by itself or (no scales on the scores) with the softmax's
-        const float row = k8 ? s_row_scale[rr] : 1.0f;
         const float once = k8 ? fmaxf(scale * row, 0x1p-149f) : scale;
         if (!w.whole(kt, pf, pl) || !no_holes(valid)) {
           const uint32_t in[4] = {valid.x, valid.y, valid.z, valid.w};
