@@ -156,47 +156,9 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
   return TD_OK;
 }
 
-// Scratch of at least `need` floats. A buffer that a captured call has used stays until the
-// context goes, since the graph holds its address; any other is freed when it is outgrown, after
-// the stream's work (the context's earlier calls are ordered before this one). Inside a capture
-// nothing can be allocated.
-constexpr size_t kScratchSpare = size_t{64} << 20;      // floats beyond the need, at most
-td_status chunk_scratch(td_ctx* c, size_t need, cudaStream_t st) {
-  if (need == 0) return TD_OK;
-  const bool captured = capturing(st);
-  if (need <= c->chunk_cap) {
-    c->chunk_kept |= captured;
-    return TD_OK;
-  }
-  if (captured) return TD_ERR_INVALID_ARG;
-  // twice the last one, so that growing calls grow it seldom; where that is not to be had, what
-  // is needed
-  size_t cap = std::max(need, std::min(2 * c->chunk_cap, need + kScratchSpare));
-  if (c->d_chunk && c->chunk_kept) {
-    c->old_chunk.reserve(c->old_chunk.size() + 1);
-  } else if (c->d_chunk) {
-    if (cudaStreamSynchronize(st) != cudaSuccess || cudaFree(c->d_chunk) != cudaSuccess) {
-      cudaGetLastError();
-      return TD_ERR_CUDA;
-    }
-    c->d_chunk = nullptr;
-    c->chunk_cap = 0;
-  }
-  float* p = nullptr;
-  if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
-    cudaGetLastError();
-    cap = need;
-    if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
-      cudaGetLastError();
-      return TD_ERR_CUDA;
-    }
-  }
-  if (c->d_chunk) c->old_chunk.push_back(c->d_chunk);
-  c->d_chunk = p;
-  c->chunk_cap = cap;
-  c->chunk_kept = false;
-  return TD_OK;
-}
+// Twice the last one, so that growing calls grow it seldom, but at most this many floats beyond
+// the need.
+constexpr size_t kScratchSpare = size_t{64} << 20;
 
 // Query rows of a sequence (per kv head) up to which the streaming kernel takes it. One more and
 // it would read the pages twice over: 28 rows on 4000 to 6000 positions of 32 agents take 66 us
@@ -557,14 +519,15 @@ td_status run_chunk_attention(td_ctx* c, const td_chunks* ch, const PoolDev& poo
       need = std::max(need, l.parts + (l.a.direct ? 0 : l.part_rows * (D + 2)));
     }
   }
-  if ((s = chunk_scratch(c, need, st)) != TD_OK) return s;
+  const size_t more = std::min(2 * c->chunk.cap, need + kScratchSpare);
+  if ((s = grow(c, &c->chunk, need, more, st)) != TD_OK) return s;
   for (const auto& next : launches) {
     Launch& l = *next;
-    l.a.part_o = c->d_chunk + l.parts;
+    l.a.part_o = c->chunk.p + l.parts;
     l.a.part_ml = l.a.direct ? nullptr : l.a.part_o + l.part_rows * D;
     if (l.group == 2) {
-      l.a.dense = reinterpret_cast<uint16_t*>(c->d_chunk);
-      l.a.dense_scale = c->d_chunk + l.scales;
+      l.a.dense = reinterpret_cast<uint16_t*>(c->chunk.p);
+      l.a.dense_scale = c->chunk.p + l.scales;
       if (!row_map(a.g.E, l.a.dense, static_cast<int64_t>(l.planes), 128, &map) ||
           launch_expand(l.a, l.list, l.dense, kind, st) != cudaSuccess)
         return TD_ERR_CUDA;

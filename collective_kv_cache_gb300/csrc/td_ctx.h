@@ -5,10 +5,22 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <new>
 #include <vector>
 
 #include "td.h"
 #include "td_internal.h"
+
+namespace td {
+
+// A context's buffer that grows with its calls.
+struct Scratch {
+  float* p = nullptr;
+  size_t cap = 0;                   // its size in floats
+  bool kept = false;                // a captured call has used it
+};
+
+}  // namespace td
 
 struct td_ctx {
   td_shape shape;
@@ -64,14 +76,11 @@ struct td_ctx {
                                     // pick_master's counter, spare
   int64_t* d_bound = nullptr;
   uint32_t* d_err = nullptr;
-  float* d_attn = nullptr;          // attention partials, grown on demand
-  size_t attn_cap = 0;              // its size in floats
+  td::Scratch attn;                 // attention partials
   uint32_t attn_tx_pad = 0;         // fault injection: bytes the attention never receives
-  float* d_chunk = nullptr;         // chunk attention's partial results, grown on demand
-  size_t chunk_cap = 0;             // its size in floats
-  bool chunk_kept = false;          // a captured call has used it
+  td::Scratch chunk;                // chunk attention's unfolded pages and partial results
   uint32_t chunk_launched = 0;      // its kernels that this context has launched, a bit each
-  std::vector<float*> old_chunk;    // outgrown ones that captured calls have used
+  std::vector<float*> outgrown;     // scratch that captured calls have used, and that was too small
   // pinned host words for results
   int64_t* h_words = nullptr;       // [4]
 };
@@ -97,6 +106,46 @@ inline bool capturing(cudaStream_t st) {
     return false;
   }
   return cs != cudaStreamCaptureStatusNone;
+}
+
+// Scratch of at least `need` floats, `more` of them where that is to be had. A buffer that a
+// captured call has used stays until the context goes, since the graph holds its address; any
+// other is freed when it is outgrown, after the stream's work (the context's earlier calls of
+// the group are ordered before this one). Inside a capture nothing can be allocated.
+inline td_status grow(td_ctx* c, Scratch* s, size_t need, size_t more, cudaStream_t st) {
+  if (need == 0) return TD_OK;
+  const bool captured = capturing(st);
+  if (need <= s->cap) {
+    s->kept |= captured;
+    return TD_OK;
+  }
+  if (captured) return TD_ERR_INVALID_ARG;
+  if (s->p && s->kept) {
+    try {
+      c->outgrown.reserve(c->outgrown.size() + 1);
+    } catch (const std::bad_alloc&) {
+      return TD_ERR_CUDA;
+    }
+  } else if (s->p) {
+    if (cudaStreamSynchronize(st) != cudaSuccess || cudaFree(s->p) != cudaSuccess) {
+      cudaGetLastError();
+      return TD_ERR_CUDA;
+    }
+    *s = Scratch{};
+  }
+  float* p = nullptr;
+  size_t cap = more > need ? more : need;
+  if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
+    cudaGetLastError();
+    cap = need;
+    if (cudaMalloc(&p, cap * sizeof(float)) != cudaSuccess) {
+      cudaGetLastError();
+      return TD_ERR_CUDA;
+    }
+  }
+  if (s->p) c->outgrown.push_back(s->p);
+  *s = Scratch{p, cap, false};
+  return TD_OK;
 }
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }

@@ -37,9 +37,9 @@ void free_ctx(td_ctx* c) {
   cudaFree(c->d_ints);
   cudaFree(c->d_bound);
   cudaFree(c->d_err);
-  cudaFree(c->d_attn);
-  cudaFree(c->d_chunk);
-  for (float* p : c->old_chunk) cudaFree(p);
+  cudaFree(c->attn.p);
+  cudaFree(c->chunk.p);
+  for (float* p : c->outgrown) cudaFree(p);
   if (c->h_stage) cudaFreeHost(c->h_stage);
   if (c->h_words) cudaFreeHost(c->h_words);
   if (c->stage_done) cudaEventDestroy(c->stage_done);
@@ -360,7 +360,7 @@ td_status run_attention(td_ctx* c, const td_round* r, const td_diff_store* store
     }
   }
   const int split = nl - n_short;
-  // partials of the largest agent list; grown once, after the work that used them
+  // partials of the largest agent list
   int64_t most = 0;
   for (int x0 = 0; x0 < n_list; x0 += kMaxListAgents) {
     int64_t sum = 0;
@@ -388,14 +388,7 @@ td_status run_attention(td_ctx* c, const td_round* r, const td_diff_store* store
     maps.master_k = maps.master_v = maps.val_k = maps.val_v = maps.pool;
   }
   const size_t need = static_cast<size_t>(most) * H * kAttnGMax * (D + 2);
-  if (need > c->attn_cap) {
-    if (cudaStreamSynchronize(st) != cudaSuccess) return TD_ERR_CUDA;
-    cudaFree(c->d_attn);
-    c->d_attn = nullptr;
-    c->attn_cap = 0;
-    if (cudaMalloc(&c->d_attn, need * sizeof(float)) != cudaSuccess) return TD_ERR_CUDA;
-    c->attn_cap = need;
-  }
+  if ((s = grow(c, &c->attn, need, need, st)) != TD_OK) return s;
   for (int x0 = 0; x0 < n_list; x0 += kMaxListAgents) {
     AttnList L;
     L.n = n_list - x0 < kMaxListAgents ? n_list - x0 : kMaxListAgents;
@@ -414,8 +407,8 @@ td_status run_attention(td_ctx* c, const td_round* r, const td_diff_store* store
                           static_cast<int64_t>(L.base2[L.n]) * n_short * H;
     if (units > INT32_MAX) return TD_ERR_INVALID_ARG;
     a.x0 = x0;
-    a.part_o = c->d_attn;
-    a.part_ml = c->d_attn + static_cast<size_t>(units) * kAttnGMax * D;
+    a.part_o = c->attn.p;
+    a.part_ml = c->attn.p + static_cast<size_t>(units) * kAttnGMax * D;
     if (launch_attention(a, L, maps, store == nullptr, st) != cudaSuccess) return TD_ERR_CUDA;
   }
   return note_use(c, st);

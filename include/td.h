@@ -315,8 +315,10 @@ td_status td_check_select_noalloc(const td_shape* shape, const td_round* round,
  *   lse       DEVICE float [layer_end-layer_begin][n_list][n_q_heads], or NULL
  * Head dims 64 and 128 (else TD_ERR_INVALID_ARG). The store must be in device memory (a
  * store kept in host memory is refused with TD_ERR_INVALID_ARG: restore from it instead).
- * The context owns the partial results' scratch and grows it when a call needs more (synchronising the stream first). An
- * unmapped history page sets TD_ERR_UNMAPPED_PAGE in the error word; a bounded wait on the
+ * The context owns the partial results' scratch and grows it when a call needs more
+ * (synchronising the stream first; a buffer that a captured call has used stays until the
+ * context goes). A call made in a stream capture must find it large enough: make the call once
+ * before capturing it (else TD_ERR_INVALID_ARG). An unmapped history page sets TD_ERR_UNMAPPED_PAGE in the error word; a bounded wait on the
  * copy engine that runs out sets TD_ERR_DEVICE_TIMEOUT (that unit's result is not written). */
 td_status td_fused_attention(td_ctx* ctx, const td_round* round, const td_diff_store* store,
                              const td_paged* pool, const int32_t* agents, int32_t n_list,
