@@ -15,10 +15,10 @@
 // 2 x 2^14 exponentials 1024 (32 a cycle): the products bound D = 128, both D = 64.
 //
 // Measured on one GB300: two chunks of 2048 tokens after 8192, 28 query heads on 4, D = 128,
-// take 349 us = 1.55 PFLOP/s (81% of what a large library product reaches), the tensor pipe
+// take 350 us = 1.54 PFLOP/s (80% of what a large library product reaches), the tensor pipe
 // busy for 73% of the cycles; ragged spans of 1 to 301 tokens after 6000 to 13000, 40 heads on
-// 8, reach 1.33 (whatever the page size from 8 on). Under a window of 1024 at D = 64 a block has
-// 11 KV tiles, the first and last of them partly masked: 315 us = 597 TFLOP/s of visible work
+// 8, reach 1.31 (whatever the page size from 8 on). Under a window of 1024 at D = 64 a block has
+// 11 KV tiles, the first and last of them partly masked: 314 us = 599 TFLOP/s of visible work
 // (64 heads on 8, four chunks of 1500 to 4097), a quarter of it the block's start and end and
 // the rest bound by the softmax's issue. e4m3 pages, four chunks of 500 to 700 after 4096 to
 // 8192, 40 heads on 8, D = 128: 262 us = 1.25 PFLOP/s with the pages unfolded first; converted

@@ -162,17 +162,19 @@ constexpr size_t kScratchSpare = size_t{64} << 20;
 
 // Query rows of a sequence (per kv head) up to which the streaming kernel takes it. One more and
 // it would read the pages twice over: 28 rows on 4000 to 6000 positions of 32 agents take 66 us
-// on the tensor-core kernel and 146 on the streaming one (D = 128; 44 and 83 at D = 64, int8
-// pages 114 and 116), 56 rows 67 and 257. Short contexts lean the other way by a little (30
-// rows on 1000 positions: 15.1 and 13.1 us), and up to 16 rows the tensor-core kernel's tile of
-// 128 is mostly empty.
+// on the tensor-core kernel and 143 on the streaming one (D = 128; 44 and 87 at D = 64), 56 rows 67
+// and 271, 30 rows on 1000 positions 17 and 32. Over 8-bit pages two passes come out even: 28 rows
+// 117 and 119 us over int8, 118 and 114 over e4m3 (D = 64: 90 and 78, 78 and 72; 30 rows on 1000
+// positions 26 and 28, 24 and 27), 56 rows 117 and 218. Up to 16 rows the tensor-core kernel's
+// tile of 128 is mostly empty.
 constexpr int kFewRows = 16;
 
 // Over 8-bit pages the tensor-core kernel converts the codes itself for up to two tiles of query
 // rows (of 256); from three on they are unfolded once, before it. Two tiles of 480 rows on 12000
-// positions of 16 agents take 254 us converted in the kernel and 266 unfolded (int8, 4 kv heads,
-// D = 128; 2000 positions of 8: 43 and 47), 960 rows 559 and 419 (54 and 51), 2560 rows 1240
-// and 888 (157 and 120). At D = 64 the crossing is the same.
+// positions of 16 agents take 259 us converted in the kernel and 269 unfolded (int8, 4 kv heads,
+// D = 128; 2000 positions of 8: 42.5 and 43.4; e4m3 242 and 260), 960 rows 564 and 420 (53 and 46;
+// 529 and 403), 2560 rows 1093 and 795 (129 and 104; 1021 and 735). At D = 64 the crossing is the
+// same.
 constexpr int kOwnRows = 512;
 // The unfolded copy of one launch, at most: sequences that would pass it go to the next one, a
 // sequence that is longer by itself is converted in the kernel.

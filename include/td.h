@@ -426,8 +426,14 @@ td_status td_dequantise_read(td_ctx* ctx, const td_chunks* chunks, const td_page
  * Positions that no token of the chunk sees are not read: their pages may be unmapped.
  * Positions that a token does not see have no part in its row, whatever they hold. An
  * unmapped page within sight sets TD_ERR_UNMAPPED_PAGE and its positions are left out; a row
- * left with none is zeros with lse = -infinity. A NaN that a token sees makes its row NaN.
- * Scores, softmax and sums are float32.
+ * left with none is zeros with lse = -infinity. A NaN in K that a token sees makes its row NaN;
+ * a NaN or an infinity in V makes that element of the row a NaN or infinite, however small
+ * the weight, and changes no other element.
+ * Scores (sums of exact products), softmax and sums are float32: q . K and the scores have to
+ * stay within it, and sums of V under weights of at most 1. The weights are rounded before
+ * they meet V: to 16 bits in chunks of up to 16 query rows (tokens x n_q_heads / H), and in
+ * chunks of more to bf16, 2^-8 of a weight at most (pages that are no multiple of 8 tokens: 16
+ * bits throughout); lse is taken before that.
  *   q     DEVICE bf16 [layer_end-layer_begin][T][n_q_heads][D], rotated, 16-byte aligned
  *   out   DEVICE bf16, as q
  *   lse   DEVICE float [layer_end-layer_begin][T][n_q_heads], or NULL
@@ -446,6 +452,11 @@ td_status td_chunk_attention(td_ctx* ctx, const td_chunks* chunks, const td_page
 
 /* The same over 8-bit pages: K and V are code * scale, with any scale. (The e4m3 codes that
  * stand for a NaN, which td_quantise_append does not write, have no defined value in sight.)
+ * A NaN scale that a token sees, K's or V's, makes its row NaN. q . code has to stay within
+ * float32 too. In chunks of up to 512 query rows (and longer ones whose unfolded copy, below,
+ * would be too large) the queries go through f16, each row under a power of two of its own:
+ * elements keep their 8 bits down to 2^-28 of the row's largest, fewer below, and are 0 under
+ * 2^-39 of it.
  * For long chunks the visible pages are first unfolded into the context's scratch, at most
  * 2^30 bytes of it at a time, beside the partial results. */
 td_status td_chunk_attention_q8(td_ctx* ctx, const td_chunks* chunks, const td_paged8* cache,
