@@ -22,7 +22,7 @@ namespace td {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = kTablesThreads;
 constexpr int kWarpsT = kThreads / 32;
 
 // Sums over requests, none past kMany: a sum of numbers that are not negative stays there once it is
@@ -136,12 +136,13 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   full = full || all.tokens > static_cast<uint32_t>(A.max_slots) || left < 0 || left > A.capacity ||
          max(max(all.items, all.tokens), max(all.taken, all.given)) >= kMany;
   const bool ok = !bad && !full;
-  const int gthread = blockIdx.x * kThreads + tid, gthreads = gridDim.x * kThreads;
+  const TablesIndex gthread = blockIdx.x * kThreads + tid, gthreads = gridDim.x * kThreads;
+  const TablesIndex max_slots = static_cast<TablesIndex>(A.max_slots);
   if (!ok) {
     if (gthread == 0) atomicOr(A.err, err_bit(bad ? TD_ERR_INVALID_ARG : TD_ERR_CAPACITY));
     if (A.token_start && blockIdx.x == 0)
       for (int x = tid; x <= n; x += kThreads) A.token_start[x] = 0;
-    for (int i = gthread; i < A.max_slots; i += gthreads) A.slots[i] = -1;
+    for (TablesIndex i = gthread; i < max_slots; i += gthreads) A.slots[i] = -1;
     pdl_trigger();
     return;
   }
@@ -155,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   if (tid == 0) s_tok[n] = static_cast<int32_t>(all.tokens);
   __syncthreads();
   pdl_trigger();
-  const int items = static_cast<int>(all.items), given = static_cast<int>(all.given);
-  const int taken = static_cast<int>(all.taken), tokens = static_cast<int>(all.tokens);
+  const TablesIndex items = all.items, taken = all.taken, tokens = all.tokens;
+  const int given = static_cast<int>(all.given);
   auto entry = [&](int x, int lp) {
     return A.bt + static_cast<int64_t>(A.row ? A.row[x] : x) * A.max_lp + lp;
   };
@@ -171,10 +172,10 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   const int sub = lane & (gs - 1), group = lane / gs;
   bool hole = false;
   // a lane finds a page, then the warp writes the slots of its 32
-  for (int i0 = gthread - lane; i0 < items; i0 += gthreads) {
+  for (TablesIndex i0 = gthread - lane; i0 < items; i0 += gthreads) {
     int page = -1, lo = 0, hi = 0, to_slot = 0;       // its new tokens [lo, hi), and slot 0's place
     if (i0 + lane < items) {
-      const int i = i0 + lane, x = find(s_item, n, i);
+      const int i = static_cast<int>(i0 + lane), x = find(s_item, n, i);
       const int len = A.len[x], end = len + A.add[x];
       const int lp = len / P + i - s_item[x], have = (len + P - 1) / P;
       int32_t* to = entry(x, lp);
@@ -197,9 +198,9 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
       if (lp >= have) *to = page;
       lo = max(len - lp * P, 0);
       hi = min(end - lp * P, P);
-      to_slot = s_tok[x] + lp * P - len;
+      to_slot = s_tok[x] + (lp * P - len);
     }
-    const int most_here = min(32, items - i0);
+    const int most_here = static_cast<int>(min(32u, items - i0));
     for (int k = group; k - group < most_here; k += 32 / gs) {       // (as many rounds for every lane)
       const int k_page = __shfl_sync(0xFFFFFFFFu, page, k), k_to = __shfl_sync(0xFFFFFFFFu, to_slot, k);
       const int k_lo = __shfl_sync(0xFFFFFFFFu, lo, k), k_hi = __shfl_sync(0xFFFFFFFFu, hi, k);
@@ -207,17 +208,17 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
         if (s >= k_lo) A.slots[k_to + s] = k_page < 0 ? -1 : k_page * P + s;
     }
   }
-  for (int i = taken + gthread; i < given; i += gthreads) {
-    int32_t* from = returned(i);
+  for (TablesIndex i = taken + gthread; i < all.given; i += gthreads) {
+    int32_t* from = returned(static_cast<int>(i));
     const int page = *from;
     hole |= page < 0 || page >= A.num_pages;
-    A.pages[count + given - 1 - i] = page;
+    A.pages[count + (given - 1 - static_cast<int>(i))] = page;
     *from = -1;
   }
   if (hole) atomicOr(A.err, err_bit(TD_ERR_UNMAPPED_PAGE));
   if (A.token_start && blockIdx.x == 0)
     for (int x = tid; x <= n; x += kThreads) A.token_start[x] = s_tok[x];
-  for (int i = tokens + gthread; i < A.max_slots; i += gthreads) A.slots[i] = -1;
+  for (TablesIndex i = tokens + gthread; i < max_slots; i += gthreads) A.slots[i] = -1;
   // every CTA has read the lengths and the count: the last one replaces them
   __syncthreads();
   if (tid == 0) {
@@ -232,10 +233,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
 }
 
 cudaError_t launch_tables(const TablesArgs& a, int sm_count, cudaStream_t st) {
-  // a thread for every page that can be touched, a CTA for 2 requests (which may give back many
-  // pages), up to four an SM
-  const int want = max((a.max_slots / a.P + a.n) / kThreads + 1, a.n / 2 + 1);
-  const unsigned grid = static_cast<unsigned>(min(want, 4 * sm_count));
+  const unsigned grid = tables_grid(a, sm_count);
   const size_t smem = (static_cast<size_t>(a.n + 1) * 4 + (a.max_rows + 31) / 32) * 4;
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(

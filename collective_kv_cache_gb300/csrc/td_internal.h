@@ -278,6 +278,18 @@ struct TablesArgs {
 };
 cudaError_t launch_tables(const TablesArgs& a, int sm_count, cudaStream_t st);
 
+constexpr int kTablesThreads = 256;
+// What the loops over pages and slots count with: counts are below 2^31 and a step of the grid below
+// 2^30, so the index that ends a loop fits.
+typedef uint32_t TablesIndex;
+// Blocks: a thread for every page that can be touched, a block for 2 requests (which may give back
+// many pages), up to four an SM.
+inline unsigned tables_grid(const TablesArgs& a, int sm_count) {
+  const int64_t pages = static_cast<int64_t>(a.max_slots) / a.P + a.n;
+  const int64_t want = pages / kTablesThreads > a.n / 2 ? pages / kTablesThreads + 1 : a.n / 2 + 1;
+  return static_cast<unsigned>(want < 4 * sm_count ? want : 4 * sm_count);
+}
+
 struct SlotArgs {
   Geom g;
   Cache4Dev cache;

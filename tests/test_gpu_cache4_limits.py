@@ -1,0 +1,67 @@
+"""The calls over 4-bit pages and device lengths at the ends of their ranges: sizes, scales and
+queries where index arithmetic or precision could give out."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def td():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a GPU")
+    from collective_kv_cache_gb300 import build
+    build.build()
+    from collective_kv_cache_gb300 import td as _td
+    return _td
+
+
+def _ctx(td, H=1, D=64, P=16, L=1, rows=8):
+    return td.Context(td.td_shape(L, H, D, P, 16, 1e6), rows, 1, 1)
+
+
+def _stream():
+    return torch.cuda.current_stream().cuda_stream
+
+
+def _errors(td, ctx):
+    return td.td_get_error(ctx.handle, _stream())
+
+
+def _dev(a):
+    return torch.tensor(np.asarray(a, dtype=np.int32), device="cuda")
+
+
+# ------------------------------------------------------------------------------ tables
+@pytest.mark.parametrize("met", [True, False])
+@pytest.mark.parametrize("max_slots", [2 ** 31 - 1, 2 ** 31 - 155000])
+def test_the_largest_slot_map(td, max_slots, met):
+    """Every slot past the tokens' is -1, in a call that is met and in one that is not; nothing before
+    or behind the map is written."""
+    guard = 1 << 18
+    if torch.cuda.mem_get_info()[0] < 4.5 * max_slots:
+        pytest.skip("the slot map does not fit this GPU's free memory")
+    mem = torch.full((max_slots + 2 * guard,), 7, dtype=torch.int32, device="cuda")
+    slots = mem[guard:guard + max_slots]
+    ctx = _ctx(td, P=1, rows=2)
+    lens, bt = _dev([2, 0]), torch.full((2, 8), -1, dtype=torch.int32, device="cuda")
+    bt[0, :2] = _dev([5, 3])
+    pages, count = _dev([0, 1, 2, 4]), _dev([4])
+    start = torch.full((3,), -5, dtype=torch.int32, device="cuda")
+    add = _dev([1, 2 if met else 4])
+    td.td_update_tables(ctx.handle, td.make_requests(lens), add.data_ptr(), bt.data_ptr(), 8,
+                        td.make_page_list(pages, count, 6), start.data_ptr(), slots.data_ptr(), max_slots,
+                        _stream())
+    e = 0 if met else td.TD_ERR_CAPACITY
+    assert _errors(td, ctx) == (e, 1 << e if e else 0)
+    assert bool((mem[:guard] == 7).all()) and bool((mem[guard + max_slots:] == 7).all())
+    tokens = [4, 2, 1] if met else [-1, -1, -1]
+    assert slots[:3].tolist() == tokens
+    assert start.tolist() == ([0, 1, 3] if met else [0, 0, 0])
+    assert lens.tolist() == ([3, 2] if met else [2, 0])
+    for part in slots[3:].split(1 << 28):
+        assert bool((part == -1).all())
