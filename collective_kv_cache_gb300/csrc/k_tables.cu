@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   auto returned = [&](int i) {
     const int x = find(s_give, n, i);
     const int end = A.len[x] + A.add[x];
-    return entry(x, (end + P - 1) / P + i - s_give[x]);
+    return entry(x, pages_of(end, P) + i - s_give[x]);
   };
   int gs = 1;                              // lanes that write a page's slots
   while (gs < P && gs < 32) gs *= 2;
@@ -177,7 +177,7 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
     if (i0 + lane < items) {
       const int i = static_cast<int>(i0 + lane), x = find(s_item, n, i);
       const int len = A.len[x], end = len + A.add[x];
-      const int lp = len / P + i - s_item[x], have = (len + P - 1) / P;
+      const int lp = len / P + i - s_item[x], have = pages_of(len, P);
       int32_t* to = entry(x, lp);
       if (lp < have) {
         page = *to;

@@ -282,6 +282,11 @@ constexpr int kTablesThreads = 256;
 // What the loops over pages and slots count with: counts are below 2^31 and a step of the grid below
 // 2^30, so the index that ends a loop fits.
 typedef uint32_t TablesIndex;
+// Pages of P positions that `len` positions take (neither is negative; the sum may pass 2^31).
+TD_HD inline int pages_of(int len, int P) {
+  return static_cast<int>((static_cast<uint32_t>(len) + static_cast<uint32_t>(P) - 1u) /
+                          static_cast<uint32_t>(P));
+}
 // Blocks: a thread for every page that can be touched, a block for 2 requests (which may give back
 // many pages), up to four an SM.
 inline unsigned tables_grid(const TablesArgs& a, int sm_count) {

@@ -19,5 +19,6 @@ int host_tables_goes_on(int64_t i, int64_t step, int64_t end) {
   at += static_cast<TablesIndex>(step);
   return at < static_cast<TablesIndex>(end);
 }
+int host_pages_of(int len, int P) { return pages_of(len, P); }
 
 }  // extern "C"

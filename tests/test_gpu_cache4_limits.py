@@ -65,3 +65,23 @@ def test_the_largest_slot_map(td, max_slots, met):
     assert lens.tolist() == ([3, 2] if met else [2, 0])
     for part in slots[3:].split(1 << 28):
         assert bool((part == -1).all())
+
+
+@pytest.mark.parametrize("P", [2 ** 30 + 7, 2 ** 31 - 1])
+def test_pages_past_2_to_30_positions(td, P):
+    """One page holds whatever a request may hold: the second call takes none, the last gives it back."""
+    ctx = _ctx(td, P=P, rows=1)
+    lens, bt = _dev([0]), _dev([[-1, -1]])
+    mem, count = _dev([-9, -9, 0, -9, -9]), _dev([1])
+    slots = torch.empty(5, dtype=torch.int32, device="cuda")
+    held = 0
+    for add, free in ((3, 0), (2, 0), (-1, 0), (-4, 1)):
+        a = _dev([add])
+        td.td_update_tables(ctx.handle, td.make_requests(lens), a.data_ptr(), bt.data_ptr(), 2,
+                            td.make_page_list(mem[2:3], count, 1), None, slots.data_ptr(), 5, _stream())
+        assert _errors(td, ctx) == (0, 0)
+        new = list(range(held, held + add))
+        held += add
+        assert slots.tolist() == new + [-1] * (5 - len(new))
+        assert lens.tolist() == [held] and count.tolist() == [free] and mem.tolist() == [-9, -9, 0, -9, -9]
+        assert bt.tolist() == [[-1 if free else 0, -1]]

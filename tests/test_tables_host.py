@@ -44,3 +44,9 @@ def test_no_index_is_below_the_end_again_once_it_has_passed_it(lib, end):
             last = thread + (end - 1 - thread) // step * step
             assert not lib.host_tables_goes_on(last, step, end)
         assert not lib.host_tables_goes_on(end, thread, end)
+
+
+@pytest.mark.parametrize("P", [1, 3, 16, 2 ** 30 - 1, 2 ** 30, 2 ** 30 + 1, MOST - 1, MOST])
+def test_pages_of_the_longest_requests_and_the_largest_pages(lib, P):
+    for length in (0, 1, 2, 5, 16, 2 ** 30 - 2, 2 ** 30 - 1):
+        assert lib.host_pages_of(length, P) == -(-length // P)
