@@ -232,12 +232,20 @@ __global__ void __launch_bounds__(kThreads) tables_kernel(const __grid_constant_
   if (tid == 0) *A.count = static_cast<int32_t>(left);
 }
 
+// Dynamic shared memory for n requests of a table of max_rows rows.
+static constexpr size_t tables_smem(int n, int max_rows) {
+  return (static_cast<size_t>(n + 1) * 4 + (max_rows + 31) / 32) * 4;
+}
+
 cudaError_t launch_tables(const TablesArgs& a, int sm_count, cudaStream_t st) {
   const unsigned grid = tables_grid(a, sm_count);
-  const size_t smem = (static_cast<size_t>(a.n + 1) * 4 + (a.max_rows + 31) / 32) * 4;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  const size_t smem = tables_smem(a.n, a.max_rows);
+  // (what a block may have unasked covers the static part too; what is asked for holds for the device,
+  // whoever calls, so it is the same for every call)
+  if (smem > 47 * 1024) {
+    const cudaError_t e =
+        cudaFuncSetAttribute(tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(tables_smem(kMaxAgents, kMaxAgents)));
     if (e != cudaSuccess) return e;
   }
   return launch_after(tables_kernel, grid, kThreads, smem, st, a);

@@ -443,7 +443,7 @@ td_status td_ctx_create(const td_shape* shape, int32_t max_agents, int32_t max_b
     return TD_ERR_INVALID_ARG;
   const int64_t E = static_cast<int64_t>(s.n_kv_heads) * s.head_dim;
   if (E > 2048) return TD_ERR_INVALID_ARG;  // a tile holds 16 rows of at most 2048 elements
-  if (max_agents < 1 || max_blocks < 1 || max_shared < 1 || max_agents > 4096 ||
+  if (max_agents < 1 || max_blocks < 1 || max_shared < 1 || max_agents > kMaxAgents ||
       max_shared > (1 << 22))
     return TD_ERR_INVALID_ARG;
   const int max_nb = (max_shared + kDiffBlock - 1) / kDiffBlock;

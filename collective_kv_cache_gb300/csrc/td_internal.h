@@ -258,6 +258,8 @@ struct Cache4Dev {
   uint32_t* word;
 };
 
+constexpr int kMaxAgents = 4096;       // a context's, at most
+
 // Block tables and slots from lengths (k_tables.cu).
 struct TablesArgs {
   int n, max_rows;           // requests; rows that the table may have

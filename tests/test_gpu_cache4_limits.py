@@ -2,12 +2,17 @@
 queries where index arithmetic or precision could give out."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -85,3 +90,11 @@ def test_pages_past_2_to_30_positions(td, P):
         assert slots.tolist() == new + [-1] * (5 - len(new))
         assert lens.tolist() == [held] and count.tolist() == [free] and mem.tolist() == [-9, -9, 0, -9, -9]
         assert bt.tolist() == [[-1 if free else 0, -1]]
+
+
+@pytest.mark.parametrize("what", ["sizes", "threads"])
+def test_many_requests_in_a_process_of_their_own(td, what):
+    """Whatever sizes came before, and whatever another thread asks for (tests/tables_many.py)."""
+    done = subprocess.run([sys.executable, "-m", "tests.tables_many", what], cwd=ROOT, capture_output=True,
+                          text=True, timeout=300)
+    assert done.returncode == 0 and done.stdout.strip() == "ok", done.stdout + done.stderr
