@@ -6,7 +6,7 @@
 // nearest quotients by the exact residual x - n s, as the 8-bit pages' (k_quant.cu).
 // e2m1, a quarter of a row: s = the least power of two with amax <= 6 s, so x / s is exact, and the
 // conversion instruction rounds it to the nearest code.
-// Reading back: bf16((code - z) s), or code * s, which is a bf16.
+// Reading back: bf16((code - z) s), or code * s, which is a bf16 (and NaN in a quarter whose byte is 255).
 //
 // Both kernels move 2.53 bytes an element once (D = 128). A lane of the write takes 16 elements (32
 // bytes in, 8 out), of int4's, which costs more a row, 32; of the read two vectors of 8, half a row
@@ -311,8 +311,6 @@ slots_kernel(const __grid_constant__ SlotArgs A) {
         for (int i = 0; i < kIn; ++i) {
           uint4 out = values8<kKind>(cw[u][i], wd[u], part / (kLanes / 2) + 2 * i);
           if (row[u] == -2) out = make_uint4(0u, 0u, 0u, 0u);
-          else if (kKind == kCacheE2m1 && largest_byte(wd[u]) == 255u)
-            out = make_uint4(0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u, 0x7FC07FC0u);
           st16(to + i * kLanes * 8, out);
         }
       }

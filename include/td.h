@@ -566,8 +566,8 @@ td_status td_quantise_slots(td_ctx* ctx, const int32_t* slots, int32_t n_slots,
                             int32_t layer_begin, int32_t layer_end, void* stream);
 
 /* Read slots of 4-bit pages back as dense bf16 rows: the element's value rounded to nearest even
- * (E2M1's are bf16 already). Rows of a slot -1 stay as they are; those of any other slot that is
- * none of the pool's become zeros and set TD_ERR_UNMAPPED_PAGE.
+ * (E2M1's are bf16 already; a byte 255 makes its own quarter NaN). Rows of a slot -1 stay as they
+ * are; those of any other slot that is none of the pool's become zeros and set TD_ERR_UNMAPPED_PAGE.
  *   k_out, v_out   DEVICE bf16 [layer_end-layer_begin][n_slots][H][D], 16-byte aligned */
 td_status td_dequantise_slots(td_ctx* ctx, const int32_t* slots, int32_t n_slots,
                               const td_paged4* cache, int32_t layer_begin, int32_t layer_end,

@@ -2,6 +2,7 @@
 queries where index arithmetic or precision could give out."""
 from __future__ import annotations
 
+import math
 import os
 import subprocess
 import sys
@@ -10,6 +11,8 @@ import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
+
+from tests import cache4kit as k4
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -98,3 +101,32 @@ def test_many_requests_in_a_process_of_their_own(td, what):
     done = subprocess.run([sys.executable, "-m", "tests.tables_many", what], cwd=ROOT, capture_output=True,
                           text=True, timeout=300)
     assert done.returncode == 0 and done.stdout.strip() == "ok", done.stdout + done.stderr
+
+
+# --------------------------------------------------------------------------- slots: reading
+@pytest.mark.parametrize("D", [64, 128])
+def test_a_quarter_that_is_nan_reads_back_as_nan_and_the_others_do_not(td, D):
+    """e2m1: a byte 255 stands for NaN in its own quarter; the other quarters have their values."""
+    H, P, pages = 3, 5, 8
+    ctx = _ctx(td, H, D, P)
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    codes = torch.randint(0, 256, (1, 2, pages, H, P, D // 2), generator=gen, device="cuda",
+                          dtype=torch.uint8)
+    byte = torch.randint(120, 130, (1, 2, pages, H, P, 4), generator=gen, device="cuda")
+    byte[torch.rand(byte.shape, generator=gen, device="cuda") < 0.3] = 255
+    word = k4.words(byte, "e2m1")
+    bt = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    T = pages * P
+    slots = torch.randperm(T, generator=gen, device="cuda").int()
+    ko, vo = (torch.empty((1, T, H, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    td.td_dequantise_slots(ctx.handle, slots.data_ptr(), T, td.make_paged4(codes, word, bt, "e2m1"), 0, 1,
+                           ko.data_ptr(), vo.data_ptr(), _stream())
+    assert _errors(td, ctx) == (0, 0)
+    grid = torch.tensor(k4.E2M1 + tuple(-x for x in k4.E2M1), dtype=torch.float64, device="cuda")
+    want = grid[k4.unpack(codes).long()].unflatten(-1, (4, -1)) * 2.0 ** (byte[..., None].double() - 127)
+    want = torch.where(byte[..., None] == 255, math.nan, want).flatten(-2)[0]    # [2][pages][H][P][D]
+    s = slots.long()
+    for got, val in zip((ko, vo), want):
+        val = val[s // P, :, s % P]
+        assert bool((got.isnan() == val.isnan()[None]).all()) and bool(got.isnan().any(-1).any())
+        assert torch.equal(got.nan_to_num(9.0), val.to(torch.bfloat16)[None].nan_to_num(9.0))
