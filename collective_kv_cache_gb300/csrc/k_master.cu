@@ -82,10 +82,12 @@ cudaError_t launch_pick_master(const int32_t* sel, int N, int S, int B, int k, i
   const int nb = (S + B - 1) / B;
   const int nbw = (nb + 31) / 32;
   const size_t smem = ((static_cast<size_t>(N) * nbw * 4 + 7) & ~size_t(7)) + 8 * static_cast<size_t>(N);
-  if (smem > 48 * 1024) {
+  // (what a block may have unasked covers the static part too; what is asked for holds for the device,
+  // whoever calls, so it is a context's largest, 160 KiB and the masks rounded up to 8 bytes)
+  if (smem > 47 * 1024) {
     cudaError_t e = cudaFuncSetAttribute(pick_master_kernel,
                                          cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+                                         160 * 1024 + 8);
     if (e != cudaSuccess) return e;
   }
   const int threads = k >= 512 ? 1024 : 256;
