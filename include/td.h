@@ -577,8 +577,8 @@ td_status td_dequantise_slots(td_ctx* ctx, const int32_t* slots, int32_t n_slots
  * NaN (E2M1: b = 255 in any of the row's four bytes); one that is infinite has no defined value.
  * The scores have to stay within float32, 2^8 times the sums of V too, elements of q below 2^110 and K's
  * scales below 2^112. Chunks of up to 48 query rows (len * n_q_heads / H) go through f16. The queries,
- * each row under a power of two of its own: elements keep their 8 bits down to 2^-20 of the row's
- * largest (E2M1 2^-24), fewer below, and are 0 under 2^-28 of it (2^-32). The weights times V's
+ * each row under a power of two of its own: elements keep their 8 bits down to 2^-19 of the row's
+ * largest (E2M1 2^-23), fewer below, and may be 0 from 2^-27 of it down (2^-31). The weights times V's
  * scales: rounded by 2^-11 at most down to 2^-20 of the largest scale in their part of the context (a
  * weight of 1 being that of the largest score), 0 under 2^-31 of it. E2M1: a byte b = 0 counts as a
  * scale of 0, and so does a quarter of V whose scale is 2^-27 of the row's largest or less. Longer

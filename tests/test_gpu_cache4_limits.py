@@ -130,3 +130,47 @@ def test_a_quarter_that_is_nan_reads_back_as_nan_and_the_others_do_not(td, D):
         val = val[s // P, :, s % P]
         assert bool((got.isnan() == val.isnan()[None]).all()) and bool(got.isnan().any(-1).any())
         assert torch.equal(got.nan_to_num(9.0), val.to(torch.bfloat16)[None].nan_to_num(9.0))
+
+
+# --------------------------------------------------------------------------------- attention
+def _attend(td, b, codes, word, fmt, q, scale, decode=False):
+    """Output and log-sum-exp of the batch's chunks (decode: its tokens) over all layers."""
+    ctx = _ctx(td, b.H, b.D, b.P, b.L, rows=b.n_agents)
+    out = torch.full(q.shape, math.nan, dtype=torch.bfloat16, device="cuda")
+    z = torch.full(q.shape[:3], math.nan, device="cuda")
+    pages = td.make_paged4(codes, word, b.bt_t, fmt)
+    tail = (0, b.L, q.data_ptr(), q.shape[2], scale, 0, 0, out.data_ptr(), z.data_ptr(), _stream())
+    if decode:
+        td.td_decode_attention_q4(ctx.handle, td.make_requests(_dev([s + 1 for s in b.starts])), pages, *tail)
+    else:
+        td.td_chunk_attention_q4(ctx.handle, td.make_chunks(b.agents, b.starts, b.lens), pages, *tail)
+    assert _errors(td, ctx) == (0, 0)
+    return out, z
+
+
+@pytest.mark.parametrize("fmt", k4.FORMATS)
+def test_elements_of_a_query_far_below_its_largest(td, fmt):
+    """Elements of 8 bits keep them down to 2^-19 of their row's largest (e2m1 2^-23), and count for
+    something over 2^-27 (2^-31) of it: a query row a head, one small element each at another dim, its
+    largest where K is zero. Of one position the log-sum-exp is the score, q_small * k * scale."""
+    D, G, edge, last = 128, 40, 19 if fmt == "int4" else 23, 27 if fmt == "int4" else 31
+    b = k4.Batch([0], [1], 1, D, 16, seed=31)
+    code = torch.zeros(b.shape((D,)), dtype=torch.uint8, device="cuda")
+    code[..., :G] = 2                                  # int4: 2; e2m1: 1
+    if fmt == "int4":
+        word = k4.words(torch.ones(b.shape(), device="cuda"), fmt, torch.zeros(b.shape(), device="cuda"))
+        k = 2.0
+    else:
+        word, k = k4.words(torch.full(b.shape((4,)), 127, device="cuda"), fmt), 1.0
+    codes = k4.pack(code)
+    for small, low, high in ((255 / 128 * 2.0 ** -edge, 1 - 2.0 ** -12, 1 + 2.0 ** -12),
+                             (1.5 * 2.0 ** -last, 2.0 ** -8, 2.0)):
+        q = torch.zeros((1, 1, G, D), device="cuda")
+        i = torch.arange(G, device="cuda")
+        q[0, 0, i, i] = small
+        q[0, 0, i, G + i] = torch.where(i % 2 == 0, 1.0, -1.0)
+        scale = 2.0 ** edge
+        for decode in (False, True):
+            _, z = _attend(td, b, codes, word, fmt, q.to(torch.bfloat16), scale, decode)
+            ratio = z.double()[0, 0] / (small * k * scale)
+            assert bool(((ratio >= low) & (ratio <= high)).all()), ratio.tolist()
