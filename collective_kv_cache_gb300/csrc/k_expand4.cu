@@ -6,7 +6,8 @@
 // 2^(b - 127) is a bf16 as long as the row's four bytes are in [27, 227] (rows as
 // td_quantise_slots writes them, up to 2^100), and is stored multiplied, with the scale 1; in other
 // rows the quarters' powers of two relative to the largest go into the values and that one is the
-// scale. Nothing is rounded either way. Positions that no token of the chunk sees become zeros with
+// scale. Nothing is rounded either way, but a quarter 127 or more binades below its row's largest counts
+// as 0. Positions that no token of the chunk sees become zeros with
 // the scale 1, so that 0 * V is 0; a position of an unmapped page zeros with kHole.
 //
 // It reads 0.53 bytes and writes 2 an element, once: bound by memory. A CTA takes 32 positions of one

@@ -584,7 +584,8 @@ td_status td_dequantise_slots(td_ctx* ctx, const int32_t* slots, int32_t n_slots
  * scale of 0, and so does a quarter of V whose scale is 2^-27 of the row's largest or less. Longer
  * chunks (and shorter ones that a call takes with them) are computed as td_chunk_attention_q8's, those
  * of up to 512 query rows with the queries as f16; E2M1: a quarter of K whose scale is 2^-36 of the row's
- * largest or less then counts with fewer bits, or as 0. */
+ * largest or less then counts with fewer bits, or as 0; in those of more
+ * rows only one of 2^-127 of it or less counts as 0, K's or V's. */
 td_status td_chunk_attention_q4(td_ctx* ctx, const td_chunks* chunks, const td_paged4* cache,
                                 int32_t layer_begin, int32_t layer_end, const void* q,
                                 int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,

@@ -13,6 +13,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 from tests import cache4kit as k4
+from tests import chunkkit as ck
 
 pytestmark = pytest.mark.gpu
 ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
@@ -174,3 +175,98 @@ def test_elements_of_a_query_far_below_its_largest(td, fmt):
             _, z = _attend(td, b, codes, word, fmt, q.to(torch.bfloat16), scale, decode)
             ratio = z.double()[0, 0] / (small * k * scale)
             assert bool(((ratio >= low) & (ratio <= high)).all()), ratio.tolist()
+
+
+KINDS = {
+    # name: (starts, lens, H, G, D, P)
+    "token": ([700], [1], 1, 3, 128, 16),
+    "few": ([300, 90], [3, 2], 2, 7, 64, 16),
+    "converted": ([400, 90], [20, 30], 2, 7, 128, 16),
+    "converted_d64": ([700], [60], 2, 3, 64, 24),
+    "unfolded": ([300, 30], [150, 90], 1, 7, 128, 16),
+    "unfolded_d64": ([900], [520], 2, 2, 64, 24),
+    "unfolded_256": ([100, 0], [600, 500], 8, 4, 64, 16),
+}
+
+
+def _apart(b, gen, kv, base, most, word):
+    """Bytes of every row's quarters: base less 0 to most, one of them base itself."""
+    d = torch.randint(0, most + 1, b.shape((4,))[:1] + b.shape((4,))[2:], generator=gen, device="cuda")
+    d.scatter_(-1, torch.randint(0, 4, d.shape[:-1] + (1,), generator=gen, device="cuda"), 0)
+    word[:, kv] = k4.words(base - d, "e2m1")
+    return d
+
+
+@pytest.mark.parametrize("base", [127, 60, 235])
+@pytest.mark.parametrize("name", list(KINDS))
+def test_quarters_of_v_up_to_2_to_40_apart(td, name, base):
+    """Rows of V whose quarters lie 2^0 to 2^40 apart, around 1, from 2^-67 down to 2^-107, and from 2^108
+    down: chunks of up to 48 query rows count a quarter of 2^-27 of its row's largest or less as 0; the
+    others nothing."""
+    starts, lens, H, G, D, P = KINDS[name]
+    b = k4.Batch(starts, lens, H, D, P, seed=33)
+    codes, word, _, _ = b.random_pages("e2m1")
+    d = _apart(b, b.gen, 1, base, 40, word)
+    val = k4.values(codes, word, "e2m1").transpose(3, 4)
+    q = b.rows(1, b.T, H * G, D)
+    scale = D ** -0.5
+    got = _attend(td, b, codes, word, "e2m1", q, scale)
+    want = ck.attend(b, val[:, 0], val[:, 1], q)
+    few = max(lens) * G <= 48
+    tol, tol_lse = k4.bounds(want, q, word, "e2m1", scale, few, 0)
+    tol = tol - 1e-30 + 2.0 ** -132                     # (the bound's floor would hide the small ones)
+    if few:
+        # the quarters left out; and weights below f16's normal range, 2^-31 of every row's largest scale
+        off = (d >= 27)[..., None].expand(d.shape + (D // 4,)).flatten(-2).transpose(2, 3)
+        tol = tol + ck.attend(b, val[:, 0], torch.where(off, val[:, 1], 0.0), q)[2]
+        C = max(s + t for s, t in zip(starts, lens))
+        tol = tol + C * 2.0 ** -31 * ck.attend(b, val[:, 0], val[:, 1], q, scale=0.0)[2]
+    err = (got[0].double() - want[0]).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float((err / tol).max()))
+    assert bool(((got[1].double() - want[1]).abs() <= tol_lse).all())
+
+
+@pytest.mark.parametrize("base,up", [(26, 100), (235, -106), (228, -100), (40, 88)])
+@pytest.mark.parametrize("name", [n for n in KINDS if n != "few"])
+def test_quarters_of_k_at_the_ends_of_their_bytes(td, name, base, up):
+    """Rows of K whose bytes are at, or reach below, the least ones that an unfolded copy holds multiplied
+    out, or above the largest, up to 2^20 apart, under queries that bring the scores back to order 1."""
+    starts, lens, H, G, D, P = KINDS[name]
+    b = k4.Batch(starts, lens, H, D, P, seed=34)
+    codes, word, _, _ = b.random_pages("e2m1")
+    _apart(b, b.gen, 0, base, 20, word)
+    val = k4.values(codes, word, "e2m1").transpose(3, 4)
+    q = (b.rows(1, b.T, H * G, D).float() * 2.0 ** up).to(torch.bfloat16)
+    scale = D ** -0.5
+    got = _attend(td, b, codes, word, "e2m1", q, scale)
+    want = ck.attend(b, val[:, 0], val[:, 1], q)
+    assert float(want[3].max()) > 2.0 ** -6             # (the scores differ)
+    few = max(lens) * G <= 48
+    tol, tol_lse = k4.bounds(want, q, word, "e2m1", scale, few, max(s + t for s, t in zip(starts, lens)))
+    err = (got[0].double() - want[0]).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float((err / tol).max()))
+    assert bool(((got[1].double() - want[1]).abs() <= tol_lse).all())
+
+
+@pytest.mark.parametrize("name", [n for n in KINDS if n not in ("token", "few")])
+def test_quarters_of_v_as_far_apart_as_they_count(td, name):
+    """Chunks of more query rows: quarters up to 2^126 apart have their values; in an unfolded copy one of
+    2^-127 of its row's largest counts as 0."""
+    starts, lens, H, G, D, P = KINDS[name]
+    b = k4.Batch(starts, lens, H, D, P, seed=35)
+    codes, word, _, _ = b.random_pages("e2m1")
+    _apart(b, b.gen, 1, 235, 126, word)
+    q = b.rows(1, b.T, H * G, D)
+    scale = D ** -0.5
+    val = k4.values(codes, word, "e2m1").transpose(3, 4)
+    got = _attend(td, b, codes, word, "e2m1", q, scale)
+    want = ck.attend(b, val[:, 0], val[:, 1], q)
+    tol = k4.bounds(want, q, word, "e2m1", scale, False, 0)[0] - 1e-30 + 2.0 ** -132
+    err = (got[0].double() - want[0]).abs()
+    assert bool((err <= tol).all()), (float((err - tol).max()), float((err / tol).max()))
+    if not name.startswith("unfolded"):
+        return
+    word[:, 1] = k4.words(torch.tensor([235, 108, 235, 107], device="cuda").expand(b.shape((4,))[:1] +
+                                                                               b.shape((4,))[2:]), "e2m1")
+    out = _attend(td, b, codes, word, "e2m1", q, scale)[0].unflatten(-1, (4, -1))
+    assert bool((out[..., 1::2, :] == 0).all()) and bool((out[..., 0::2, :] != 0).any())
