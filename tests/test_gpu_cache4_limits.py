@@ -177,6 +177,63 @@ def test_elements_of_a_query_far_below_its_largest(td, fmt):
             assert bool(((ratio >= low) & (ratio <= high)).all()), ratio.tolist()
 
 
+SUMS = {
+    # name: (starts, lens, H, G, D, P, decode)
+    "tokens": ([5000, 1, 700], [1, 1, 1], 2, 7, 128, 16, True),
+    "tokens_d64": ([3000, 64, 127, 128], [1] * 4, 4, 3, 64, 24, True),
+    "one_long_token": ([12000], [1], 8, 8, 128, 16, True),
+    "drafts": ([4000, 300], [2, 3], 2, 7, 128, 16, False),
+    "drafts_d64": ([4000, 300], [5, 2], 2, 8, 64, 5, False),
+    "converted": ([3000, 90], [20, 30], 2, 7, 128, 16, False),
+    "converted_d64": ([2000], [70], 3, 7, 64, 16, False),
+    "unfolded": ([900, 30], [150, 90], 1, 7, 128, 16, False),
+    "unfolded_d64": ([2000, 500], [520, 600], 8, 2, 64, 24, False),
+    "unfolded_256": ([500, 0], [600, 700], 8, 4, 128, 16, False),
+}
+
+
+@pytest.mark.parametrize("fmt", k4.FORMATS)
+@pytest.mark.parametrize("name", list(SUMS))
+def test_sums_of_thousands_of_positions(td, name, fmt):
+    """Weights and scales that are powers of two, which no way of the kernels rounds: 2^0 to 2^3 by one
+    element of K (a query head has one dim of its own, and the softmax scale is ln 2, 2^-24 off at
+    most), V's scales 2^-1 to 2^1. A product of weight, scale and code is a multiple of 2^-2 up to
+    15 * 2^4 (a weight can be 2^-16 of that where the reference lags: the factor is common), and the sums
+    of 12001 of them stay under 2^24 such steps, so float32 adds them exactly, cut or rounded. What is
+    left: the exponential's 2^-21 of a weight with its exponent's 3 * 2^-23, the parts' and the last
+    scalings' few 2^-24, under 2^-18 of sum w |v| in all; and the output's rounding, 2^-8 of it. An
+    output is near 4 / sqrt(C), far above the former."""
+    starts, lens, H, G, D, P, decode = SUMS[name]
+    b = k4.Batch(starts, lens, H, D, P, seed=32)
+    codes, _, _, _ = b.random_pages(fmt)
+    code = k4.unpack(codes)
+    dims = torch.arange(D, device="cuda") < G
+    n = torch.randint(0, 4, code[:, 0].shape, generator=b.gen, device="cuda").to(torch.uint8)
+    if fmt == "int4":
+        zero = torch.randint(0, 12, b.shape(), generator=b.gen, device="cuda")
+        zero[:, 1] = torch.randint(0, 16, zero[:, 1].shape, generator=b.gen, device="cuda")
+        power = torch.randint(-1, 2, b.shape(), generator=b.gen, device="cuda")
+        power[:, 0] = 0
+        word = k4.words(2.0 ** power.float(), fmt, zero)
+        code[:, 0] = torch.where(dims, n + zero[:, 0, ..., None].to(torch.uint8), code[:, 0])
+    else:
+        power = torch.randint(126, 129, b.shape((4,)), generator=b.gen, device="cuda")
+        power[:, 0] = 128                              # (a code n is n / 2 up to 2, and 3 is 1.5)
+        word = k4.words(power, fmt)
+        code[:, 0] = torch.where(dims, n, code[:, 0])
+    codes = k4.pack(code)
+    val = k4.values(codes, word, fmt).transpose(3, 4)
+    q = torch.zeros((1, b.T, H, G, D), device="cuda")
+    i = torch.arange(G, device="cuda")
+    q[:, :, :, i, i] = 1.0
+    q = q.flatten(2, 3).to(torch.bfloat16)
+    out, z = _attend(td, b, codes, word, fmt, q, math.log(2.0), decode)
+    want, lse, mag, _ = ck.attend(b, val[:, 0], val[:, 1], q, scale=math.log(2.0))
+    err, tol = (out.double() - want).abs(), want.abs() * 2.0 ** -8 + mag * 2.0 ** -18
+    assert bool((err <= tol).all()), float((err / tol).max())
+    assert float((z.double() - lse).abs().max()) <= 2.0 ** -17 + 2.0 ** -23 * float(lse.abs().max())
+
+
 KINDS = {
     # name: (starts, lens, H, G, D, P)
     "token": ([700], [1], 1, 3, 128, 16),
