@@ -576,16 +576,22 @@ td_status td_dequantise_slots(td_ctx* ctx, const int32_t* slots, int32_t n_slots
 /* td_chunk_attention over 4-bit pages. A NaN scale that a token sees, K's or V's, makes its row
  * NaN (E2M1: b = 255 in any of the row's four bytes); one that is infinite has no defined value.
  * The scores have to stay within float32, 2^8 times the sums of V too, elements of q below 2^110 and K's
- * scales below 2^112. Chunks of up to 48 query rows (len * n_q_heads / H) go through f16. The queries,
- * each row under a power of two of its own: elements keep their 8 bits down to 2^-19 of the row's
- * largest (E2M1 2^-23), fewer below, and may be 0 from 2^-27 of it down (2^-31). The weights times V's
- * scales: rounded by 2^-11 at most down to 2^-20 of the largest scale in their part of the context (a
- * weight of 1 being that of the largest score), 0 under 2^-31 of it. E2M1: a byte b = 0 counts as a
- * scale of 0, and so does a quarter of V whose scale is 2^-27 of the row's largest or less. Longer
- * chunks (and shorter ones that a call takes with them) are computed as td_chunk_attention_q8's, those
- * of up to 512 query rows with the queries as f16; E2M1: a quarter of K whose scale is 2^-36 of the row's
- * largest or less then counts with fewer bits, or as 0; in those of more
- * rows only one of 2^-127 of it or less counts as 0, K's or V's. */
+ * scales below 2^112.
+ * Chunks of up to 48 query rows (len * n_q_heads / H) go through f16, in a call that has no longer
+ * ones. The queries, each row under a power of two of its own: elements keep their 8 bits down to
+ * 2^-19 of the row's largest (E2M1 2^-23), fewer below, and may be 0 from 2^-27 of it down (2^-31).
+ * The weights times V's scales: rounded by 2^-11 at most down to 2^-20 of the largest scale in their
+ * part of the context (a weight of 1 being that of the largest score), 0 under 2^-31 of it. INT4: the
+ * products are those of the codes, whose zero points come off the float32 sums, so that these are off
+ * relative to 15 scales where a value may be less. E2M1: a byte b = 0 counts as a scale of 0, and so does
+ * a quarter of V whose scale is 2^-27 of the row's largest or less.
+ * Longer chunks are computed as td_chunk_attention_q8's (weights as bf16, 2^-8), those of up to 512
+ * query rows with the queries as f16; E2M1: a quarter of K whose scale is 2^-36 of the row's largest or
+ * less then counts with fewer bits, or as 0; in those of more rows only one of 2^-127 of it or less
+ * counts as 0, K's or V's.
+ * In a call of shorter and longer chunks the shorter ones may be computed as the longer ones are,
+ * where that spares a launch: it depends on the call's sizes, not on any value. Chunks of up to 48
+ * query rows that are to keep the finer weights go in a call of their own. */
 td_status td_chunk_attention_q4(td_ctx* ctx, const td_chunks* chunks, const td_paged4* cache,
                                 int32_t layer_begin, int32_t layer_end, const void* q,
                                 int32_t n_q_heads, float scale, int32_t window, int32_t n_sink,
