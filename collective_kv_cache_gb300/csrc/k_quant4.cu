@@ -15,8 +15,8 @@
 //
 // Measured on one GB300 at D = 128: 51200 tokens of 8 layers and 8 heads read back in 314 us from
 // either (6.8 TB/s, the rate of a copy; one vector a lane 318 from int4, 330 from e2m1). 7070 tokens of
-// 28 layers and 4 heads written and read back in 160 us as e2m1 (5.7 TB/s) and in 175 as int4, whose
-// write takes 100 of them, bound by its instructions (issue slots busy in three cycles of four). A
+// 28 layers and 4 heads written and read back in 157 us as e2m1 (5.9 TB/s) and in 172 as int4, whose
+// write takes 99 of them, bound by its instructions (issue slots busy in three cycles of four). A
 // token of ten agents: 5 us in a graph, the launches.
 #include "td_cache4.cuh"
 
@@ -25,7 +25,7 @@ namespace td {
 namespace {
 
 // Threads of a CTA; int4's rows have half the lanes of e2m1's in the write (256: 179 us for the
-// prompts below written and read, 175 so).
+// prompts below written and read, 173 so).
 TD_HD constexpr int slot_threads(int kind, bool write) { return write && kind == kCacheInt4 ? 128 : 256; }
 constexpr uint32_t kScaleMin = 27u << 23;        // 2^-100
 

@@ -142,8 +142,10 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
 // positions 26 and 28, 24 and 27), 56 rows 117 and 218. Up to 16 rows the tensor-core kernel's
 // tile of 128 is mostly empty. Over 4-bit pages the streaming kernel is bound by its instructions
 // and the other by converting the codes, which more rows share: 28 rows on 5000 positions of 32
-// agents take 59 us streamed and 92 on the tensor-core kernel (int4, 4 kv heads, D = 128), 56 rows
-// 109 and 92.
+// agents take 57 us streamed and 91 on the tensor-core kernel (int4, 4 kv heads, D = 128; e2m1 61 and
+// 96), 48 rows 79 and 91 (84 and 96), 56 rows 100 and 91 (107 and 96); at D = 64 38 and 70 (41 and 69), 53
+// and 70 (56 and 71), 67 and 70 (72 and 71). On 1000 positions of 8 agents 48 rows 13.2 and 16.3 (13.3 and
+// 15.3; 10.0 and 13.9, 10.2 and 12.9), 56 rows 14.1 and 16.8 (14.4 and 15.8; 11.0 and 14.3, 11.3 and 13.3).
 constexpr int kFewRows = 16;
 constexpr int kFewRows4 = 48;
 
@@ -428,9 +430,12 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
   int64_t most = 0;
   for (int x = 0; x < list.n; ++x)
     most = std::max<int64_t>(most, static_cast<int64_t>(list.row[x + 1] - list.row[x]) * a->G);
-  // 4-bit pages: where few units see little, tiles of 128 rows too, twice the units (8 sequences of 252
-  // rows on 1000 positions 27.4 us in tiles of 256 and 23.8 so, 3 of 6000 on 2000, unfolded, 30 and
-  // 20.1; on long contexts the conversion is the bound, and is made twice: 16 of 252 on 12000 140 and 200)
+  // 4-bit pages: where few units see little, tiles of 128 rows too, twice the units. On long contexts
+  // the conversion is the bound, and is made twice: 8 sequences of 252 rows (int4, D = 128, in graphs) on
+  // 500 positions 18.5 us in tiles of 256 and 16.0 in tiles of 128, on 1000 27.6 and 23.8, on 2000 35.7 and
+  // 39.3, on 2400, past the limit, 37.3 and 42.6, on 6000 55 and 70; e2m1 and D = 64 cross at the same
+  // place. Unfolded, 2 of 1050 rows: on 1000 23.5 and 18.0, on 5000 44 and 37, past the limit on 5800 48
+  // and 40, on 9000 63 and 53.
   bool small = most <= 128;
   if (a->word && !small) {
     int64_t n = 0, steps = 0;
@@ -467,8 +472,10 @@ int64_t plan_tc(const td_ctx* c, const ChunkList& list, ChunkArgs* a, ChunkUnits
 // launch of its own. Unfolded (order[2]) are also the others whose copies are small; the tensor-core
 // kernel (order[1]) also takes streamed ones (order[0]) of few KV tiles, where all units run at once.
 // 24 chunks of 7 to 700 rows on 2000 to 2500 positions 102 us in three kinds, 76 joined; 8 of 7 to
-// 840 on 500 to 1500 41 and 28; 46 of 42 and 49 on 20 to 110 14.3 and 7.4. Joined all the same, 16 of
-// 7 to 140 on 4000 to 5000 would take 63 instead of 60.
+// 840 on 500 to 1500 41 and 28; 46 of 42 and 49 on 20 to 110 14.3 and 7.4. The streamed ones' limit: 16 of 7
+// to 140 rows (int4, D = 128, in graphs) on 500 positions take 17 us joined and 33 apart, on 1000 23 and
+// 35, on 2000, past it, 39 and 44, on 3000 53 and 50, on 4000 65 and 60 (e2m1 36 and 42, 50 and 48, 64 and
+// 58; D = 64 31 and 37, 44 and 42, 55 and 48).
 void join_orders(const td_ctx* c, const td_chunks* ch, const ChunkArgs& a, int64_t longest,
                  int64_t most_tiles, std::vector<int32_t>* order) {
   auto move = [&](int from, int to) {
