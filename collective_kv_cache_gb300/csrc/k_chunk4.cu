@@ -10,8 +10,11 @@
 //          bits higher 16 u 2^-24: a mask makes two operands of a word, without a conversion (a
 //          shift by 8 brings the other half of the codes there). The queries' elements that meet the
 //          higher ones are a sixteenth, the outputs of such dims are divided by 16. The zero point z
-//          comes off the sums, sum q (u - z) = sum q u - z sum q and sum p (u - z) = sum p u - sum p z,
-//          by one product more each: z is such an operand too.
+//          comes off the sums: sum q (u - z) = sum q u - z sum q in float32, sum p (u - z) = sum p u -
+//          sum p z by one product more, where z is such an operand too. (The tensor cores cut addends
+//          some 24 bits below the largest, a subnormal's counted as 2^-14: bits that q's elements, of 8,
+//          leave free and their sum does not. With z times the sum a product too, of three f16 parts, the
+//          log-sum-exp of a few positions was 1e-5 to 3e-5 off; 2e-6 to 3e-6 so, and the call 2% faster.)
 //   e2m1   two codes a conversion instruction. K's quarters are products of their own, each under its
 //          power of two; V's elements take that of their quarter relative to the row's largest, which
 //          goes on the weight.
@@ -251,7 +254,7 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
   [[maybe_unused]] uint2 qf[kKeep ? KCH : 1];
   auto query = [&](int nb, int kc) { return kKeep ? qf[kKeep ? kc : 0] : s_q[(nb * KCH + kc) * 32]; };
   float row_scale[NB][2];       // scale * log2(e) under the row's power of two
-  [[maybe_unused]] uint32_t q_sum[NB];          // int4: less the row's sum, in three f16
+  [[maybe_unused]] float q_sum[NB][2];          // int4: less the row's sum, 2^-24 of it
 #pragma unroll
   for (int nb = 0; nb < NB; ++nb) {
 #pragma unroll
@@ -320,18 +323,15 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
       }
     }
     if constexpr (kInt4) {
-      // (at most 2^14) minus the sum as an operand: dims 0 and 1 the first two parts, 2 the third
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
       sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-      const float s1 = f16_lo(pack_f16(-sum, 0.0f)), s2 = -sum - s1;
-      const float s3 = s2 - f16_lo(pack_f16(s2, 0.0f));
-      q_sum[nb] = tig == 0 ? pack_f16(s1, s2) : (tig == 1 ? pack_f16(s3, 0.0f) : 0u);
     }
 #pragma unroll
     for (int e = 0; e < 2; ++e) {               // (row c's is in the lanes 4 c .. 4 c + 3)
       const float inv = __shfl_sync(0xFFFFFFFFu, inverse, (2 * tig + e) * 4);
       // (int4's products come out 2^24 too small)
       row_scale[nb][e] = inv * 0x1p8f * A.scale_log2 * (kInt4 ? 0x1p24f : 1.0f);
+      if constexpr (kInt4) q_sum[nb][e] = __shfl_sync(0xFFFFFFFFu, sum, (2 * tig + e) * 4) * -0x1p-24f;
     }
   }
 
@@ -430,10 +430,9 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
     float s[2][NB][4];
     if constexpr (kInt4) {
       uint32_t kr[2][2][D / 32];                // the lane's piece of rows mix, mix + 8
-      float ks[2][2];
+      float ks[2][2], kz[2][2];                 // scales and zero points
 #pragma unroll
-      for (int sub = 0; sub < 2; ++sub) {
-        uint32_t kz[4] = {0u, 0u, 0u, 0u};      // the zero points, twice
+      for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           const int at = sub * 16 + mix + 8 * i;
@@ -451,11 +450,8 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
           }
           const uint32_t wd = words[at];
           ks[sub][i] = __uint_as_float(wd & 0xFFFF0000u);
-          kz[i] = __byte_perm(wd, 0u, 0x1010);
+          kz[sub][i] = __uint_as_float((wd & 0xFFFFu) | 0x4B000000u) - 0x1p23f;
         }
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) mma_f16_new(s[sub][nb], kz, q_sum[nb], 0u);
-      }
       // (the chains of products of both halves of the step side by side)
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
@@ -476,7 +472,10 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
           for (int nb = 0; nb < NB; ++nb) {
             const uint2 b = query(nb, 2 * c + k);
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) mma_f16(s[sub][nb], a[sub][k], b.x, b.y);
+            for (int sub = 0; sub < 2; ++sub) {
+              if (c == 0 && k == 0) mma_f16_new(s[sub][nb], a[sub][k], b.x, b.y);
+              else mma_f16(s[sub][nb], a[sub][k], b.x, b.y);
+            }
           }
       }
 #pragma unroll
@@ -486,8 +485,10 @@ __device__ __forceinline__ void attend(const ChunkArgs& A, const volatile Place&
 #pragma unroll
           for (int i = 0; i < 4; i += 2) {
             // (the query row's factor, then K's scale: the two multiplied first could pass float32)
-            const float2 x = mul2(make_float2(s[sub][nb][i], s[sub][nb][i + 1]),
-                                  make_float2(row_scale[nb][0], row_scale[nb][1]));
+            const float z = kz[sub][i >> 1];
+            const float2 u = fma2(make_float2(z, z), make_float2(q_sum[nb][0], q_sum[nb][1]),
+                                  make_float2(s[sub][nb][i], s[sub][nb][i + 1]));
+            const float2 x = mul2(u, make_float2(row_scale[nb][0], row_scale[nb][1]));
             const float2 y = fma2(x, make_float2(ks[sub][i >> 1], ks[sub][i >> 1]),
                                   make_float2(m_neg[nb][0], m_neg[nb][1]));
             s[sub][nb][i] = y.x;

@@ -327,3 +327,29 @@ def test_quarters_of_v_as_far_apart_as_they_count(td, name):
                                                                                b.shape((4,))[2:]), "e2m1")
     out = _attend(td, b, codes, word, "e2m1", q, scale)[0].unflatten(-1, (4, -1))
     assert bool((out[..., 1::2, :] == 0).all()) and bool((out[..., 0::2, :] != 0).any())
+
+
+@pytest.mark.parametrize("decode", [False, True])
+@pytest.mark.parametrize("D,G", [(128, 7), (64, 16)])
+def test_scores_over_int4_pages_are_float32(td, D, G, decode):
+    """Requests of one position, whose log-sum-exp is the score. Elements of the queries have 8 bits and
+    lie at most 2^5 below the row's largest, so that products with codes of 0 to 15 are multiples of 2^-12
+    of the largest's power of two and their sums stay under 2^24 such steps: t = sum q u and sum q are
+    exact in float32. (q, q and K's zero point: t - z sum q is then rounded once, multiplied three times by
+    scales, one of them rounded itself, and by ln 2: 6 times 2^-24, under 2^-21 of the score.)"""
+    n, H = 40, 2
+    b = k4.Batch([0] * n, [1] * n, H, D, 16, seed=36)
+    codes, _, _, _ = b.random_pages("int4")
+    zero = torch.randint(0, 16, b.shape(), generator=b.gen, device="cuda")
+    power = torch.rand(b.shape(), generator=b.gen, device="cuda") + 0.5
+    word = k4.words(power, "int4", zero)
+    val = k4.values(codes, word, "int4").transpose(3, 4)
+    shape = (1, n, H * G, D)
+    rand = lambda lo, hi: torch.randint(lo, hi, shape, generator=b.gen, device="cuda")  # noqa: E731
+    q = rand(128, 256).float() * 2.0 ** -(7 + rand(0, 6)).float() * (2 * rand(0, 2) - 1)
+    q[..., 5] = 1.0
+    q = q.to(torch.bfloat16)
+    _, z = _attend(td, b, codes, word, "int4", q, D ** -0.5, decode)
+    want = ck.attend(b, val[:, 0], val[:, 1], q)[1]
+    err = (z.double() - want).abs()
+    assert bool((err <= want.abs() * 2.0 ** -21 + 1e-30).all()), float((err / want.abs()).max())
