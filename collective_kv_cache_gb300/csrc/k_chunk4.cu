@@ -35,7 +35,7 @@
 //
 // Measured on one GB300, 4 kv heads of 7 query heads, D = 128: one token of 64 requests on 8192 to 24576
 // positions 105 us over int4 pages (5.5 TB/s; the copies alone take 95), 115 over e2m1 (5.0); at D = 64
-// 76 and 81. Two tokens each on 4096 to 12288: 79 and 85 us, tensor pipe 39% and issue slots 45% busy: 12
+// 76 and 81. Two tokens each on 4096 to 12288: 78 and 85 us, tensor pipe 38% and issue slots 46% busy: 12
 // warps an SM wait for their own products and shared memory in turn. Ten requests on 3060 to 6560 15.5
 // us, of which 14.3 remain in a graph.
 #include "td_cache4.cuh"

@@ -142,10 +142,10 @@ td_status run_quant(td_ctx* c, const td_chunks* ch, const td_paged8* cache, cons
 // positions 26 and 28, 24 and 27), 56 rows 117 and 218. Up to 16 rows the tensor-core kernel's
 // tile of 128 is mostly empty. Over 4-bit pages the streaming kernel is bound by its instructions
 // and the other by converting the codes, which more rows share: 28 rows on 5000 positions of 32
-// agents take 57 us streamed and 91 on the tensor-core kernel (int4, 4 kv heads, D = 128; e2m1 61 and
-// 96), 48 rows 79 and 91 (84 and 96), 56 rows 100 and 91 (107 and 96); at D = 64 38 and 70 (41 and 69), 53
-// and 70 (56 and 71), 67 and 70 (72 and 71). On 1000 positions of 8 agents 48 rows 13.2 and 16.3 (13.3 and
-// 15.3; 10.0 and 13.9, 10.2 and 12.9), 56 rows 14.1 and 16.8 (14.4 and 15.8; 11.0 and 14.3, 11.3 and 13.3).
+// agents take 56 us streamed and 91 on the tensor-core kernel (int4, 4 kv heads, D = 128; e2m1 61 and
+// 96), 48 rows 77 and 91 (84 and 96), 56 rows 98 and 91 (107 and 96); at D = 64 38 and 70 (41 and 69), 52
+// and 70 (56 and 71), 67 and 70 (72 and 71). On 1000 positions of 8 agents 48 rows 13.1 and 16.3 (13.3 and
+// 15.3; 10.0 and 13.9, 10.2 and 12.9), 56 rows 13.9 and 16.8 (14.4 and 15.8; 10.9 and 14.4, 11.3 and 13.3).
 constexpr int kFewRows = 16;
 constexpr int kFewRows4 = 48;
 
